@@ -596,6 +596,131 @@ PQE_API int pqe_expert_quant_error(const void *x_bf16, int n, const uint8_t *pag
 PQE_API int64_t pqe_module_batch_size(int E, int k, int H, int I, double hbm_gbs, double fp8_tflops, int granule);
 
 /* ------------------------------------------------------------------------
+ * KV cache -- the attention half of a decoder layer beside the expert layer:
+ * K and V rows are quantised to MXFP4 as they enter a paged cache, and
+ * attention reads them there. (No counterpart in the cited pages; formats and
+ * conventions are those of the expert pages above.)
+ *
+ * A cache is n_pages pages of page_size tokens each, page p at pages + p *
+ * page_stride. A page holds, for each of its n_kv heads in order, page_size /
+ * 16 blocks of 16 tokens, 17 * d bytes each (4.25 bits per value), so head h's
+ * block i of a page starts at (h * page_size / 16 + i) * 17 * d. A block:
+ *   K codes  at 0       a row of d/2 bytes per token: byte t*(d/8) + 4*G + i
+ *                       holds elements 32*G + 8*t + 2*i and the next
+ *                       (t < 4, i < 4, G < d/32)
+ *   V codes  at 8*d     byte (G/2)*512 + (4*g + t)*16 + 4*j + 2*(G%2) + i holds
+ *                       elements 32*G + 4*g + 2*i and the next of token
+ *                       2*t + j%2 + 8*(j/2)  (g < 8, t < 4, j < 4, i < 2)
+ *   K scales at 16*d    E8M0 bytes [token][G]
+ *   V scales at 16*d + d/2   E8M0 bytes [t][G][j], token as for the V codes
+ * where a byte's low nibble is the even element, and value = e2m1(code) *
+ * 2^(scale - 127). The order inside a block is that in which the attention's
+ * tensor-core fragments take it. Every byte belongs to one token, so tokens
+ * may be written in any order and by different calls. A scale byte of 255
+ * marks a block of 32 values that held a NaN or an infinity (its codes are
+ * 0); it reads as NaN.
+ * Limits: d 64 or 128; page_size a power of two, 16 to 1024; 1 <= n_kv <= 256;
+ * n_pages >= 1; pages 16-byte aligned, page_stride a multiple of 16 and at
+ * least pqe_kv_page_bytes(page_size, n_kv, d).
+ * ------------------------------------------------------------------------ */
+typedef struct pqe_kv_cache {
+    void *pages;        /* device: n_pages * page_stride bytes */
+    size_t page_stride; /* bytes from one page to the next */
+    int32_t n_pages, page_size, n_kv, d;
+} pqe_kv_cache;
+
+/* Bytes of one page; 0 for arguments outside the limits. */
+PQE_API size_t pqe_kv_page_bytes(int page_size, int n_kv, int d);
+
+/* kv_cache_write -- quantise n tokens' K and V rows into the cache. Per block
+ * of 32 along d: X = 2^(floor(log2 amax) - 2) as E8M0 (byte 0 for an all-zero
+ * block, and where the exponent would be below it), element RNE_e2m1(v / X)
+ * saturating at 6 (OCP MX v1.0), as pqe_quantize_mxfp4_rows; 255 and zero codes
+ * for a block with a NaN or an infinity.
+ * k, v     device bf16: token i's n_kv heads of d values start at i * k_stride
+ *          (v_stride) elements, e.g. inside the rows of a fused q|k|v
+ *          projection; 16-byte aligned, strides multiples of 8 and at least
+ *          n_kv * d.
+ * slots    device int64 [n]: token i goes to place slots[i] % page_size of page
+ *          slots[i] / page_size; a negative slot skips the token; one at or
+ *          beyond n_pages * page_size is skipped and sets PQE_STATUS_BAD_PAGE.
+ *          Two tokens of one call with the same slot: either one's bytes, or a
+ *          mixture of both.
+ * n >= 0; n == 0 is a no-op. */
+PQE_API int kv_cache_write(const pqe_kv_cache *cache, const void *k, const void *v, int64_t k_stride,
+                           int64_t v_stride, const int64_t *slots, int n, int32_t *status, void *stream);
+
+/* kv_cache_read -- the values of n tokens, exact in bf16 (a value below bf16's
+ * range, which only a scale byte under 2 can give, is rounded). slots as for
+ * kv_cache_write; a skipped token's rows are zero. k, v: device bf16
+ * [n, n_kv, d] out, 16-byte aligned; either may be NULL. */
+PQE_API int kv_cache_read(const pqe_kv_cache *cache, const int64_t *slots, int n, void *k, void *v, int32_t *status,
+                          void *stream);
+
+/* kv_paged_attention -- grouped-query attention of B sequences' newest tokens
+ * over their cached K and V. Sequence b has m = q_offsets[b+1] - q_offsets[b]
+ * query tokens, rows q_offsets[b].. of q, and L = kv_lens[b] cached tokens, its
+ * queries' own among them (written before); token j lies at place j %
+ * page_size of page block_table[b][j / page_size]. Query i stands at position
+ * p = L - m + i; query head h reads kv head h / (n_q / n_kv):
+ *   s_j = scale * q . k_j over the j it sees;  out = sum_j softmax(s)_j v_j.
+ *   causal:  j <= p, and j > p - window when window > 0;
+ *   else:    every j < L (window must then be 0).
+ * A query that sees nothing gives zeros (lse -infinity). One whose q holds a
+ * NaN or an infinity gives NaN. What is masked never reaches an output,
+ * whatever it holds. Statistics and sums are fp32; q and the probabilities
+ * enter the tensor cores in f16, q scaled per row by a power of two (exact
+ * down to 2^-22 of the row's largest value) and the probabilities scaled by
+ * one too: those under 2^-33 of the row's largest count as zero, as do V
+ * blocks whose scale is below 2^-21 of the largest they are summed with.
+ * q        device bf16, token rows q_stride elements apart, [n_q][d] each;
+ *          16-byte aligned, q_stride a multiple of 8 and at least n_q * d
+ * q_offsets device int32 [B + 1], ascending from 0 or more, at most total_q
+ * kv_lens  device int32 [B]; block_table device int32 [B, max_pages]
+ * max_q    the largest m (it chooses the kernel; the lengths themselves are
+ *          read on the device, so a captured call follows them)
+ * out      device bf16 [total_q, n_q, d], 16-byte aligned; rows of no
+ *          sequence are left as they are
+ * lse      device fp32 [total_q, n_q] or NULL: ln sum_j exp(s_j)
+ * ws       device scratch of at least kv_paged_attention_workspace_size bytes,
+ *          256-byte aligned; the call leaves nothing in it for the next, and
+ *          calls that may overlap on the GPU need one each
+ * status   device int32: PQE_STATUS_BAD_PAGE for a table entry outside the
+ *          cache (its tokens count as masked) or a length beyond the table
+ *          (cut); PQE_STATUS_TIMEOUT as elsewhere
+ * Limits: n_q a multiple of n_kv, n_q <= 1024; B >= 0, total_q >= 0 (either 0:
+ * a no-op); max_pages * page_size < 2^31; scale finite. */
+PQE_API size_t kv_paged_attention_workspace_size(int B, int total_q, int max_q, int n_q, int n_kv, int d);
+PQE_API int kv_paged_attention(const pqe_kv_cache *cache, const void *q, int64_t q_stride, const int32_t *q_offsets,
+                               const int32_t *kv_lens, const int32_t *block_table, int max_pages, int B, int total_q,
+                               int max_q, int n_q, float scale, int causal, int window, void *out, float *lse,
+                               void *ws, size_t ws_bytes, int32_t *status, void *stream);
+
+/* ------------------------------------------------------------------------
+ * add_rms_norm -- residual addition, root-mean-square norm, and the result in
+ * 8 bits, as the layers before and after the expert layer need it. Per row of
+ * H values, in fp32:
+ *   h = x + residual (x alone when residual is NULL);  sum_out = bf16(h)
+ *   y = h * (1 / sqrt(mean(h^2) + eps)) * weight;      y_out = bf16(y)
+ *   PQE_Q8_ROW: s = max|y| / 448 (1 for an all-zero row) as fp32 [T],
+ *               code = RNE_e4m3(y / s), as pqe_quantize_fp8_rows
+ *   PQE_Q8_MX:  per 32 values X = 2^(floor(log2 max|y|) - 8) as E8M0 [T, H/32]
+ *               (byte 0 as for kv_cache_write), code = RNE_e4m3(y / X)
+ * saturating at 448. y is quantised unrounded. A NaN in a row (or block of 32)
+ * of y gives NaN codes and a NaN scale (255).
+ * x, residual device bf16, rows x_stride (r_stride) elements apart; weight
+ * device bf16 [H]; all 16-byte aligned, strides multiples of 8 and >= H.
+ * sum_out, y_out device bf16 [T, H] or NULL; sum_out may be residual or x
+ * itself (same rows and stride H). q device uint8 [T, H] E4M3 or NULL, with
+ * q_scale its scales. At least one of sum_out, y_out, q is given.
+ * H % 32 == 0, 32 <= H <= 16384; T >= 0; eps >= 0. */
+#define PQE_Q8_ROW 0
+#define PQE_Q8_MX 1
+PQE_API int add_rms_norm(const void *x, int64_t x_stride, const void *residual, int64_t r_stride, const void *weight,
+                         float eps, int T, int H, void *sum_out, void *y_out, uint8_t *q, void *q_scale, int q_fmt,
+                         void *stream);
+
+/* ------------------------------------------------------------------------
  * Layer runtime -- one MoE layer over its own slot pool, one call per step.
  * A step: moe_route -> moe_permute -> per-expert counts to the host (the one
  * host synchronisation of a step; the LRU state lives on the host) ->

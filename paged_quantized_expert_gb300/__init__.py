@@ -12,6 +12,7 @@ PyTorch is used for device memory and streams only.
 from __future__ import annotations
 
 import ctypes as C
+import math
 import os
 from typing import Optional
 
@@ -35,6 +36,8 @@ PQE_STATUS_TIMEOUT = 0x8
 
 PQE_FMT_FP8 = 0
 PQE_FMT_MXFP4 = 1
+PQE_Q8_ROW = 0
+PQE_Q8_MX = 1
 PQE_HUFF_LUT_BYTES = 16384
 
 LIB_PATH = _build.LIB
@@ -73,6 +76,11 @@ class pqe_layer_buffers_t(C.Structure):
 class pqe_pool(C.Structure):
     _fields_ = [("base", C.c_void_p), ("wb_base", C.c_void_p), ("slot_stride", C.c_size_t),
                 ("n_slots", C.c_int32), ("n_wb", C.c_int32), ("H", C.c_int32), ("I", C.c_int32)]
+
+
+class pqe_kv_cache(C.Structure):
+    _fields_ = [("pages", C.c_void_p), ("page_stride", C.c_size_t), ("n_pages", C.c_int32), ("page_size", C.c_int32),
+                ("n_kv", C.c_int32), ("d", C.c_int32)]
 
 
 _lib: Optional[C.CDLL] = None
@@ -133,6 +141,13 @@ _SIGS = {
     "pqe_layer_device_stats": (I32, [P, P, P, P, P, P]),
     "pqe_pack_fp8_page": (I32, [P, P, I32, I32, P, P]),
     "pqe_pack_mxfp4_page": (I32, [P, I32, I32, P, P]),
+    "pqe_kv_page_bytes": (SZ, [I32, I32, I32]),
+    "kv_cache_write": (I32, [C.POINTER(pqe_kv_cache), P, P, C.c_int64, C.c_int64, P, I32, P, P]),
+    "kv_cache_read": (I32, [C.POINTER(pqe_kv_cache), P, I32, P, P, P, P]),
+    "kv_paged_attention_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32]),
+    "kv_paged_attention": (I32, [C.POINTER(pqe_kv_cache), P, C.c_int64, P, P, P, I32, I32, I32, I32, I32, C.c_float,
+                                 I32, I32, P, P, P, SZ, P, P]),
+    "add_rms_norm": (I32, [P, C.c_int64, P, C.c_int64, P, C.c_float, I32, I32, P, P, P, P, I32, P]),
     "pqe_layer_scratch_bytes": (SZ, [P]),
     "pqe_layer_create": (P, [P, C.POINTER(pqe_pool), P, P, P, P, P, SZ]),
     "pqe_layer_destroy": (None, [P]),
@@ -311,6 +326,119 @@ def moe_paged_ffn(x, perm_src, offsets, page_table, expert_fmt, pool: pqe_pool, 
 def moe_combine(out_perm, inv, topk_w, T, k, H, y, stream=None):
     _check("moe_combine", lib().moe_combine(_ptr(out_perm), _ptr(inv), _ptr(topk_w), T, k, H, _ptr(y),
                                             _stream(stream)))
+
+
+# ---- attention over a 4-bit paged cache, residual norm ---------------------------
+
+def _rows(t: torch.Tensor, inner: tuple) -> tuple[int, int]:
+    """Pointer and row stride (elements) of a bf16 tensor [n, *inner] whose rows are contiguous and may lie apart."""
+    if t.dtype not in (torch.bfloat16, torch.int16) or t.shape[1:] != inner:
+        raise ValueError(f"expected bf16 rows of shape {tuple(inner)}, got {t.dtype} {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), math.prod(inner)
+    if not t[0].is_contiguous():
+        raise ValueError("each token's row must be contiguous")
+    return t.data_ptr(), t.stride(0)
+
+
+def _typed(t, dtype, name: str, n: int) -> int:
+    """Pointer of a contiguous tensor of this dtype with at least n elements."""
+    if t.dtype != dtype or t.numel() < n:
+        raise ValueError(f"{name}: expected at least {n} values of {dtype}, got {t.numel()} of {t.dtype}")
+    return _ptr(t)
+
+
+def pqe_kv_page_bytes(page_size: int, n_kv: int, d: int) -> int:
+    return lib().pqe_kv_page_bytes(page_size, n_kv, d)
+
+
+def make_kv_cache(pages: torch.Tensor, n_pages: int, page_size: int, n_kv: int, d: int) -> pqe_kv_cache:
+    """Describe a 4-bit paged KV cache (pqe.h, "KV cache") to the library; ``pages`` stays the caller's."""
+    nb = pqe_kv_page_bytes(page_size, n_kv, d)
+    if not nb:
+        raise PqeError("pqe_kv_page_bytes", PQE_ERR_INVALID_ARG)
+    if n_pages < 1 or _nbytes(pages) < n_pages * nb:
+        raise ValueError("cache tensor too small")
+    return pqe_kv_cache(_ptr(pages), nb, n_pages, page_size, n_kv, d)
+
+
+def alloc_kv_cache(n_pages: int, page_size: int, n_kv: int, d: int, device="cuda") -> tuple[torch.Tensor, pqe_kv_cache]:
+    """A cache of n_pages empty (zero) pages."""
+    nb = pqe_kv_page_bytes(page_size, n_kv, d)
+    if not nb:
+        raise PqeError("pqe_kv_page_bytes", PQE_ERR_INVALID_ARG)
+    t = torch.zeros(n_pages * nb, dtype=torch.uint8, device=device)
+    return t, make_kv_cache(t, n_pages, page_size, n_kv, d)
+
+
+def kv_cache_write(cache: pqe_kv_cache, k, v, slots, status, stream=None):
+    """Quantise rows k, v [n, n_kv, d] (bf16; rows may lie apart, as in a fused projection) into the cache at slots
+    (int64 [n]; negative: skip)."""
+    n = k.shape[0]
+    if v.shape[0] != n:
+        raise ValueError("k and v differ in their number of tokens")
+    if n == 0:
+        return
+    kp, ks = _rows(k, (cache.n_kv, cache.d))
+    vp, vs = _rows(v, (cache.n_kv, cache.d))
+    _check("kv_cache_write", lib().kv_cache_write(C.byref(cache), kp, vp, ks, vs, _typed(slots, torch.int64, "slots", n),
+                                                  n, _ptr(status), _stream(stream)))
+
+
+def kv_cache_read(cache: pqe_kv_cache, slots, k, v, status, stream=None):
+    """The cached values of slots (int64 [n]) as bf16 rows k, v [n, n_kv, d] (either may be None)."""
+    n = slots.numel()
+    if n == 0:
+        return
+    outs = [None if t is None else _typed(t, torch.bfloat16, "k/v", n * cache.n_kv * cache.d) for t in (k, v)]
+    _check("kv_cache_read", lib().kv_cache_read(C.byref(cache), _typed(slots, torch.int64, "slots", n), n, outs[0],
+                                                outs[1], _ptr(status), _stream(stream)))
+
+
+def kv_paged_attention_workspace_size(B: int, total_q: int, max_q: int, n_q: int, n_kv: int, d: int) -> int:
+    return lib().kv_paged_attention_workspace_size(B, total_q, max_q, n_q, n_kv, d)
+
+
+def kv_paged_attention(cache: pqe_kv_cache, q, q_offsets, kv_lens, block_table, max_q: int, scale: float, out, ws,
+                       status, causal: bool = True, window: int = 0, lse=None, stream=None):
+    """Attention of q [total_q, n_q, d] (bf16; rows may lie apart) over the cached tokens of each sequence
+    (q_offsets int32 [B+1], kv_lens int32 [B], block_table int32 [B, max_pages]) into out [total_q, n_q, d]."""
+    B = kv_lens.numel()
+    total_q, n_q, d = q.shape
+    if d != cache.d:
+        raise ValueError("q and the cache differ in head size")
+    if B == 0 or total_q == 0:
+        return
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_pages]")
+    qp, qs = _rows(q, (n_q, d))
+    _check("kv_paged_attention", lib().kv_paged_attention(
+        C.byref(cache), qp, qs, _typed(q_offsets, torch.int32, "q_offsets", B + 1),
+        _typed(kv_lens, torch.int32, "kv_lens", B), _typed(block_table, torch.int32, "block_table", 0),
+        block_table.shape[1], B, total_q, max_q, n_q, scale, int(causal), window,
+        _typed(out, torch.bfloat16, "out", total_q * n_q * d),
+        None if lse is None else _typed(lse, torch.float32, "lse", total_q * n_q), _ptr(ws), _nbytes(ws), _ptr(status),
+        _stream(stream)))
+
+
+def add_rms_norm(x, residual, weight, eps: float, sum_out, y, q=None, q_scale=None, q_fmt: int = PQE_Q8_ROW, stream=None):
+    """h = x + residual, y = RMSnorm(h) * weight; sum_out, y bf16 [T, H] and q E4M3 [T, H] with q_scale (fp32 [T], or
+    E8M0 bytes [T, H/32] with PQE_Q8_MX), each optional. x, residual: bf16 [T, H], rows may lie apart."""
+    T, H = x.shape
+    if T == 0:
+        return
+    xp, xs = _rows(x, (H,))
+    if residual is not None and residual.shape != x.shape:
+        raise ValueError("x and residual differ in shape")
+    rp, rs = (None, 0) if residual is None else _rows(residual, (H,))
+    outs = [None if t is None else _typed(t, torch.bfloat16, "sum_out/y", T * H) for t in (sum_out, y)]
+    if q is not None:
+        if q.element_size() != 1 or q.numel() < T * H:
+            raise ValueError("q must hold T * H bytes")
+        if q_scale is None or _nbytes(q_scale) < (4 * T if q_fmt == PQE_Q8_ROW else T * (H // 32)):
+            raise ValueError("q_scale is missing or too small")
+    _check("add_rms_norm", lib().add_rms_norm(xp, xs, rp, rs, _typed(weight, torch.bfloat16, "weight", H), eps, T, H,
+                                              outs[0], outs[1], _ptr(q), _ptr(q_scale), q_fmt, _stream(stream)))
 
 
 # ---- pager ---------------------------------------------------------------------
