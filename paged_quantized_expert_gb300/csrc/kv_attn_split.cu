@@ -1,0 +1,782 @@
+// kv_attn_split.cu -- attention over the 4-bit paged cache for few query rows
+// (single tokens, a few tokens at once), split along the cache.
+//
+// For one sequence and KV head the R = m * group query rows form the N side of
+// mma.sync m16n8k16 (f16 in, fp32 sums): S^T[token, row] = K . Q^T with 16
+// tokens as M, then O^T[d, row] = V^T . P^T with 16 channels as M, so 8 rows
+// fill a tile that 16-row forms would leave half empty. Per tile of 64 tokens:
+//   S[j, r]  = sum_G 2^(ks[j, G]) * (codes of block G . q)   K scales in fp32,
+//              after each 32-channel block's two MMAs: codes enter as they are
+//   p        = 2^(c_r S - m_r + 8), running maximum m_r, sum l_r
+//   T[d, r]  = sum_j code[j, d] * (p * 2^(vs[j, G] - top + 7)),  top the largest
+//              V scale of the tile: p and the factor stay inside f16
+//   O        = O * 2^(m_old - m_new) + T * 2^(top - 15)      fp32
+// P^T's fragments come from S^T's by movmatrix, with no trip through memory.
+//
+// The cache is read once. Work is (sequence, KV head, 8 * NT rows, tile); all of
+// it in one line is cut into equal shares, one per warp of the grid, whatever
+// the lengths are (they are read on the device). A warp fetches its tiles
+// with bulk copies into its own ring of shared memory, two ahead; it meets no
+// other warp until its share is done. A share's first and last piece may
+// belong to a (sequence, head, rows) that others share: the CTA's four warps
+// join theirs in shared memory, CTAs leave theirs in the workspace, and a
+// second kernel joins those in a fixed order.
+//
+// Bound by the cache's bytes when there are many (4.25 bits a value: 43 values a
+// clock and SM at the memory's rate, at about one instruction a value), by
+// latency when there are few.
+#include <math.h>
+
+#include "kv_attn.cuh"
+#include "tc_ptx.cuh"
+
+namespace pqe {
+namespace kv {
+namespace split {
+using namespace ptx;
+
+constexpr int WARPS = 4;
+constexpr int STAGES = 2;
+
+template <int D>
+constexpr int tile_bytes() {
+    return TILE / BLOCK * block_bytes(D);
+}
+// one partial result: O [rows][D], m [rows], l [rows], all fp32
+__host__ __device__ constexpr int part_floats(int d, int rows) { return rows * (d + 2); }
+
+template <int D, int NT>
+struct Smem {
+    alignas(16) uint8_t ring[WARPS][STAGES][tile_bytes<D>()];  // a warp's last partial takes its ring's place
+    alignas(8) uint64_t full[WARPS][STAGES];
+    int64_t scan[WARPS * 32];
+    int64_t start_off[WARPS];
+    int start_b[WARPS];
+    // pieces of (sequence, head, rows) that the warps did not finish alone: two each
+    int64_t seg_start[WARPS][2];
+    int from[WARPS][2], to[WARPS][2], len_t[WARPS][2], b[WARPS][2], seg[WARPS][2];
+    const float *ptr[WARPS][2];
+};
+
+// unit at which share i of n begins, of `total` units
+__device__ __forceinline__ int64_t share_start(int64_t i, int64_t n, int64_t total) { return i * total / n; }
+// the share that unit u falls into
+__device__ __forceinline__ int64_t share_of(int64_t u, int64_t n, int64_t total) { return ((u + 1) * n - 1) / total; }
+
+// a sequence's share of the line of work
+struct Seq {
+    int first, m, len, t0, T, nrc;
+};
+template <int NT>
+__device__ __forceinline__ Seq load_seq(const AttnArgs &a, int b, int group) {
+    Seq s;
+    sequence_of(a, b, s.first, s.m, s.len);
+    s.nrc = (s.m * group + 8 * NT - 1) / (8 * NT);
+    int lo, hi;
+    visible(a, 0, s.m, s.len, lo, hi);
+    s.t0 = min(lo, s.len) / TILE;
+    s.T = s.m > 0 ? (s.len + TILE - 1) / TILE - s.t0 : 0;
+    return s;
+}
+
+struct Cursor {
+    int b, seg, tile;  // seg = kv head * nrc + row chunk; tile counts from the sequence's t0
+    Seq s;
+};
+template <int NT>
+__device__ __forceinline__ void advance(const AttnArgs &a, Cursor &c, int group) {
+    if (++c.tile < c.s.T) return;
+    c.tile = 0;
+    if (++c.seg < a.c.n_kv * c.s.nrc) return;
+    c.seg = 0;
+    while (++c.b < a.B) {
+        c.s = load_seq<NT>(a, c.b, group);
+        if (c.s.T > 0) return;
+    }
+}
+
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+// Starts the copies of the cursor's tile into a stage; returns the bit mask of
+// its 16-token blocks that the stage will hold (a block of a bad page, or past
+// the end, is not there).
+template <int D>
+__device__ __forceinline__ uint32_t fetch(const AttnArgs &a, const Cursor &c, uint32_t dst, uint32_t bar, int lane) {
+    const int j0 = (c.s.t0 + c.tile) * TILE;
+    const int nblk = min(TILE / BLOCK, (c.s.len - j0 + BLOCK - 1) / BLOCK);
+    const int psh = min(a.c.page_shift - 4, 2), per = 1 << psh;  // blocks a copy can take: of one page
+    const int blk = lane << psh;
+    uint32_t bytes = 0, mask = 0;
+    const uint8_t *src = nullptr;
+    if (blk < nblk) {
+        const int j = j0 + blk * BLOCK;
+        const int page = a.block_table[(size_t)c.b * a.max_pages + (j >> a.c.page_shift)];
+        if (page >= 0 && page < a.c.n_pages) {
+            const int n = min(per, nblk - blk);
+            src = block_of<D>(a.c, page, j & ((1 << a.c.page_shift) - 1), c.seg / c.s.nrc);
+            bytes = n * block_bytes(D);
+            mask = ((1u << n) - 1) << blk;
+        } else {
+            atomicOr(a.status, PQE_STATUS_BAD_PAGE);
+        }
+    }
+    const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
+    mask = __reduce_or_sync(0xffffffffu, mask);
+    if (lane == 0) mbar_expect_tx(bar, total);
+    __syncwarp();
+    if (bytes) bulk_copy(dst + blk * block_bytes(D), src, bytes, bar);
+    return mask;
+}
+
+// row r of a (sequence, head, chunk): its place in q, out and lse
+__device__ __forceinline__ int64_t row_index(const AttnArgs &a, const Seq &s, int head, int group, int r) {
+    return (int64_t)(s.first + r / group) * a.n_q + head * group + r % group;
+}
+
+// f16 pair of V's block factors 2^(x - top + 7) from two E8M0 bytes in the halves of x; zero 21 and more below
+__device__ __forceinline__ uint32_t v_factors(uint32_t x, uint32_t least, uint32_t off) {
+    return __vmaxu2(x, least) * 1024u - off;
+}
+// the same where a byte may be 255 (NaN)
+__device__ __forceinline__ uint32_t v_factors_nan(uint32_t x, uint32_t least, uint32_t off) {
+    const uint32_t lo = x & 0xFFFFu, hi = x >> 16;
+    uint32_t f = v_factors((lo == 255 ? 0u : lo) | (hi == 255 ? 0u : hi << 16), least, off);
+    if (lo == 255) f = (f & 0xFFFF0000u) | 0x7E00u;
+    if (hi == 255) f = (f & 0xFFFFu) | 0x7E000000u;
+    return f;
+}
+// p * f where a masked row's p, 0, gives 0 whatever f is
+__device__ __forceinline__ uint32_t weigh_nan(uint32_t p, uint32_t f) {
+    uint32_t r = mul_f16x2(p, f);
+    if (!(p & 0x7FFFu)) r &= 0xFFFF0000u;
+    if (!(p & 0x7FFF0000u)) r &= 0xFFFFu;
+    return r;
+}
+
+// The rows of one (sequence, KV head, chunk) while its tiles pass.
+template <int D, int NT>
+struct Rows {
+    uint32_t q[NT][D / 32][4];  // B fragments: row 8 * nt + g, channels 32 * G + 8 * t ..
+    float c[NT][2];             // of rows 8 * nt + 2 * t, + 1: the factor from S to an exponent of two
+    int lo[NT][2], hi[NT][2];   // and the tokens they see
+    int min_lo, max_lo, min_hi, max_hi;
+    float m[NT][2], l[NT][2];   // l: this lane's tokens only
+    float o[D / 32][2][NT][4];  // O^T: block G, channels 4g + {0, 1} and 4g + {2, 3}
+};
+
+template <int D, int NT>
+__device__ __forceinline__ void begin_rows(const AttnArgs &a, const Cursor &c, int group, int lane, Rows<D, NT> &R) {
+    const int g = lane >> 2, t = lane & 3;
+    const int head = c.seg / c.s.nrc, r0 = (c.seg % c.s.nrc) * 8 * NT, n = c.s.m * group;
+    R.min_lo = R.min_hi = INT32_MAX;
+    R.max_lo = R.max_hi = 0;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = r0 + 8 * nt + g;
+        uint4 raw[D / 32];
+        uint32_t top = 0;
+        int lo = 0, hi = 0;
+        if (r < n) {
+            const uint16_t *row = a.q + (int64_t)(c.s.first + r / group) * a.q_stride + (head * group + r % group) * D;
+            visible(a, r / group, c.s.m, c.s.len, lo, hi);
+#pragma unroll
+            for (int G = 0; G < D / 32; ++G) raw[G] = *reinterpret_cast<const uint4 *>(row + 32 * G + 8 * t);
+            R.min_lo = min(R.min_lo, lo);
+            R.max_lo = max(R.max_lo, lo);
+            R.min_hi = min(R.min_hi, hi);
+            R.max_hi = max(R.max_hi, hi);
+        } else {
+#pragma unroll
+            for (int G = 0; G < D / 32; ++G) raw[G] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int G = 0; G < D / 32; ++G) {
+            const uint32_t w[4] = {raw[G].x, raw[G].y, raw[G].z, raw[G].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        float f, inv;
+        q_factor(top, f, inv);
+        inv = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : inv * a.scale;  // a row that is not finite gives NaN
+#pragma unroll
+        for (int G = 0; G < D / 32; ++G) {
+            const uint32_t w[4] = {raw[G].x, raw[G].y, raw[G].z, raw[G].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                R.q[nt][G][i] = pack_f16(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xFFFF0000u) * f);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int src = (2 * t + i) * 4;  // a lane that holds row 8 * nt + 2 * t + i
+            R.c[nt][i] = __shfl_sync(0xffffffffu, inv, src);
+            R.lo[nt][i] = __shfl_sync(0xffffffffu, lo, src);
+            R.hi[nt][i] = __shfl_sync(0xffffffffu, hi, src);
+            R.m[nt][i] = -INFINITY;
+            R.l[nt][i] = 0.f;
+        }
+    }
+    R.min_lo = __reduce_min_sync(0xffffffffu, R.min_lo);
+    R.max_lo = __reduce_max_sync(0xffffffffu, R.max_lo);
+    R.min_hi = __reduce_min_sync(0xffffffffu, R.min_hi);
+    R.max_hi = __reduce_max_sync(0xffffffffu, R.max_hi);
+#pragma unroll
+    for (int G = 0; G < D / 32; ++G)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) R.o[G][h][nt][i] = 0.f;
+}
+
+// O += T of one tile. NANS: some V scale of it is 255.
+template <int D, int NT, bool NANS>
+__device__ __forceinline__ void add_values(const uint8_t *tile, int lane, uint32_t top, const uint32_t (&p)[4][NT][2],
+                                           const float (&keep)[NT][2], Rows<D, NT> &R) {
+    const int t = lane & 3;
+    const uint32_t least = (uint32_t)max((int)top - 22, 0) * 0x10001u;
+    const uint32_t off = (uint32_t)((int)top - 22) * (1024u * 0x10001u);
+    const float back = v_factor(top);
+#pragma unroll
+    for (int q2 = 0; q2 < D / 64; ++q2) {
+        float T[2][2][NT][4];
+#pragma unroll
+        for (int i = 0; i < 16 * NT; ++i) (&T[0][0][0][0])[i] = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+            const uint8_t *blk = tile + mt * block_bytes(D);
+            // four tokens (2t, 2t+1, 2t+8, 2t+9) x channels 4g.. of two blocks
+            const uint4 w = *reinterpret_cast<const uint4 *>(blk + 8 * D + q2 * 512 + lane * 16);
+            const uint2 vs = *reinterpret_cast<const uint2 *>(blk + 16 * D + D / 2 + t * (D / 8) + q2 * 8);
+            uint32_t a0[4], a1[4], a2[4], a3[4];
+            e2m1x8_to_f16((w.x & 0x0F0F0F0Fu) | ((w.y << 4) & 0xF0F0F0F0u), a0);  // token pairs of the even channels
+            e2m1x8_to_f16(((w.x >> 4) & 0x0F0F0F0Fu) | (w.y & 0xF0F0F0F0u), a1);  // and of the odd ones
+            e2m1x8_to_f16((w.z & 0x0F0F0F0Fu) | ((w.w << 4) & 0xF0F0F0F0u), a2);
+            e2m1x8_to_f16(((w.z >> 4) & 0x0F0F0F0Fu) | (w.w & 0xF0F0F0F0u), a3);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t s = h ? vs.y : vs.x;
+                const uint32_t x0 = __byte_perm(s, 0, 0x4140), x1 = __byte_perm(s, 0, 0x4342);
+                const uint32_t f0 = NANS ? v_factors_nan(x0, least, off) : v_factors(x0, least, off);
+                const uint32_t f1 = NANS ? v_factors_nan(x1, least, off) : v_factors(x1, least, off);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint32_t b0 = NANS ? weigh_nan(p[mt][nt][0], f0) : mul_f16x2(p[mt][nt][0], f0);
+                    const uint32_t b1 = NANS ? weigh_nan(p[mt][nt][1], f1) : mul_f16x2(p[mt][nt][1], f1);
+                    mma_f16(T[h][0][nt], a0[2 * h], a1[2 * h], a2[2 * h], a3[2 * h], b0, b1);
+                    mma_f16(T[h][1][nt], a0[2 * h + 1], a1[2 * h + 1], a2[2 * h + 1], a3[2 * h + 1], b0, b1);
+                }
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float &o = R.o[2 * q2 + h][e][nt][i];
+                        o = fmaf(T[h][e][nt][i], back, o * keep[nt][i & 1]);
+                    }
+    }
+}
+
+// One tile: scores, softmax step, values. have: the 16-token blocks that are there.
+template <int D, int NT>
+__device__ __forceinline__ void add_tile(uint8_t *tile, int j0, uint32_t have, int lane, Rows<D, NT> &R) {
+    const int g = lane >> 2, t = lane & 3;
+    float x[4][NT][4];  // S^T, then exponents, then p: tokens 16 * mt + g (+ 8), rows 8 * nt + 2t (+ 1)
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+        const uint8_t *blk = tile + mt * block_bytes(D);
+        uint32_t k0[D / 32], k1[D / 32], s0, s1;
+        if constexpr (D == 128) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(blk + g * 64 + t * 16);
+            const uint4 v = *reinterpret_cast<const uint4 *>(blk + (g + 8) * 64 + t * 16);
+            k0[0] = u.x, k0[1] = u.y, k0[2] = u.z, k0[3] = u.w;
+            k1[0] = v.x, k1[1] = v.y, k1[2] = v.z, k1[3] = v.w;
+            s0 = *reinterpret_cast<const uint32_t *>(blk + 16 * D + g * 4);
+            s1 = *reinterpret_cast<const uint32_t *>(blk + 16 * D + (g + 8) * 4);
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2 *>(blk + g * 32 + t * 8);
+            const uint2 v = *reinterpret_cast<const uint2 *>(blk + (g + 8) * 32 + t * 8);
+            k0[0] = u.x, k0[1] = u.y;
+            k1[0] = v.x, k1[1] = v.y;
+            s0 = *reinterpret_cast<const uint16_t *>(blk + 16 * D + g * 2);
+            s1 = *reinterpret_cast<const uint16_t *>(blk + 16 * D + (g + 8) * 2);
+        }
+#pragma unroll
+        for (int G = 0; G < D / 32; ++G) {
+            uint32_t a[4], b[4];
+            e2m1x8_to_f16(k0[G], a);
+            e2m1x8_to_f16(k1[G], b);
+            // E8M0 byte into the exponent: 255 gives infinity, and NaN on the zero codes that go with it; 0 gives 0
+            const float f0 = __uint_as_float(__byte_perm(s0, 0, 0x0444 | (G << 12)) >> 1);
+            const float f1 = __uint_as_float(__byte_perm(s1, 0, 0x0444 | (G << 12)) >> 1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16(d, a[0], b[0], a[1], b[1], R.q[nt][G][0], R.q[nt][G][1]);
+                mma_f16(d, a[2], b[2], a[3], b[3], R.q[nt][G][2], R.q[nt][G][3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float f = i < 2 ? f0 : f1;
+                    x[mt][nt][i] = G == 0 ? d[i] * f : fmaf(d[i], f, x[mt][nt][i]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[mt][nt][i] *= R.c[nt][i & 1];
+    if (have != 0xFu || j0 + TILE > R.min_hi || j0 < R.max_lo) {
+        // some row does not see all of it: exponents of -infinity there
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = j0 + 16 * mt + g + 8 * (i >> 1);
+                    if (!(have >> mt & 1) || j >= R.hi[nt][i & 1] || j < R.lo[nt][i & 1]) x[mt][nt][i] = -INFINITY;
+                }
+        // V of tokens that no row sees may hold anything: scale bytes of zero
+        __syncwarp();
+        for (int i = lane; i < TILE; i += 32) {
+            const int j = j0 + i, tok = i & 15;
+            if (!(have >> (i >> 4) & 1) || j >= R.max_hi || j < R.min_lo)
+#pragma unroll
+                for (int G = 0; G < D / 32; ++G) tile[(i >> 4) * block_bytes(D) + v_scale<D>(tok, G)] = 0;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next copy into this stage
+        __syncwarp();
+    }
+    // the running maximum; rows' values lie in the eight lanes of equal t
+    float keep[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float top = R.m[nt][i];
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) top = fmaxf(top, fmaxf(x[mt][nt][i], x[mt][nt][i + 2]));
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float base = top == -INFINITY ? 0.f : top;
+            keep[nt][i] = top == R.m[nt][i] ? 1.f : exp2_approx(R.m[nt][i] - base);
+            R.m[nt][i] = top;
+            float sum = 0.f;
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                for (int h = 0; h < 4; h += 2) {
+                    const float p = exp2_approx(x[mt][nt][i + h] - base + 8.f);
+                    x[mt][nt][i + h] = p;
+                    sum += p;
+                }
+            R.l[nt][i] = fmaf(R.l[nt][i], keep[nt][i], sum);
+        }
+    uint32_t p[4][NT][2];
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            p[mt][nt][0] = transpose8x8(pack_f16(x[mt][nt][0], x[mt][nt][1]));
+            p[mt][nt][1] = transpose8x8(pack_f16(x[mt][nt][2], x[mt][nt][3]));
+        }
+    // the tile's largest V scale: D/2 bytes a block, D/16 a lane
+    uint32_t top = 0;
+    const uint8_t *vs = tile + (lane >> 3) * block_bytes(D) + 16 * D + D / 2 + (lane & 7) * (D / 16);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+        const uint32_t w = reinterpret_cast<const uint32_t *>(vs)[i];
+        top = __vmaxu2(top, __vmaxu2(w & 0x00FF00FFu, (w >> 8) & 0x00FF00FFu));
+    }
+    top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
+    if (top != 255) {
+        add_values<D, NT, false>(tile, lane, top, p, keep, R);
+    } else {
+        top = 0;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) top = max(top, vs[i] == 255 ? 0u : (uint32_t)vs[i]);
+        top = __reduce_max_sync(0xffffffffu, top);
+        add_values<D, NT, true>(tile, lane, top, p, keep, R);
+    }
+}
+
+// four channels of a row's result, and its lse
+__device__ __forceinline__ void store_out(const AttnArgs &a, int64_t row, int D, int d, const float4 &o, float m, float l) {
+    const float inv = l == 0.f ? 0.f : 256.f / l;
+    uint2 u;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.x) : "f"(o.y * inv), "f"(o.x * inv));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.y) : "f"(o.w * inv), "f"(o.z * inv));
+    *reinterpret_cast<uint2 *>(a.out + row * D + d) = u;
+    if (a.lse && d == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l) - 8.f) * 0.693147180559945309f;
+}
+
+// The end of a piece: l summed over the lanes; the rows go out if the piece was all of them, else into a partial.
+template <int D, int NT>
+__device__ __forceinline__ void end_rows(const AttnArgs &a, const Cursor &c, int group, int lane, Rows<D, NT> &R,
+                                         bool whole, float *part) {
+    const int g = lane >> 2, t = lane & 3;
+    const int head = c.seg / c.s.nrc, r0 = (c.seg % c.s.nrc) * 8 * NT, n = c.s.m * group;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float l = R.l[nt][i];
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            const int r = 8 * nt + 2 * t + i;
+            if (whole && r0 + r >= n) continue;
+            const int64_t row = whole ? row_index(a, c.s, head, group, r0 + r) : 0;
+#pragma unroll
+            for (int G = 0; G < D / 32; ++G) {
+                const float4 o = make_float4(R.o[G][0][nt][i], R.o[G][0][nt][i + 2], R.o[G][1][nt][i], R.o[G][1][nt][i + 2]);
+                if (whole)
+                    store_out(a, row, D, 32 * G + 4 * g, o, R.m[nt][i], l);
+                else
+                    *reinterpret_cast<float4 *>(part + r * D + 32 * G + 4 * g) = o;
+            }
+            if (!whole && g == 0) {
+                part[8 * NT * D + r] = R.m[nt][i];
+                part[8 * NT * D + 8 * NT + r] = l;
+            }
+        }
+}
+
+// Workspace: prefix [B + 1] of the sequences' units, then per CTA two partials for the joining kernel and one per
+// warp for a first piece that is not its last
+__host__ __device__ inline size_t prefix_bytes(int B) { return round_up(((size_t)B + 1) * 8, 256); }
+
+template <int D, int NT>
+__global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 3 : 2) attn_split_kernel(const AttnArgs a, uint8_t *ws) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    auto &sm = *reinterpret_cast<Smem<D, NT> *>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int group = a.n_q / a.c.n_kv;
+    constexpr int PART = part_floats(D, 8 * NT);
+    int64_t *prefix = reinterpret_cast<int64_t *>(ws);
+    float *parts = reinterpret_cast<float *>(ws + prefix_bytes(a.B));
+    float *scratch = parts + (size_t)gridDim.x * 2 * PART;
+
+    if (lane == 0)
+        for (int s = 0; s < STAGES; ++s) mbar_init(smem_u32(&sm.full[warp][s]), 1);
+    if (lane < 2) sm.ptr[warp][lane] = nullptr;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    pdl_acquire();
+
+    // ---- the line of work: each thread a run of sequences, then a scan over the threads ----
+    const int per = (a.B + WARPS * 32 - 1) / (WARPS * 32);
+    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        const Seq s = load_seq<NT>(a, b, group);
+        mine += (int64_t)s.T * s.nrc * a.c.n_kv;
+        if (blockIdx.x == 0 && a.kv_lens[b] > s.len) atomicOr(a.status, PQE_STATUS_BAD_PAGE);
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) sm.scan[warp] = incl;
+    __syncthreads();
+    int64_t total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) before += sm.scan[w];
+        total += sm.scan[w];
+    }
+    before += incl - mine;
+    // shares of at least a tile a warp
+    const int64_t n_cta = min((int64_t)gridDim.x, (total + WARPS - 1) / WARPS);
+    if (blockIdx.x == 0) {
+        int64_t at = before;
+        for (int b = b0; b < b1; ++b) {
+            prefix[b] = at;
+            const Seq s = load_seq<NT>(a, b, group);
+            at += (int64_t)s.T * s.nrc * a.c.n_kv;
+        }
+        if (tid == 0) prefix[a.B] = total;
+    }
+    if (blockIdx.x >= n_cta) return;
+    const int64_t nw = n_cta * WARPS;
+    for (int w = 0; w < WARPS; ++w) {
+        const int64_t u = share_start((int64_t)blockIdx.x * WARPS + w, nw, total);
+        if (u >= before && u < before + mine) {
+            int64_t at = before;
+            for (int b = b0; b < b1; ++b) {
+                const Seq s = load_seq<NT>(a, b, group);
+                const int64_t n = (int64_t)s.T * s.nrc * a.c.n_kv;
+                if (u < at + n) {
+                    sm.start_b[w] = b;
+                    sm.start_off[w] = u - at;
+                    break;
+                }
+                at += n;
+            }
+        }
+    }
+    __syncthreads();
+
+    // ---- this warp's share ----
+    const int64_t u0 = share_start((int64_t)blockIdx.x * WARPS + warp, nw, total);
+    const int64_t u1 = share_start((int64_t)blockIdx.x * WARPS + warp + 1, nw, total);
+    const int64_t cta0 = share_start((int64_t)blockIdx.x * WARPS, nw, total);
+    if (u0 < u1) {
+        Cursor c;  // of the tile at hand
+        c.b = sm.start_b[warp];
+        c.s = load_seq<NT>(a, c.b, group);
+        c.seg = (int)(sm.start_off[warp] / c.s.T);
+        c.tile = (int)(sm.start_off[warp] % c.s.T);
+        Cursor f = c;  // of the tile to fetch next
+        const uint32_t ring = smem_u32(sm.ring[warp][0]), bar = smem_u32(&sm.full[warp][0]);
+        uint32_t have[STAGES] = {};
+        int64_t fu = u0;
+#pragma unroll
+        for (int s = 0; s < STAGES; ++s)
+            if (fu < u1) {
+                have[s] = fetch<D>(a, f, ring + s * tile_bytes<D>(), bar + 8 * s, lane);
+                advance<NT>(a, f, group);
+                ++fu;
+            }
+        Rows<D, NT> R;
+        int from = c.tile;
+        bool ok = true;
+        begin_rows<D, NT>(a, c, group, lane, R);
+        for (int64_t u = u0; u < u1; ++u) {
+            const int it = (int)(u - u0), s = it & 1;
+            if (ok && !mbar_wait(bar + 8 * s, (uint32_t)(it >> 1) & 1u, a.wait_limit)) ok = false;
+            ok = __all_sync(0xffffffffu, ok);
+            const int j0 = (c.s.t0 + c.tile) * TILE;
+            if (ok && j0 < R.max_hi)  // else no row of the chunk sees it
+                add_tile<D, NT>(sm.ring[warp][s], j0, s ? have[1] : have[0], lane, R);
+            __syncwarp();
+            if (ok && fu < u1) {
+                const uint32_t h = fetch<D>(a, f, ring + s * tile_bytes<D>(), bar + 8 * s, lane);
+                if (s)
+                    have[1] = h;
+                else
+                    have[0] = h;
+                advance<NT>(a, f, group);
+                ++fu;
+            }
+            const bool last = u + 1 == u1;
+            if (last || c.tile + 1 == c.s.T) {
+                const bool whole = from == 0 && c.tile + 1 == c.s.T;
+                float *part = nullptr;
+                if (!whole) {
+                    // the last piece stays in shared memory, in the ring that nothing is fetched into any more; an
+                    // earlier one, of which there is at most one, goes through memory
+                    const int k = last ? 1 : 0;
+                    part = last ? reinterpret_cast<float *>(sm.ring[warp][0])
+                                : scratch + ((size_t)blockIdx.x * WARPS + warp) * PART;
+                    if (lane == 0) {
+                        sm.seg_start[warp][k] = u - c.tile;
+                        sm.from[warp][k] = from;
+                        sm.to[warp][k] = c.tile + 1;
+                        sm.len_t[warp][k] = c.s.T;
+                        sm.b[warp][k] = c.b;
+                        sm.seg[warp][k] = c.seg;
+                        sm.ptr[warp][k] = part;
+                    }
+                }
+                __syncwarp();
+                end_rows<D, NT>(a, c, group, lane, R, whole, part);
+                if (!last) {
+                    advance<NT>(a, c, group);
+                    from = 0;
+                    begin_rows<D, NT>(a, c, group, lane, R);
+                }
+            } else {
+                ++c.tile;
+            }
+        }
+        if (!ok) {
+            // the copies in flight land before the block ends (bounded)
+            for (int s = 0; s < STAGES; ++s) {
+                mbar_wait(bar + 8 * s, 0, a.wait_limit);
+                mbar_wait(bar + 8 * s, 1, a.wait_limit);
+            }
+            if (lane == 0) atomicOr(a.status, PQE_STATUS_TIMEOUT);
+        }
+    }
+    __syncthreads();
+
+    // ---- join the CTA's pieces, in order ----
+    for (int i = 0; i < 2 * WARPS;) {
+        const int w = i >> 1, k = i & 1;
+        if (!sm.ptr[w][k]) {
+            ++i;
+            continue;
+        }
+        int e = i + 1, to = sm.to[w][k];
+        while (e < 2 * WARPS && (!sm.ptr[e >> 1][e & 1] || sm.seg_start[e >> 1][e & 1] == sm.seg_start[w][k])) {
+            if (sm.ptr[e >> 1][e & 1]) to = sm.to[e >> 1][e & 1];
+            ++e;
+        }
+        const bool whole = sm.from[w][k] == 0 && to == sm.len_t[w][k];
+        const Seq s = load_seq<NT>(a, sm.b[w][k], group);
+        const int head = sm.seg[w][k] / s.nrc, r0 = (sm.seg[w][k] % s.nrc) * 8 * NT;
+        float *part = parts + ((size_t)blockIdx.x * 2 + (sm.seg_start[w][k] > cta0 ? 1 : 0)) * PART;
+        for (int item = tid; item < 8 * NT * D / 4; item += WARPS * 32) {
+            const int r = item / (D / 4), d = item % (D / 4) * 4;
+            float m = -INFINITY, l = 0.f;
+            for (int x = i; x < e; ++x)
+                if (const float *p = sm.ptr[x >> 1][x & 1]) m = fmaxf(m, p[8 * NT * D + r]);
+            const float base = m == -INFINITY ? 0.f : m;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int x = i; x < e; ++x)
+                if (const float *p = sm.ptr[x >> 1][x & 1]) {
+                    const float f = exp2_approx(p[8 * NT * D + r] - base);
+                    const float4 v = *reinterpret_cast<const float4 *>(p + r * D + d);
+                    l = fmaf(p[8 * NT * D + 8 * NT + r], f, l);
+                    o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+                }
+            if (whole) {
+                if (r0 + r < s.m * group) store_out(a, row_index(a, s, head, group, r0 + r), D, d, o, m, l);
+            } else {
+                *reinterpret_cast<float4 *>(part + r * D + d) = o;
+                if (d == 0) {
+                    part[8 * NT * D + r] = m;
+                    part[8 * NT * D + 8 * NT + r] = l;
+                }
+            }
+        }
+        i = e;
+    }
+}
+
+// One warp per (query token, head): joins the partials of a row that more than
+// one CTA took part in, in the order of the cache; and writes the rows of
+// sequences with no token to see.
+template <int D, int NT>
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a, const uint8_t *ws, int split_ctas) {
+    constexpr int PART = part_floats(D, 8 * NT), E = D / 32;
+    pdl_acquire();
+    const int lane = threadIdx.x & 31, group = a.n_q / a.c.n_kv;
+    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= (int64_t)a.total_q * a.n_q) return;
+    const int tok = (int)(row / a.n_q), h = (int)(row % a.n_q);
+    // the last sequence that begins at or before the token (sequences without queries begin where the next does)
+    int lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (a.q_offsets[mid] <= tok)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const Seq s = load_seq<NT>(a, lo, group);
+    if (tok < s.first || tok >= s.first + s.m) return;  // a row of no sequence
+    if (s.T == 0) {
+        if (lane < D / 4) store_out(a, row, D, lane * 4, make_float4(0.f, 0.f, 0.f, 0.f), 0.f, 0.f);
+        return;
+    }
+    const int64_t *prefix = reinterpret_cast<const int64_t *>(ws);
+    const float *parts = reinterpret_cast<const float *>(ws + prefix_bytes(a.B));
+    const int64_t total = prefix[a.B], n_cta = min((int64_t)split_ctas, (total + WARPS - 1) / WARPS);
+    const int rr = (tok - s.first) * group + h % group, r = rr % (8 * NT);
+    const int64_t s0 = prefix[lo] + ((int64_t)(h / group) * s.nrc + rr / (8 * NT)) * s.T;
+    const int64_t nw = n_cta * WARPS;
+    const int64_t c0 = share_of(s0, nw, total) / WARPS, c1 = share_of(s0 + s.T - 1, nw, total) / WARPS;
+    if (c0 == c1) return;  // that CTA wrote it
+    // the first CTA's partial is its second one if the row begins inside its share
+    const bool inside = s0 > share_start(c0 * WARPS, nw, total);
+    auto at = [&](int64_t c) { return parts + (size_t)(2 * c + (c == c0 && inside ? 1 : 0)) * PART; };
+    float m = -INFINITY;
+    for (int64_t c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, at(c)[8 * NT * D + r]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float base = m == -INFINITY ? 0.f : m;
+    float o[E] = {}, l = 0.f;
+#pragma unroll 4
+    for (int64_t c = c0; c <= c1; ++c) {
+        const float *p = at(c);
+        const float f = exp2_approx(p[8 * NT * D + r] - base);
+        l = fmaf(p[8 * NT * D + 8 * NT + r], f, l);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(p[r * D + lane * E + e], f, o[e]);
+    }
+    const float inv = l == 0.f ? 0.f : 256.f / l;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+        uint32_t u;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(o[e + 1] * inv), "f"(o[e] * inv));
+        *reinterpret_cast<uint32_t *>(a.out + row * D + lane * E + e) = u;
+    }
+    if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l) - 8.f) * 0.693147180559945309f;
+}
+
+template <int D, int NT>
+int launch(const AttnArgs &a, int max_q, int sms, void *ws, cudaStream_t s) {
+    // as many CTAs as fit, or as the longest sequences that the table can describe give work for
+    const int group = a.n_q / a.c.n_kv;
+    const int64_t nrc = ((int64_t)max_q * group + 8 * NT - 1) / (8 * NT);
+    const int64_t tiles = (((int64_t)a.max_pages << a.c.page_shift) + TILE - 1) / TILE;
+    const double most = (double)a.B * a.c.n_kv * nrc * tiles / WARPS + 1;
+    int grid = sms * (NT == 1 ? 3 : 2);
+    if (most < grid) grid = (int)most;
+    static bool set[PQE_MAX_DEVICES] = {};
+    int dev = 0, n = 0;
+    int rc = device_info(dev, n);
+    if (rc != PQE_OK) return rc;
+    constexpr int smem = (int)sizeof(Smem<D, NT>);
+    if (!set[dev]) {
+        PQE_CUDA_TRY(cudaFuncSetAttribute(attn_split_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+        set[dev] = true;
+    }
+    rc = launch_pdl(attn_split_kernel<D, NT>, dim3((unsigned)grid), dim3(WARPS * 32), smem, s, a,
+                    static_cast<uint8_t *>(ws));
+    if (rc != PQE_OK) return rc;
+    const int64_t rows = (int64_t)a.total_q * a.n_q;
+    return launch_pdl(attn_join_kernel<D, NT>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a,
+                      static_cast<const uint8_t *>(ws), grid);
+}
+
+}  // namespace split
+
+// Rows of a KV head taken together: 8 where a step has no more, else 16.
+size_t attn_split_ws(int B, int max_q, int group, int d) {
+    const int NT = (int64_t)max_q * group <= 8 ? 1 : 2;
+    int dev = 0, sms = 0;
+    if (device_info(dev, sms) != PQE_OK) sms = 160;  // without a device: an upper bound
+    return split::prefix_bytes(B) +
+           (size_t)sms * (NT == 1 ? 3 : 2) * (2 + split::WARPS) * split::part_floats(d, 8 * NT) * sizeof(float);
+}
+
+int attn_split(const pqe_kv_cache *cache, const AttnArgs &a, int max_q, int sms, void *ws, cudaStream_t s) {
+    const bool one = (int64_t)max_q * (a.n_q / a.c.n_kv) <= 8;
+    if (cache->d == 128) return one ? split::launch<128, 1>(a, max_q, sms, ws, s) : split::launch<128, 2>(a, max_q, sms, ws, s);
+    return one ? split::launch<64, 1>(a, max_q, sms, ws, s) : split::launch<64, 2>(a, max_q, sms, ws, s);
+}
+
+}  // namespace kv
+}  // namespace pqe
