@@ -689,7 +689,7 @@ PQE_API int kv_cache_read(const pqe_kv_cache *cache, const int64_t *slots, int n
  *          cache (its tokens count as masked) or a length beyond the table
  *          (cut); PQE_STATUS_TIMEOUT as elsewhere
  * Limits: n_q a multiple of n_kv, n_q <= 1024; B >= 0, total_q >= 0 (either 0:
- * a no-op); max_pages * page_size < 2^31; scale finite. */
+ * a no-op); total_q * n_q and max_pages * page_size below 2^31; scale finite. */
 PQE_API size_t kv_paged_attention_workspace_size(int B, int total_q, int max_q, int n_q, int n_kv, int d);
 PQE_API int kv_paged_attention(const pqe_kv_cache *cache, const void *q, int64_t q_stride, const int32_t *q_offsets,
                                const int32_t *kv_lens, const int32_t *block_table, int max_pages, int B, int total_q,

@@ -7,10 +7,11 @@
 // fill a tile that 16-row forms would leave half empty. Per tile of 64 tokens:
 //   S[j, r]  = sum_G 2^(ks[j, G]) * (codes of block G . q)   K scales in fp32,
 //              after each 32-channel block's two MMAs: codes enter as they are
-//   p        = 2^(c_r S - m_r + 8), running maximum m_r, sum l_r
-//   T[d, r]  = sum_j code[j, d] * (p * 2^(vs[j, G] - top + 7)),  top the largest
-//              V scale of the tile: p and the factor stay inside f16
-//   O        = O * 2^(m_old - m_new) + T * 2^(top - 15)      fp32
+//   p        = 2^(c_r (S - m_r) + 8), running maximum m_r, sum l_r
+//   O[d, r] += code[j, d] * (p * 2^(vs[j, G] - top + 7)), top the largest V scale
+//              of the tiles so far: p and the factor stay inside f16, O in fp32
+// and O is scaled when a maximum or top has grown, which is rare after the
+// first tiles.
 // P^T's fragments come from S^T's by movmatrix, with no trip through memory.
 //
 // The cache is read once. Work is (sequence, KV head, 8 * NT rows, tile); all of
@@ -45,16 +46,24 @@ constexpr int tile_bytes() {
 // one partial result: O [rows][D], m [rows], l [rows], all fp32
 __host__ __device__ constexpr int part_floats(int d, int rows) { return rows * (d + 2); }
 
+// what a tile's scale bytes become for the MMAs' lanes
+template <int D>
+struct Factors {
+    float k[TILE][D / 32];        // [token][block]: 2^(scale - 127)
+    uint32_t v[4][4][D / 32][2];  // [16 tokens][t][block]: f16 pairs for tokens 2t, 2t+1 and 2t+8, 2t+9
+};
+
 template <int D, int NT>
 struct Smem {
     alignas(16) uint8_t ring[WARPS][STAGES][tile_bytes<D>()];  // a warp's last partial takes its ring's place
+    alignas(16) Factors<D> fac[WARPS];
     alignas(8) uint64_t full[WARPS][STAGES];
-    int64_t scan[WARPS * 32];
+    int64_t scan[WARPS];
     int64_t start_off[WARPS];
     int start_b[WARPS];
     // pieces of (sequence, head, rows) that the warps did not finish alone: two each
     int64_t seg_start[WARPS][2];
-    int from[WARPS][2], to[WARPS][2], len_t[WARPS][2], b[WARPS][2], seg[WARPS][2];
+    int from[WARPS][2], to[WARPS][2], len_t[WARPS][2], b[WARPS][2], head[WARPS][2], chunk[WARPS][2];
     const float *ptr[WARPS][2];
 };
 
@@ -63,9 +72,14 @@ __device__ __forceinline__ int64_t share_start(int64_t i, int64_t n, int64_t tot
 // the share that unit u falls into
 __device__ __forceinline__ int64_t share_of(int64_t u, int64_t n, int64_t total) { return ((u + 1) * n - 1) / total; }
 
-// a sequence's share of the line of work
+// Beginning and ending a (sequence, head, rows) costs about as much as a tile: it counts as one in the line of work,
+// before its first tile. (64 sequences of 1 to 8192 tokens: without it the slowest SM took 1.27 times the mean.)
+constexpr int OPEN = 1;
+
+// a sequence's part of the line of work
 struct Seq {
     int first, m, len, t0, T, nrc;
+    __device__ __forceinline__ int64_t units(int n_kv) const { return T > 0 ? (int64_t)(T + OPEN) * nrc * n_kv : 0; }
 };
 template <int NT>
 __device__ __forceinline__ Seq load_seq(const AttnArgs &a, int b, int group) {
@@ -80,15 +94,16 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs &a, int b, int group) {
 }
 
 struct Cursor {
-    int b, seg, tile;  // seg = kv head * nrc + row chunk; tile counts from the sequence's t0
+    int b, head, chunk, tile;  // tile counts from the sequence's t0
     Seq s;
 };
 template <int NT>
-__device__ __forceinline__ void advance(const AttnArgs &a, Cursor &c, int group) {
-    if (++c.tile < c.s.T) return;
+__device__ __forceinline__ void next_rows(const AttnArgs &a, Cursor &c, int group) {
     c.tile = 0;
-    if (++c.seg < a.c.n_kv * c.s.nrc) return;
-    c.seg = 0;
+    if (++c.chunk < c.s.nrc) return;
+    c.chunk = 0;
+    if (++c.head < a.c.n_kv) return;
+    c.head = 0;
     while (++c.b < a.B) {
         c.s = load_seq<NT>(a, c.b, group);
         if (c.s.T > 0) return;
@@ -109,38 +124,56 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// the same into zeros
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
 
+// A tile's copies: lane i's takes the blocks from i << shift on, of one page.
+__device__ __forceinline__ int blocks_shift(const AttnArgs &a) { return min(a.c.page_shift - 4, 2); }
+__device__ __forceinline__ int tile_blocks(const Cursor &c) {
+    return min(TILE / BLOCK, (c.s.len - (c.s.t0 + c.tile) * TILE + BLOCK - 1) / BLOCK);
+}
+
+// The table entry that this lane's copy of the cursor's tile needs. Asked for a tile early, so that fetch() does not wait.
+__device__ __forceinline__ int table_entry(const AttnArgs &a, const Cursor &c, int lane) {
+    const int blk = lane << blocks_shift(a);
+    if (blk >= tile_blocks(c)) return -1;
+    return a.block_table[(size_t)c.b * a.max_pages + (((c.s.t0 + c.tile) * TILE + blk * BLOCK) >> a.c.page_shift)];
+}
+
 // Starts the copies of the cursor's tile into a stage; returns the bit mask of
 // its 16-token blocks that the stage will hold (a block of a bad page, or past
 // the end, is not there).
 template <int D>
-__device__ __forceinline__ uint32_t fetch(const AttnArgs &a, const Cursor &c, uint32_t dst, uint32_t bar, int lane) {
-    const int j0 = (c.s.t0 + c.tile) * TILE;
-    const int nblk = min(TILE / BLOCK, (c.s.len - j0 + BLOCK - 1) / BLOCK);
-    const int psh = min(a.c.page_shift - 4, 2), per = 1 << psh;  // blocks a copy can take: of one page
-    const int blk = lane << psh;
+__device__ __forceinline__ uint32_t fetch(const AttnArgs &a, const Cursor &c, int page, uint32_t dst, uint32_t bar,
+                                          int lane) {
+    const int nblk = tile_blocks(c), blk = lane << blocks_shift(a);
     uint32_t bytes = 0, mask = 0;
     const uint8_t *src = nullptr;
     if (blk < nblk) {
-        const int j = j0 + blk * BLOCK;
-        const int page = a.block_table[(size_t)c.b * a.max_pages + (j >> a.c.page_shift)];
         if (page >= 0 && page < a.c.n_pages) {
-            const int n = min(per, nblk - blk);
-            src = block_of<D>(a.c, page, j & ((1 << a.c.page_shift) - 1), c.seg / c.s.nrc);
+            const int n = min(1 << blocks_shift(a), nblk - blk);
+            const int j = (c.s.t0 + c.tile) * TILE + blk * BLOCK;
+            src = block_of<D>(a.c, page, j & ((1 << a.c.page_shift) - 1), c.head);
             bytes = n * block_bytes(D);
             mask = ((1u << n) - 1) << blk;
         } else {
             atomicOr(a.status, PQE_STATUS_BAD_PAGE);
         }
     }
-    const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
     mask = __reduce_or_sync(0xffffffffu, mask);
-    if (lane == 0) mbar_expect_tx(bar, total);
+    if (lane == 0) mbar_expect_tx(bar, __popc(mask) * block_bytes(D));
     __syncwarp();
     if (bytes) bulk_copy(dst + blk * block_bytes(D), src, bytes, bar);
     return mask;
@@ -151,17 +184,9 @@ __device__ __forceinline__ int64_t row_index(const AttnArgs &a, const Seq &s, in
     return (int64_t)(s.first + r / group) * a.n_q + head * group + r % group;
 }
 
-// f16 pair of V's block factors 2^(x - top + 7) from two E8M0 bytes in the halves of x; zero 21 and more below
-__device__ __forceinline__ uint32_t v_factors(uint32_t x, uint32_t least, uint32_t off) {
-    return __vmaxu2(x, least) * 1024u - off;
-}
-// the same where a byte may be 255 (NaN)
-__device__ __forceinline__ uint32_t v_factors_nan(uint32_t x, uint32_t least, uint32_t off) {
-    const uint32_t lo = x & 0xFFFFu, hi = x >> 16;
-    uint32_t f = v_factors((lo == 255 ? 0u : lo) | (hi == 255 ? 0u : hi << 16), least, off);
-    if (lo == 255) f = (f & 0xFFFF0000u) | 0x7E00u;
-    if (hi == 255) f = (f & 0xFFFFu) | 0x7E000000u;
-    return f;
+// f16 bits of V's block factor 2^(x - top + 7), x an E8M0 byte; zero from 22 below top on, NaN for 255
+__device__ __forceinline__ uint32_t v_weight(uint32_t x, uint32_t top) {
+    return x == 255 ? 0x7E00u : (uint32_t)max((int)(x - top) + 22, 0) << 10;
 }
 // p * f where a masked row's p, 0, gives 0 whatever f is
 __device__ __forceinline__ uint32_t weigh_nan(uint32_t p, uint32_t f) {
@@ -175,17 +200,19 @@ __device__ __forceinline__ uint32_t weigh_nan(uint32_t p, uint32_t f) {
 template <int D, int NT>
 struct Rows {
     uint32_t q[NT][D / 32][4];  // B fragments: row 8 * nt + g, channels 32 * G + 8 * t ..
-    float c[NT][2];             // of rows 8 * nt + 2 * t, + 1: the factor from S to an exponent of two
+    float c[NT][2];             // of rows 8 * nt + 2 * t, + 1: the factor (above 0) from S to an exponent of two
     int lo[NT][2], hi[NT][2];   // and the tokens they see
     int min_lo, max_lo, min_hi, max_hi;
-    float m[NT][2], l[NT][2];   // l: this lane's tokens only
+    float m[NT][2], l[NT][2];   // m: of S; l: this lane's tokens only
+    uint32_t top;               // the E8M0 byte that o is in units of (2^-15 more)
     float o[D / 32][2][NT][4];  // O^T: block G, channels 4g + {0, 1} and 4g + {2, 3}
 };
 
 template <int D, int NT>
 __device__ __forceinline__ void begin_rows(const AttnArgs &a, const Cursor &c, int group, int lane, Rows<D, NT> &R) {
     const int g = lane >> 2, t = lane & 3;
-    const int head = c.seg / c.s.nrc, r0 = (c.seg % c.s.nrc) * 8 * NT, n = c.s.m * group;
+    const int head = c.head, r0 = c.chunk * 8 * NT, n = c.s.m * group;
+    R.top = 0;
     R.min_lo = R.min_hi = INT32_MAX;
     R.max_lo = R.max_hi = 0;
 #pragma unroll
@@ -217,7 +244,10 @@ __device__ __forceinline__ void begin_rows(const AttnArgs &a, const Cursor &c, i
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         float f, inv;
         q_factor(top, f, inv);
-        inv = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : inv * a.scale;  // a row that is not finite gives NaN
+        inv *= fabsf(a.scale);
+        if (a.scale < 0.f) f = -f;
+        if (inv == 0.f) f = 0.f, inv = 1.f;                       // scores of zero
+        if (top >= 0x7F80u) f = __uint_as_float(0x7FC00000u);  // a row that is not finite: scores of NaN
 #pragma unroll
         for (int G = 0; G < D / 32; ++G) {
             const uint32_t w[4] = {raw[G].x, raw[G].y, raw[G].z, raw[G].w};
@@ -249,25 +279,18 @@ __device__ __forceinline__ void begin_rows(const AttnArgs &a, const Cursor &c, i
                 for (int i = 0; i < 4; ++i) R.o[G][h][nt][i] = 0.f;
 }
 
-// O += T of one tile. NANS: some V scale of it is 255.
+// O += codes . (p * factors) of one tile. NANS: some V scale of it is 255.
 template <int D, int NT, bool NANS>
-__device__ __forceinline__ void add_values(const uint8_t *tile, int lane, uint32_t top, const uint32_t (&p)[4][NT][2],
-                                           const float (&keep)[NT][2], Rows<D, NT> &R) {
+__device__ __forceinline__ void add_values(const uint8_t *tile, const Factors<D> &fac, int lane,
+                                           const uint32_t (&p)[4][NT][2], Rows<D, NT> &R) {
     const int t = lane & 3;
-    const uint32_t least = (uint32_t)max((int)top - 22, 0) * 0x10001u;
-    const uint32_t off = (uint32_t)((int)top - 22) * (1024u * 0x10001u);
-    const float back = v_factor(top);
 #pragma unroll
     for (int q2 = 0; q2 < D / 64; ++q2) {
-        float T[2][2][NT][4];
-#pragma unroll
-        for (int i = 0; i < 16 * NT; ++i) (&T[0][0][0][0])[i] = 0.f;
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
-            const uint8_t *blk = tile + mt * block_bytes(D);
             // four tokens (2t, 2t+1, 2t+8, 2t+9) x channels 4g.. of two blocks
-            const uint4 w = *reinterpret_cast<const uint4 *>(blk + 8 * D + q2 * 512 + lane * 16);
-            const uint2 vs = *reinterpret_cast<const uint2 *>(blk + 16 * D + D / 2 + t * (D / 8) + q2 * 8);
+            const uint4 w = *reinterpret_cast<const uint4 *>(tile + mt * block_bytes(D) + 8 * D + q2 * 512 + lane * 16);
+            const uint4 vf = *reinterpret_cast<const uint4 *>(fac.v[mt][t][2 * q2]);
             uint32_t a0[4], a1[4], a2[4], a3[4];
             e2m1x8_to_f16((w.x & 0x0F0F0F0Fu) | ((w.y << 4) & 0xF0F0F0F0u), a0);  // token pairs of the even channels
             e2m1x8_to_f16(((w.x >> 4) & 0x0F0F0F0Fu) | (w.y & 0xF0F0F0F0u), a1);  // and of the odd ones
@@ -275,86 +298,128 @@ __device__ __forceinline__ void add_values(const uint8_t *tile, int lane, uint32
             e2m1x8_to_f16(((w.z >> 4) & 0x0F0F0F0Fu) | (w.w & 0xF0F0F0F0u), a3);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t s = h ? vs.y : vs.x;
-                const uint32_t x0 = __byte_perm(s, 0, 0x4140), x1 = __byte_perm(s, 0, 0x4342);
-                const uint32_t f0 = NANS ? v_factors_nan(x0, least, off) : v_factors(x0, least, off);
-                const uint32_t f1 = NANS ? v_factors_nan(x1, least, off) : v_factors(x1, least, off);
+                const uint32_t f0 = h ? vf.z : vf.x, f1 = h ? vf.w : vf.y;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const uint32_t b0 = NANS ? weigh_nan(p[mt][nt][0], f0) : mul_f16x2(p[mt][nt][0], f0);
                     const uint32_t b1 = NANS ? weigh_nan(p[mt][nt][1], f1) : mul_f16x2(p[mt][nt][1], f1);
-                    mma_f16(T[h][0][nt], a0[2 * h], a1[2 * h], a2[2 * h], a3[2 * h], b0, b1);
-                    mma_f16(T[h][1][nt], a0[2 * h + 1], a1[2 * h + 1], a2[2 * h + 1], a3[2 * h + 1], b0, b1);
+                    mma_f16(R.o[2 * q2 + h][0][nt], a0[2 * h], a1[2 * h], a2[2 * h], a3[2 * h], b0, b1);
+                    mma_f16(R.o[2 * q2 + h][1][nt], a0[2 * h + 1], a1[2 * h + 1], a2[2 * h + 1], a3[2 * h + 1], b0, b1);
                 }
             }
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float &o = R.o[2 * q2 + h][e][nt][i];
-                        o = fmaf(T[h][e][nt][i], back, o * keep[nt][i & 1]);
-                    }
     }
 }
 
 // One tile: scores, softmax step, values. have: the 16-token blocks that are there.
 template <int D, int NT>
-__device__ __forceinline__ void add_tile(uint8_t *tile, int j0, uint32_t have, int lane, Rows<D, NT> &R) {
+__device__ __forceinline__ void add_tile(uint8_t *tile, Factors<D> &fac, int j0, uint32_t have, int lane, Rows<D, NT> &R) {
     const int g = lane >> 2, t = lane & 3;
+    const bool part = have != 0xFu || j0 + TILE > R.min_hi || j0 < R.max_lo;  // some row does not see all of it
+    if (part) {
+        // V of tokens that no row sees may hold anything: scale bytes of zero
+        for (int i = lane; i < TILE; i += 32) {
+            const int j = j0 + i;
+            if (!(have >> (i >> 4) & 1) || j >= R.max_hi || j < R.min_lo)
+#pragma unroll
+                for (int G = 0; G < D / 32; ++G) tile[(i >> 4) * block_bytes(D) + v_scale<D>(i & 15, G)] = 0;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next copy into this stage
+        __syncwarp();
+    }
+    // The scale bytes as the factors that the lanes take. Each would otherwise be made by the four lanes (K) or eight
+    // (V) that use it, on the integer pipe that the code conversions fill.
+    uint32_t top = 0;
+    {
+        const uint8_t *sc = tile + (lane >> 4) * block_bytes(D) + 16 * D;  // of tokens lane and lane + 32
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float f[D / 32];
+            const uint8_t *at = sc + 2 * h * block_bytes(D) + (lane & 15) * (D / 32);
+            const uint32_t w = D == 128 ? *reinterpret_cast<const uint32_t *>(at) : *reinterpret_cast<const uint16_t *>(at);
+            // byte into the exponent: 255 gives infinity, and NaN on the zero codes that go with it; 0 gives 0
+#pragma unroll
+            for (int G = 0; G < D / 32; ++G) f[G] = __uint_as_float(w << (23 - 8 * G > 0 ? 23 - 8 * G : 0) >> (G == 3 ? 1 : 0) & 0x7F800000u);
+            if constexpr (D == 128)
+                *reinterpret_cast<float4 *>(fac.k[lane + 32 * h]) = make_float4(f[0], f[1], f[2], f[3]);
+            else
+                *reinterpret_cast<float2 *>(fac.k[lane + 32 * h]) = make_float2(f[0], f[1]);
+        }
+        uint32_t w[D / 64];  // D/64 of the tile's words [16 tokens][t][block]
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+            w[i] = *reinterpret_cast<const uint32_t *>(tile + (lane >> 3) * block_bytes(D) + 16 * D + D / 2 +
+                                                       (lane & 7) * (D / 16) + 4 * i);
+            top = max(top, max(max(w[i] & 255u, w[i] >> 8 & 255u), max(w[i] >> 16 & 255u, w[i] >> 24)));
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (top == 255) {
+            uint32_t u = 0;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+                for (int j = 0; j < 32; j += 8) u = max(u, (w[i] >> j & 255u) == 255 ? 0u : w[i] >> j & 255u);
+            top = __reduce_max_sync(0xffffffffu, u) | 256u;  // the bit: there are some
+        }
+        const bool nans = top > 255;
+        top = max(top & 255u, R.top) | (nans ? 256u : 0u);
+        uint32_t *vf = &fac.v[0][0][0][0] + lane * (D / 32);
+        uint32_t o[D / 32];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            const uint32_t x = w[i >> 1] >> (16 * (i & 1));
+            o[i] = v_weight(x & 255u, top & 255u) | v_weight(x >> 8 & 255u, top & 255u) << 16;
+        }
+        if constexpr (D == 128)
+            *reinterpret_cast<uint4 *>(vf) = make_uint4(o[0], o[1], o[2], o[3]);
+        else
+            *reinterpret_cast<uint2 *>(vf) = make_uint2(o[0], o[1]);
+    }
+    __syncwarp();
     float x[4][NT][4];  // S^T, then exponents, then p: tokens 16 * mt + g (+ 8), rows 8 * nt + 2t (+ 1)
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
         const uint8_t *blk = tile + mt * block_bytes(D);
-        uint32_t k0[D / 32], k1[D / 32], s0, s1;
+        uint32_t k0[D / 32], k1[D / 32];
+        float f0[D / 32], f1[D / 32];
         if constexpr (D == 128) {
             const uint4 u = *reinterpret_cast<const uint4 *>(blk + g * 64 + t * 16);
             const uint4 v = *reinterpret_cast<const uint4 *>(blk + (g + 8) * 64 + t * 16);
             k0[0] = u.x, k0[1] = u.y, k0[2] = u.z, k0[3] = u.w;
             k1[0] = v.x, k1[1] = v.y, k1[2] = v.z, k1[3] = v.w;
-            s0 = *reinterpret_cast<const uint32_t *>(blk + 16 * D + g * 4);
-            s1 = *reinterpret_cast<const uint32_t *>(blk + 16 * D + (g + 8) * 4);
+            const float4 a = *reinterpret_cast<const float4 *>(fac.k[16 * mt + g]);
+            const float4 b = *reinterpret_cast<const float4 *>(fac.k[16 * mt + g + 8]);
+            f0[0] = a.x, f0[1] = a.y, f0[2] = a.z, f0[3] = a.w;
+            f1[0] = b.x, f1[1] = b.y, f1[2] = b.z, f1[3] = b.w;
         } else {
             const uint2 u = *reinterpret_cast<const uint2 *>(blk + g * 32 + t * 8);
             const uint2 v = *reinterpret_cast<const uint2 *>(blk + (g + 8) * 32 + t * 8);
             k0[0] = u.x, k0[1] = u.y;
             k1[0] = v.x, k1[1] = v.y;
-            s0 = *reinterpret_cast<const uint16_t *>(blk + 16 * D + g * 2);
-            s1 = *reinterpret_cast<const uint16_t *>(blk + 16 * D + (g + 8) * 2);
+            const float2 a = *reinterpret_cast<const float2 *>(fac.k[16 * mt + g]);
+            const float2 b = *reinterpret_cast<const float2 *>(fac.k[16 * mt + g + 8]);
+            f0[0] = a.x, f0[1] = a.y;
+            f1[0] = b.x, f1[1] = b.y;
         }
 #pragma unroll
         for (int G = 0; G < D / 32; ++G) {
             uint32_t a[4], b[4];
             e2m1x8_to_f16(k0[G], a);
             e2m1x8_to_f16(k1[G], b);
-            // E8M0 byte into the exponent: 255 gives infinity, and NaN on the zero codes that go with it; 0 gives 0
-            const float f0 = __uint_as_float(__byte_perm(s0, 0, 0x0444 | (G << 12)) >> 1);
-            const float f1 = __uint_as_float(__byte_perm(s1, 0, 0x0444 | (G << 12)) >> 1);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_f16(d, a[0], b[0], a[1], b[1], R.q[nt][G][0], R.q[nt][G][1]);
+                float d[4];
+                mma_f16_first(d, a[0], b[0], a[1], b[1], R.q[nt][G][0], R.q[nt][G][1]);
                 mma_f16(d, a[2], b[2], a[3], b[3], R.q[nt][G][2], R.q[nt][G][3]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float f = i < 2 ? f0 : f1;
+                    const float f = i < 2 ? f0[G] : f1[G];
                     x[mt][nt][i] = G == 0 ? d[i] * f : fmaf(d[i], f, x[mt][nt][i]);
                 }
             }
         }
     }
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[mt][nt][i] *= R.c[nt][i & 1];
-    if (have != 0xFu || j0 + TILE > R.min_hi || j0 < R.max_lo) {
-        // some row does not see all of it: exponents of -infinity there
+    if (part) {
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
@@ -364,42 +429,47 @@ __device__ __forceinline__ void add_tile(uint8_t *tile, int j0, uint32_t have, i
                     const int j = j0 + 16 * mt + g + 8 * (i >> 1);
                     if (!(have >> mt & 1) || j >= R.hi[nt][i & 1] || j < R.lo[nt][i & 1]) x[mt][nt][i] = -INFINITY;
                 }
-        // V of tokens that no row sees may hold anything: scale bytes of zero
-        __syncwarp();
-        for (int i = lane; i < TILE; i += 32) {
-            const int j = j0 + i, tok = i & 15;
-            if (!(have >> (i >> 4) & 1) || j >= R.max_hi || j < R.min_lo)
-#pragma unroll
-                for (int G = 0; G < D / 32; ++G) tile[(i >> 4) * block_bytes(D) + v_scale<D>(tok, G)] = 0;
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next copy into this stage
-        __syncwarp();
     }
     // the running maximum; rows' values lie in the eight lanes of equal t
     float keep[NT][2];
+    bool moved = (top & 255u) != R.top;
+    const float shrink = moved ? exp2_approx((float)(int)(R.top - (top & 255u))) : 1.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            float top = R.m[nt][i];
+            float m = R.m[nt][i];
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) top = fmaxf(top, fmaxf(x[mt][nt][i], x[mt][nt][i + 2]));
+            for (int mt = 0; mt < 4; ++mt) m = fmaxf(m, fmaxf(x[mt][nt][i], x[mt][nt][i + 2]));
 #pragma unroll
-            for (int o = 4; o <= 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float base = top == -INFINITY ? 0.f : top;
-            keep[nt][i] = top == R.m[nt][i] ? 1.f : exp2_approx(R.m[nt][i] - base);
-            R.m[nt][i] = top;
+            for (int o = 4; o <= 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float c = R.c[nt][i], base = m == -INFINITY ? -8.f : fmaf(m, c, -8.f);
+            const float k = m == R.m[nt][i] ? 1.f : exp2_approx((R.m[nt][i] - m) * c);
+            moved |= k != 1.f;
+            keep[nt][i] = k * shrink;
+            R.m[nt][i] = m;
             float sum = 0.f;
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
                 for (int h = 0; h < 4; h += 2) {
-                    const float p = exp2_approx(x[mt][nt][i + h] - base + 8.f);
+                    const float p = exp2_approx(fmaf(x[mt][nt][i + h], c, -base));
                     x[mt][nt][i + h] = p;
                     sum += p;
                 }
-            R.l[nt][i] = fmaf(R.l[nt][i], keep[nt][i], sum);
+            R.l[nt][i] = fmaf(R.l[nt][i], k, sum);
         }
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int G = 0; G < D / 32; ++G)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) R.o[G][e][nt][i] *= keep[nt][i & 1];
+        R.top = top & 255u;
+    }
     uint32_t p[4][NT][2];
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
@@ -408,24 +478,11 @@ __device__ __forceinline__ void add_tile(uint8_t *tile, int j0, uint32_t have, i
             p[mt][nt][0] = transpose8x8(pack_f16(x[mt][nt][0], x[mt][nt][1]));
             p[mt][nt][1] = transpose8x8(pack_f16(x[mt][nt][2], x[mt][nt][3]));
         }
-    // the tile's largest V scale: D/2 bytes a block, D/16 a lane
-    uint32_t top = 0;
-    const uint8_t *vs = tile + (lane >> 3) * block_bytes(D) + 16 * D + D / 2 + (lane & 7) * (D / 16);
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-        const uint32_t w = reinterpret_cast<const uint32_t *>(vs)[i];
-        top = __vmaxu2(top, __vmaxu2(w & 0x00FF00FFu, (w >> 8) & 0x00FF00FFu));
-    }
-    top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
-    if (top != 255) {
-        add_values<D, NT, false>(tile, lane, top, p, keep, R);
-    } else {
-        top = 0;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) top = max(top, vs[i] == 255 ? 0u : (uint32_t)vs[i]);
-        top = __reduce_max_sync(0xffffffffu, top);
-        add_values<D, NT, true>(tile, lane, top, p, keep, R);
-    }
+    if (top < 256)
+        add_values<D, NT, false>(tile, fac, lane, p, R);
+    else
+        add_values<D, NT, true>(tile, fac, lane, p, R);
+    __syncwarp();  // before the factors of the next tile
 }
 
 // four channels of a row's result, and its lse
@@ -443,11 +500,13 @@ template <int D, int NT>
 __device__ __forceinline__ void end_rows(const AttnArgs &a, const Cursor &c, int group, int lane, Rows<D, NT> &R,
                                          bool whole, float *part) {
     const int g = lane >> 2, t = lane & 3;
-    const int head = c.seg / c.s.nrc, r0 = (c.seg % c.s.nrc) * 8 * NT, n = c.s.m * group;
+    const int head = c.head, r0 = c.chunk * 8 * NT, n = c.s.m * group;
+    const float back = v_factor(R.top);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+            const float m = R.m[nt][i] == -INFINITY ? -INFINITY : R.m[nt][i] * R.c[nt][i];
             float l = R.l[nt][i];
 #pragma unroll
             for (int o = 4; o <= 16; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -456,14 +515,15 @@ __device__ __forceinline__ void end_rows(const AttnArgs &a, const Cursor &c, int
             const int64_t row = whole ? row_index(a, c.s, head, group, r0 + r) : 0;
 #pragma unroll
             for (int G = 0; G < D / 32; ++G) {
-                const float4 o = make_float4(R.o[G][0][nt][i], R.o[G][0][nt][i + 2], R.o[G][1][nt][i], R.o[G][1][nt][i + 2]);
+                const float4 o = make_float4(R.o[G][0][nt][i] * back, R.o[G][0][nt][i + 2] * back,
+                                             R.o[G][1][nt][i] * back, R.o[G][1][nt][i + 2] * back);
                 if (whole)
-                    store_out(a, row, D, 32 * G + 4 * g, o, R.m[nt][i], l);
+                    store_out(a, row, D, 32 * G + 4 * g, o, m, l);
                 else
                     *reinterpret_cast<float4 *>(part + r * D + 32 * G + 4 * g) = o;
             }
             if (!whole && g == 0) {
-                part[8 * NT * D + r] = R.m[nt][i];
+                part[8 * NT * D + r] = m;
                 part[8 * NT * D + 8 * NT + r] = l;
             }
         }
@@ -497,7 +557,7 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 3 : 2) attn_split_kernel
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b) {
         const Seq s = load_seq<NT>(a, b, group);
-        mine += (int64_t)s.T * s.nrc * a.c.n_kv;
+        mine += s.units(a.c.n_kv);
         if (blockIdx.x == 0 && a.kv_lens[b] > s.len) atomicOr(a.status, PQE_STATUS_BAD_PAGE);
     }
     int64_t incl = mine;
@@ -522,7 +582,7 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 3 : 2) attn_split_kernel
         for (int b = b0; b < b1; ++b) {
             prefix[b] = at;
             const Seq s = load_seq<NT>(a, b, group);
-            at += (int64_t)s.T * s.nrc * a.c.n_kv;
+            at += s.units(a.c.n_kv);
         }
         if (tid == 0) prefix[a.B] = total;
     }
@@ -534,7 +594,7 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 3 : 2) attn_split_kernel
             int64_t at = before;
             for (int b = b0; b < b1; ++b) {
                 const Seq s = load_seq<NT>(a, b, group);
-                const int64_t n = (int64_t)s.T * s.nrc * a.c.n_kv;
+                const int64_t n = s.units(a.c.n_kv);
                 if (u < at + n) {
                     sm.start_b[w] = b;
                     sm.start_off[w] = u - at;
@@ -554,70 +614,75 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 3 : 2) attn_split_kernel
         Cursor c;  // of the tile at hand
         c.b = sm.start_b[warp];
         c.s = load_seq<NT>(a, c.b, group);
-        c.seg = (int)(sm.start_off[warp] / c.s.T);
-        c.tile = (int)(sm.start_off[warp] % c.s.T);
-        Cursor f = c;  // of the tile to fetch next
+        const int per_rows = c.s.T + OPEN, nth = (int)(sm.start_off[warp] / per_rows);
+        int skip = (int)(sm.start_off[warp] % per_rows) - OPEN;
+        c.head = nth / c.s.nrc;
+        c.chunk = nth % c.s.nrc;
+        c.tile = max(skip, 0);
+        int64_t u = u0 - min(skip, 0), fu = u;  // the unit at hand and the next one to fetch: never one of OPEN
+        Cursor f = c;
         const uint32_t ring = smem_u32(sm.ring[warp][0]), bar = smem_u32(&sm.full[warp][0]);
         uint32_t have[STAGES] = {};
-        int64_t fu = u0;
-#pragma unroll
-        for (int s = 0; s < STAGES; ++s)
-            if (fu < u1) {
-                have[s] = fetch<D>(a, f, ring + s * tile_bytes<D>(), bar + 8 * s, lane);
-                advance<NT>(a, f, group);
-                ++fu;
+        int page = fu < u1 ? table_entry(a, f, lane) : -1;
+        auto fetch_next = [&](int s) {
+            const uint32_t h = fetch<D>(a, f, page, ring + s * tile_bytes<D>(), bar + 8 * s, lane);
+            ++fu;
+            if (++f.tile == f.s.T) {
+                next_rows<NT>(a, f, group);
+                fu += OPEN;
             }
+            if (fu < u1) page = table_entry(a, f, lane);
+            return h;
+        };
+        if (fu < u1) have[0] = fetch_next(0);
+        if (fu < u1) have[1] = fetch_next(1);
         Rows<D, NT> R;
-        int from = c.tile;
         bool ok = true;
-        begin_rows<D, NT>(a, c, group, lane, R);
-        for (int64_t u = u0; u < u1; ++u) {
-            const int it = (int)(u - u0), s = it & 1;
-            if (ok && !mbar_wait(bar + 8 * s, (uint32_t)(it >> 1) & 1u, a.wait_limit)) ok = false;
-            ok = __all_sync(0xffffffffu, ok);
-            const int j0 = (c.s.t0 + c.tile) * TILE;
-            if (ok && j0 < R.max_hi)  // else no row of the chunk sees it
-                add_tile<D, NT>(sm.ring[warp][s], j0, s ? have[1] : have[0], lane, R);
-            __syncwarp();
-            if (ok && fu < u1) {
-                const uint32_t h = fetch<D>(a, f, ring + s * tile_bytes<D>(), bar + 8 * s, lane);
-                if (s)
-                    have[1] = h;
-                else
-                    have[0] = h;
-                advance<NT>(a, f, group);
-                ++fu;
+        int it = 0;
+        while (u < u1 && ok) {
+            // the tiles of one (sequence, head, rows)
+            begin_rows<D, NT>(a, c, group, lane, R);
+            const int from = c.tile, to = (int)min((int64_t)c.s.T, c.tile + (u1 - u));
+            for (; c.tile < to; ++c.tile, ++it) {
+                const int s = it & 1;
+                if (!mbar_wait(bar + 8 * s, (uint32_t)(it >> 1) & 1u, a.wait_limit)) ok = false;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const int j0 = (c.s.t0 + c.tile) * TILE;
+                if (j0 < R.max_hi)  // else no row of the chunk sees it
+                    add_tile<D, NT>(sm.ring[warp][s], sm.fac[warp], j0, s ? have[1] : have[0], lane, R);
+                if (fu < u1) {
+                    const uint32_t h = fetch_next(s);
+                    if (s)
+                        have[1] = h;
+                    else
+                        have[0] = h;
+                }
             }
-            const bool last = u + 1 == u1;
-            if (last || c.tile + 1 == c.s.T) {
-                const bool whole = from == 0 && c.tile + 1 == c.s.T;
-                float *part = nullptr;
-                if (!whole) {
-                    // the last piece stays in shared memory, in the ring that nothing is fetched into any more; an
-                    // earlier one, of which there is at most one, goes through memory
-                    const int k = last ? 1 : 0;
-                    part = last ? reinterpret_cast<float *>(sm.ring[warp][0])
-                                : scratch + ((size_t)blockIdx.x * WARPS + warp) * PART;
-                    if (lane == 0) {
-                        sm.seg_start[warp][k] = u - c.tile;
-                        sm.from[warp][k] = from;
-                        sm.to[warp][k] = c.tile + 1;
-                        sm.len_t[warp][k] = c.s.T;
-                        sm.b[warp][k] = c.b;
-                        sm.seg[warp][k] = c.seg;
-                        sm.ptr[warp][k] = part;
-                    }
+            const int64_t seg_start = u - from - OPEN;
+            u += to - from;
+            const bool ended = to == c.s.T, whole = from == 0 && ended;
+            if (ended) u += OPEN;
+            float *part = nullptr;
+            if (!whole) {
+                // the last piece stays in shared memory, in the ring that nothing is fetched into any more; an
+                // earlier one, of which there is at most one, goes through memory
+                const int k = u >= u1 ? 1 : 0;
+                part = k ? reinterpret_cast<float *>(sm.ring[warp][0]) : scratch + ((size_t)blockIdx.x * WARPS + warp) * PART;
+                if (lane == 0) {
+                    sm.seg_start[warp][k] = seg_start;
+                    sm.from[warp][k] = from;
+                    sm.to[warp][k] = to;
+                    sm.len_t[warp][k] = c.s.T;
+                    sm.b[warp][k] = c.b;
+                    sm.head[warp][k] = c.head;
+                    sm.chunk[warp][k] = c.chunk;
+                    sm.ptr[warp][k] = part;
                 }
                 __syncwarp();
-                end_rows<D, NT>(a, c, group, lane, R, whole, part);
-                if (!last) {
-                    advance<NT>(a, c, group);
-                    from = 0;
-                    begin_rows<D, NT>(a, c, group, lane, R);
-                }
-            } else {
-                ++c.tile;
             }
+            if (ok) end_rows<D, NT>(a, c, group, lane, R, whole, part);
+            if (u < u1) next_rows<NT>(a, c, group);
         }
         if (!ok) {
             // the copies in flight land before the block ends (bounded)
@@ -644,7 +709,7 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 3 : 2) attn_split_kernel
         }
         const bool whole = sm.from[w][k] == 0 && to == sm.len_t[w][k];
         const Seq s = load_seq<NT>(a, sm.b[w][k], group);
-        const int head = sm.seg[w][k] / s.nrc, r0 = (sm.seg[w][k] % s.nrc) * 8 * NT;
+        const int head = sm.head[w][k], r0 = sm.chunk[w][k] * 8 * NT;
         float *part = parts + ((size_t)blockIdx.x * 2 + (sm.seg_start[w][k] > cta0 ? 1 : 0)) * PART;
         for (int item = tid; item < 8 * NT * D / 4; item += WARPS * 32) {
             const int r = item / (D / 4), d = item % (D / 4) * 4;
@@ -674,65 +739,82 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 3 : 2) attn_split_kernel
     }
 }
 
-// One warp per (query token, head): joins the partials of a row that more than
-// one CTA took part in, in the order of the cache; and writes the rows of
-// sequences with no token to see.
+// One CTA per (query token, head): joins the partials of a row that more than
+// one CTA took part in; the warps take every fourth each, and the four sums
+// are added in order. Also writes the rows of sequences with no token to see.
+constexpr int JOIN_WARPS = 4;
 template <int D, int NT>
-__global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a, const uint8_t *ws, int split_ctas) {
+__global__ void __launch_bounds__(32 * JOIN_WARPS) attn_join_kernel(const AttnArgs a, const uint8_t *ws, int split_ctas) {
     constexpr int PART = part_floats(D, 8 * NT), E = D / 32;
-    pdl_acquire();
-    const int lane = threadIdx.x & 31, group = a.n_q / a.c.n_kv;
-    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row >= (int64_t)a.total_q * a.n_q) return;
+    __shared__ float sh_l[JOIN_WARPS];
+    __shared__ __align__(16) float sh_o[JOIN_WARPS][D];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = a.n_q / a.c.n_kv;
+    const int64_t row = blockIdx.x;
     const int tok = (int)(row / a.n_q), h = (int)(row % a.n_q);
-    // the last sequence that begins at or before the token (sequences without queries begin where the next does)
-    int lo = 0, hi = a.B;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (a.q_offsets[mid] <= tok)
-            lo = mid;
-        else
-            hi = mid;
+    // The call's own inputs were complete before the split kernel let this one start. The token's sequence: a guess that
+    // holds where all have the same number of tokens, else the last that begins at or before it (a sequence without
+    // tokens begins where the next one does).
+    int lo = (int)((int64_t)tok * a.B / a.total_q);
+    if (a.q_offsets[lo] > tok || a.q_offsets[lo + 1] <= tok) {
+        lo = 0;
+        int hi = a.B;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (a.q_offsets[mid] <= tok)
+                lo = mid;
+            else
+                hi = mid;
+        }
     }
     const Seq s = load_seq<NT>(a, lo, group);
+    pdl_acquire();
     if (tok < s.first || tok >= s.first + s.m) return;  // a row of no sequence
     if (s.T == 0) {
-        if (lane < D / 4) store_out(a, row, D, lane * 4, make_float4(0.f, 0.f, 0.f, 0.f), 0.f, 0.f);
+        if (threadIdx.x < D / 4)
+            store_out(a, row, D, threadIdx.x * 4, make_float4(0.f, 0.f, 0.f, 0.f), 0.f, 0.f);
         return;
     }
     const int64_t *prefix = reinterpret_cast<const int64_t *>(ws);
     const float *parts = reinterpret_cast<const float *>(ws + prefix_bytes(a.B));
     const int64_t total = prefix[a.B], n_cta = min((int64_t)split_ctas, (total + WARPS - 1) / WARPS);
     const int rr = (tok - s.first) * group + h % group, r = rr % (8 * NT);
-    const int64_t s0 = prefix[lo] + ((int64_t)(h / group) * s.nrc + rr / (8 * NT)) * s.T;
+    const int64_t s0 = prefix[lo] + ((int64_t)(h / group) * s.nrc + rr / (8 * NT)) * (s.T + OPEN);
     const int64_t nw = n_cta * WARPS;
-    const int64_t c0 = share_of(s0, nw, total) / WARPS, c1 = share_of(s0 + s.T - 1, nw, total) / WARPS;
+    const int c0 = (int)(share_of(s0 + OPEN, nw, total) / WARPS);
+    const int c1 = (int)(share_of(s0 + OPEN + s.T - 1, nw, total) / WARPS);
     if (c0 == c1) return;  // that CTA wrote it
     // the first CTA's partial is its second one if the row begins inside its share
-    const bool inside = s0 > share_start(c0 * WARPS, nw, total);
-    auto at = [&](int64_t c) { return parts + (size_t)(2 * c + (c == c0 && inside ? 1 : 0)) * PART; };
+    const bool inside = s0 > share_start((int64_t)c0 * WARPS, nw, total);
+    auto at = [&](int c) { return parts + (size_t)(2 * c + (c == c0 && inside ? 1 : 0)) * PART; };
     float m = -INFINITY;
-    for (int64_t c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, at(c)[8 * NT * D + r]);
+    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, at(c)[8 * NT * D + r]);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float base = m == -INFINITY ? 0.f : m;
     float o[E] = {}, l = 0.f;
 #pragma unroll 4
-    for (int64_t c = c0; c <= c1; ++c) {
+    for (int c = c0 + warp; c <= c1; c += JOIN_WARPS) {
         const float *p = at(c);
         const float f = exp2_approx(p[8 * NT * D + r] - base);
         l = fmaf(p[8 * NT * D + 8 * NT + r], f, l);
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = fmaf(p[r * D + lane * E + e], f, o[e]);
     }
-    const float inv = l == 0.f ? 0.f : 256.f / l;
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-        uint32_t u;
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(o[e + 1] * inv), "f"(o[e] * inv));
-        *reinterpret_cast<uint32_t *>(a.out + row * D + lane * E + e) = u;
+    for (int e = 0; e < E; ++e) sh_o[warp][lane * E + e] = o[e];
+    if (lane == 0) sh_l[warp] = l;
+    __syncthreads();
+    if (threadIdx.x < D / 4) {
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        l = 0.f;
+#pragma unroll
+        for (int w = 0; w < JOIN_WARPS; ++w) {
+            const float4 v = *reinterpret_cast<const float4 *>(&sh_o[w][threadIdx.x * 4]);
+            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+            l += sh_l[w];
+        }
+        store_out(a, row, D, threadIdx.x * 4, sum, m, l);
     }
-    if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l) - 8.f) * 0.693147180559945309f;
 }
 
 template <int D, int NT>
@@ -741,7 +823,7 @@ int launch(const AttnArgs &a, int max_q, int sms, void *ws, cudaStream_t s) {
     const int group = a.n_q / a.c.n_kv;
     const int64_t nrc = ((int64_t)max_q * group + 8 * NT - 1) / (8 * NT);
     const int64_t tiles = (((int64_t)a.max_pages << a.c.page_shift) + TILE - 1) / TILE;
-    const double most = (double)a.B * a.c.n_kv * nrc * tiles / WARPS + 1;
+    const double most = (double)a.B * a.c.n_kv * nrc * (tiles + OPEN) / WARPS + 1;
     int grid = sms * (NT == 1 ? 3 : 2);
     if (most < grid) grid = (int)most;
     static bool set[PQE_MAX_DEVICES] = {};
@@ -756,8 +838,7 @@ int launch(const AttnArgs &a, int max_q, int sms, void *ws, cudaStream_t s) {
     rc = launch_pdl(attn_split_kernel<D, NT>, dim3((unsigned)grid), dim3(WARPS * 32), smem, s, a,
                     static_cast<uint8_t *>(ws));
     if (rc != PQE_OK) return rc;
-    const int64_t rows = (int64_t)a.total_q * a.n_q;
-    return launch_pdl(attn_join_kernel<D, NT>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a,
+    return launch_pdl(attn_join_kernel<D, NT>, dim3((unsigned)((int64_t)a.total_q * a.n_q)), dim3(32 * JOIN_WARPS), 0, s, a,
                       static_cast<const uint8_t *>(ws), grid);
 }
 
