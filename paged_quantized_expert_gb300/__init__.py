@@ -12,7 +12,6 @@ PyTorch is used for device memory and streams only.
 from __future__ import annotations
 
 import ctypes as C
-import math
 import os
 from typing import Optional
 
@@ -214,8 +213,15 @@ def _ptr(t) -> Optional[int]:
     raise TypeError(f"cannot pass {type(t)} as a pointer")
 
 
+# The current stream's handle without the Stream object around it (3 us of a small call on the host); absent in a build
+# of torch without CUDA.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -330,22 +336,22 @@ def moe_combine(out_perm, inv, topk_w, T, k, H, y, stream=None):
 
 # ---- attention over a 4-bit paged cache, residual norm ---------------------------
 
-def _rows(t: torch.Tensor, inner: tuple) -> tuple[int, int]:
-    """Pointer and row stride (elements) of a bf16 tensor [n, *inner] whose rows are contiguous and may lie apart."""
-    if t.dtype not in (torch.bfloat16, torch.int16) or t.shape[1:] != inner:
-        raise ValueError(f"expected bf16 rows of shape {tuple(inner)}, got {t.dtype} {tuple(t.shape)}")
-    if t.is_contiguous():
-        return t.data_ptr(), math.prod(inner)
-    if not t[0].is_contiguous():
+def _rows(t: torch.Tensor, n: int, inner: tuple) -> tuple[int, int]:
+    """Pointer and row stride (elements) of bf16 rows [n, *inner], each contiguous, that may lie apart."""
+    if t.dtype is not torch.bfloat16 or t.shape != (n, *inner):
+        raise ValueError(f"expected bf16 rows of shape {(n, *inner)}, got {t.dtype} {tuple(t.shape)}")
+    if not (t.is_contiguous() or t[0].is_contiguous()):
         raise ValueError("each token's row must be contiguous")
-    return t.data_ptr(), t.stride(0)
+    return t.data_ptr(), t.stride(0) if n > 1 else t.numel()
 
 
-def _typed(t, dtype, name: str, n: int) -> int:
+def _typed(t: torch.Tensor, dtype, name: str, n: int) -> int:
     """Pointer of a contiguous tensor of this dtype with at least n elements."""
-    if t.dtype != dtype or t.numel() < n:
+    if t.dtype is not dtype or t.numel() < n:
         raise ValueError(f"{name}: expected at least {n} values of {dtype}, got {t.numel()} of {t.dtype}")
-    return _ptr(t)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def pqe_kv_page_bytes(page_size: int, n_kv: int, d: int) -> int:
@@ -375,12 +381,11 @@ def kv_cache_write(cache: pqe_kv_cache, k, v, slots, status, stream=None):
     """Quantise rows k, v [n, n_kv, d] (bf16; rows may lie apart, as in a fused projection) into the cache at slots
     (int64 [n]; negative: skip)."""
     n = k.shape[0]
-    if v.shape[0] != n:
-        raise ValueError("k and v differ in their number of tokens")
-    if n == 0:
+    if n == 0 and v.shape[0] == 0:
         return
-    kp, ks = _rows(k, (cache.n_kv, cache.d))
-    vp, vs = _rows(v, (cache.n_kv, cache.d))
+    row = (cache.n_kv, cache.d)
+    kp, ks = _rows(k, n, row)
+    vp, vs = _rows(v, n, row)
     _check("kv_cache_write", lib().kv_cache_write(C.byref(cache), kp, vp, ks, vs, _typed(slots, torch.int64, "slots", n),
                                                   n, _ptr(status), _stream(stream)))
 
@@ -390,9 +395,11 @@ def kv_cache_read(cache: pqe_kv_cache, slots, k, v, status, stream=None):
     n = slots.numel()
     if n == 0:
         return
-    outs = [None if t is None else _typed(t, torch.bfloat16, "k/v", n * cache.n_kv * cache.d) for t in (k, v)]
-    _check("kv_cache_read", lib().kv_cache_read(C.byref(cache), _typed(slots, torch.int64, "slots", n), n, outs[0],
-                                                outs[1], _ptr(status), _stream(stream)))
+    size = n * cache.n_kv * cache.d
+    kp = None if k is None else _typed(k, torch.bfloat16, "k", size)
+    vp = None if v is None else _typed(v, torch.bfloat16, "v", size)
+    _check("kv_cache_read", lib().kv_cache_read(C.byref(cache), _typed(slots, torch.int64, "slots", n), n, kp, vp,
+                                                _ptr(status), _stream(stream)))
 
 
 def kv_paged_attention_workspace_size(B: int, total_q: int, max_q: int, n_q: int, n_kv: int, d: int) -> int:
@@ -411,11 +418,11 @@ def kv_paged_attention(cache: pqe_kv_cache, q, q_offsets, kv_lens, block_table, 
         return
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [B, max_pages]")
-    qp, qs = _rows(q, (n_q, d))
+    qp, qs = _rows(q, total_q, (n_q, d))
+    i32 = torch.int32
     _check("kv_paged_attention", lib().kv_paged_attention(
-        C.byref(cache), qp, qs, _typed(q_offsets, torch.int32, "q_offsets", B + 1),
-        _typed(kv_lens, torch.int32, "kv_lens", B), _typed(block_table, torch.int32, "block_table", 0),
-        block_table.shape[1], B, total_q, max_q, n_q, scale, int(causal), window,
+        C.byref(cache), qp, qs, _typed(q_offsets, i32, "q_offsets", B + 1), _typed(kv_lens, i32, "kv_lens", B),
+        _typed(block_table, i32, "block_table", 0), block_table.shape[1], B, total_q, max_q, n_q, scale, int(causal), window,
         _typed(out, torch.bfloat16, "out", total_q * n_q * d),
         None if lse is None else _typed(lse, torch.float32, "lse", total_q * n_q), _ptr(ws), _nbytes(ws), _ptr(status),
         _stream(stream)))
@@ -427,18 +434,20 @@ def add_rms_norm(x, residual, weight, eps: float, sum_out, y, q=None, q_scale=No
     T, H = x.shape
     if T == 0:
         return
-    xp, xs = _rows(x, (H,))
-    if residual is not None and residual.shape != x.shape:
-        raise ValueError("x and residual differ in shape")
-    rp, rs = (None, 0) if residual is None else _rows(residual, (H,))
-    outs = [None if t is None else _typed(t, torch.bfloat16, "sum_out/y", T * H) for t in (sum_out, y)]
+    n = T * H
+    xp, xs = _rows(x, T, (H,))
+    rp, rs = (None, 0) if residual is None else _rows(residual, T, (H,))
+    sp = None if sum_out is None else _typed(sum_out, torch.bfloat16, "sum_out", n)
+    yp = None if y is None else _typed(y, torch.bfloat16, "y", n)
+    qp = cp = None
     if q is not None:
-        if q.element_size() != 1 or q.numel() < T * H:
+        if q.element_size() != 1 or q.numel() < n:
             raise ValueError("q must hold T * H bytes")
-        if q_scale is None or _nbytes(q_scale) < (4 * T if q_fmt == PQE_Q8_ROW else T * (H // 32)):
+        if q_scale is None or _nbytes(q_scale) < (4 * T if q_fmt == PQE_Q8_ROW else n // 32):
             raise ValueError("q_scale is missing or too small")
-    _check("add_rms_norm", lib().add_rms_norm(xp, xs, rp, rs, _typed(weight, torch.bfloat16, "weight", H), eps, T, H,
-                                              outs[0], outs[1], _ptr(q), _ptr(q_scale), q_fmt, _stream(stream)))
+        qp, cp = _ptr(q), _ptr(q_scale)
+    _check("add_rms_norm", lib().add_rms_norm(xp, xs, rp, rs, _typed(weight, torch.bfloat16, "weight", H), eps, T, H, sp, yp,
+                                              qp, cp, q_fmt, _stream(stream)))
 
 
 # ---- pager ---------------------------------------------------------------------

@@ -3,6 +3,16 @@
 
 #include "kv_attn.cuh"
 
+namespace pqe {
+namespace kv {
+
+// The split kernel takes 16 rows of a KV head at a time and reads the cache again for the next 16; the prompt kernel
+// takes 256 whatever their number. Sides measured below.
+static bool many_rows(int max_q, int group) { return (int64_t)max_q * group > 64; }
+
+}  // namespace kv
+}  // namespace pqe
+
 using namespace pqe;
 
 extern "C" {
@@ -32,6 +42,7 @@ int kv_paged_attention(const pqe_kv_cache *cache, const void *q, int64_t q_strid
     const kv::AttnArgs a{kv::cache_of(cache), static_cast<const uint16_t *>(q), q_stride, q_offsets, kv_lens,
                          block_table, max_pages, B, total_q, n_q, causal, window, scale * 1.44269504088896341f,
                          static_cast<uint16_t *>(out), lse, status, wait_limit()};
+    if (kv::many_rows(max_q, n_q / cache->n_kv)) return kv::attn_prompt(cache, a, as_stream(stream));
     return kv::attn_split(cache, a, max_q, sms, ws, as_stream(stream));
 }
 

@@ -78,6 +78,7 @@ __device__ __forceinline__ float v_factor(uint32_t r) {
 }
 
 int attn_split(const pqe_kv_cache *cache, const AttnArgs &a, int max_q, int sms, void *ws, cudaStream_t s);
+int attn_prompt(const pqe_kv_cache *cache, const AttnArgs &a, cudaStream_t s);
 size_t attn_split_ws(int B, int max_q, int group, int d);
 
 }  // namespace kv

@@ -1,0 +1,637 @@
+// kv_attn_prompt.cu -- attention over the 4-bit paged cache for many query rows
+// (prompt chunks) on the 5th-generation tensor cores.
+//
+// For one sequence and KV head the m * group query rows are cut into tiles of
+// 128; a CTA takes two of them and walks the tokens that they see, 128 at a
+// time. Per step and tile:
+//   S = Q . K^T       tcgen05 kind::f16, M = 128 rows, N = 128 tokens, into TMEM
+//   p = 2^(c S - ref + 8)   a row per thread, from TMEM to TMEM (f16, in S's place
+//                     where the head size leaves no other room)
+//   O += P . V        A from TMEM, N = d channels, fp32 in TMEM
+// The two tiles alternate, so that the tensor pipe works on one while the other's
+// softmax runs. The reference `ref` of a row follows its maximum only when
+// that has grown by 7 or more (p stays under 2^15, inside f16); O and the sum are
+// scaled then.
+//
+// Four warps turn codes into f16 in shared memory (128-byte swizzle, K-major
+// both): K as it lies, V transposed on the way, its tokens in the order in which
+// the cache's bytes hold them, which is the order P is written in. Codes are
+// multiplied by 2^(scale - top + 7) with top the largest scale that the CTA's
+// tokens have: exact while a scale is within 21 of it. Both tiles use what is
+// converted once.
+//
+// Bound by the tensor pipe (2 * 1024 clocks a step at d = 128) with the exponentials
+// and the conversions close behind on the issue slots.
+#include <math.h>
+
+#include "kv_attn.cuh"
+#include "tc_ptx.cuh"
+
+namespace pqe {
+namespace kv {
+namespace prompt {
+using namespace ptx;
+
+constexpr int BM = 128;           // rows of a tile
+constexpr int TILES = 2;          // tiles of a CTA
+constexpr int BK = 128;           // tokens of a step
+constexpr int SOFT_WARPS = 8;     // four per tile
+constexpr int CONV_WARPS = 4;
+constexpr int MMA_WARP = SOFT_WARPS + CONV_WARPS;
+constexpr int THREADS = 32 * (MMA_WARP + 1);
+constexpr int CHUNK = 128 * 128;  // bytes of 128 rows of 64 f16
+constexpr float LAZY = 7.f;       // growth of a maximum that its reference does not follow
+
+// TMEM columns
+__device__ __forceinline__ constexpr uint32_t s_col(int tile) { return 128 * tile; }
+__device__ __forceinline__ constexpr uint32_t o_col(int tile) { return 256 + 128 * tile; }
+template <int D>
+__device__ __forceinline__ constexpr uint32_t p_col(int tile) {  // P: half a column per token
+    return D == 128 ? s_col(tile) : o_col(tile) + 64;
+}
+
+template <int D>
+struct Smem {
+    alignas(1024) uint8_t q[TILES][D / 64][CHUNK];  // [128-byte rows of 64 channels]
+    uint8_t k[2][D / 64][CHUNK];
+    uint8_t v[2][2][D * 128];  // V^T: D rows of 64 tokens, two a step
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], drained;
+    uint32_t tmem;
+    int seq, tile;             // what the CTA works on
+    int k_top, v_top, v_nan;
+    // of a step's 16-token blocks, two bits from each converting warp: those that are there. Four steps' worth: a
+    // step's is rewritten only once the softmax of the step three before has ended.
+    alignas(4) uint8_t have[4][CONV_WARPS];
+};
+
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accum)
+        : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accum)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// f16 pair of 2^(x - top + 7), x an E8M0 byte; zero from 22 below top on
+__device__ __forceinline__ uint32_t weight(uint32_t x, int top) {
+    return (uint32_t)max((int)x - top + 22, 0) * (1024u * 0x10001u);
+}
+
+// 2^(top - 134): what a product with a weighted value lacks to the value's own
+__device__ __forceinline__ float unweight(int top) {
+    return __uint_as_float(top > 7 ? (uint32_t)(top - 7) << 23 : 1u << (top + 15));
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    Smem<D> &sm = *reinterpret_cast<Smem<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int group = a.n_q / a.c.n_kv, head = blockIdx.x % a.c.n_kv;
+    constexpr uint32_t IDESC_S = (1u << 4) | ((uint32_t)(BK >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+    constexpr uint32_t IDESC_O = (1u << 4) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sm.k_full[i]), CONV_WARPS);
+            mbar_init(smem_u32(&sm.v_full[i]), CONV_WARPS);
+            mbar_init(smem_u32(&sm.k_empty[i]), 1);
+            mbar_init(smem_u32(&sm.v_empty[i]), 1);
+            mbar_init(smem_u32(&sm.s_full[i]), 1);
+            mbar_init(smem_u32(&sm.p_full[i]), 4);
+            mbar_init(smem_u32(&sm.o_full[i]), 1);
+        }
+        mbar_init(smem_u32(&sm.drained), 1);
+        sm.seq = -1;
+        sm.k_top = sm.v_top = sm.v_nan = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    pdl_acquire();
+
+    // ---- this CTA's sequence and rows: tiles of all sequences in one line, the last first (they see the most) ----
+    if (warp == 0) {
+        int total = 0;
+        for (int b0 = 0; b0 < a.B; b0 += 32) {
+            int first, m = 0, len;
+            if (b0 + lane < a.B) sequence_of(a, b0 + lane, first, m, len);
+            total += __reduce_add_sync(0xffffffffu, (int)(((int64_t)m * group + BM * TILES - 1) / (BM * TILES)));
+        }
+        const int want = total - 1 - (int)(blockIdx.x / a.c.n_kv);
+        int before = 0;
+        for (int b0 = 0; want >= 0 && b0 < a.B; b0 += 32) {
+            int first, m = 0, len;
+            if (b0 + lane < a.B) sequence_of(a, b0 + lane, first, m, len);
+            const int n = (int)(((int64_t)m * group + BM * TILES - 1) / (BM * TILES));
+            int incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += up;
+            }
+            if (want >= before + incl - n && want < before + incl) {
+                sm.seq = b0 + lane;
+                sm.tile = want - (before + incl - n);
+            }
+            before += __shfl_sync(0xffffffffu, incl, 31);
+            if (before > want) break;
+        }
+    }
+    __syncthreads();
+    const int b = sm.seq;
+    if (b < 0) return;
+    int first, m, len;
+    sequence_of(a, b, first, m, len);
+    if (a.kv_lens[b] > len && tid == 0) atomicOr(a.status, PQE_STATUS_BAD_PAGE);
+    const int row0 = sm.tile * (BM * TILES), n_rows = m * group;
+    const int tiles = row0 + BM < n_rows ? 2 : 1;
+    // the tokens that some row of the CTA sees
+    int lo, hi, lo_last, hi_last;
+    visible(a, row0 / group, m, len, lo, hi);
+    visible(a, (min(row0 + BM * TILES, n_rows) - 1) / group, m, len, lo_last, hi_last);
+    const int k_first = lo / BK * BK, k_end = max(hi_last, 0);
+    const int steps = k_end > k_first ? (k_end - k_first + BK - 1) / BK : 0;
+    const int32_t *table = a.block_table + (size_t)b * a.max_pages;
+    const int page_mask = (1 << a.c.page_shift) - 1;
+
+    // ---- the largest K and V scales among those tokens ----
+    {
+        int kt = 0, vt = 0, nan = 0;
+        constexpr int PIECES = D / 16;  // 16-byte pieces of a block's scales: K's, then V's
+        const int n_blk = (k_end - k_first + BLOCK - 1) / BLOCK;
+        for (int i = tid; i < n_blk * PIECES; i += THREADS) {
+            const int j = k_first + i / PIECES * BLOCK, piece = i % PIECES;
+            if (j + BLOCK <= lo) continue;  // before the window: its page may be gone
+            const int page = table[j >> a.c.page_shift];
+            if (page < 0 || page >= a.c.n_pages) {
+                atomicOr(a.status, PQE_STATUS_BAD_PAGE);
+                continue;
+            }
+            const uint4 u = *reinterpret_cast<const uint4 *>(block_of<D>(a.c, page, j & page_mask, head) + 16 * D + 16 * piece);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+            const bool is_v = piece >= PIECES / 2;
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+                // the token that the byte belongs to: K [token][G], V [t][G][j]
+                const int at = (piece % (PIECES / 2)) * 16 + x;
+                const int tok = is_v ? 2 * (at / (D / 8)) + (x & 1) + 8 * (x >> 1 & 1) : at / (D / 32);
+                const int s = j + tok < k_end ? (int)(w[x >> 2] >> (8 * (x & 3)) & 255u) : 0;
+                if (s == 255)
+                    nan |= is_v;
+                else if (is_v)
+                    vt = max(vt, s);
+                else
+                    kt = max(kt, s);
+            }
+        }
+        kt = __reduce_max_sync(0xffffffffu, kt);
+        vt = __reduce_max_sync(0xffffffffu, vt);
+        nan = __reduce_or_sync(0xffffffffu, nan);
+        if (lane == 0) {
+            atomicMax(&sm.k_top, kt);
+            atomicMax(&sm.v_top, vt);
+            if (nan) atomicOr(&sm.v_nan, 1);
+        }
+    }
+    if (warp == MMA_WARP) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem)), "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    const int k_top = sm.k_top, v_top = sm.v_top;
+
+    if (warp < SOFT_WARPS) {
+        // ================= softmax: a row per thread =================
+        const int tile = warp >> 2, r = tid & (BM - 1), row = row0 + tile * BM + r;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const bool valid = row < n_rows;
+        const int64_t out_row = (int64_t)(first + row / group) * a.n_q + head * group + row % group;
+        int my_lo = 0, my_hi = 0;
+        float c = 1.f;
+        if (tile < tiles) {
+            // the row to f16, scaled by a power of two
+            uint4 raw[D / 8];
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+            if (valid) {
+                visible(a, row / group, m, len, my_lo, my_hi);
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (int64_t)(first + row / group) * a.q_stride +
+                                                                   (head * group + row % group) * D);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) raw[i] = src[i];
+            }
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) top = max(top, max(w[x] & 0x7FFFu, w[x] >> 16 & 0x7FFFu));
+            }
+            float f, inv;
+            q_factor(top, f, inv);
+            c = fabsf(a.scale) * inv * unweight(k_top);
+            if (a.scale < 0.f) f = -f;
+            if (c == 0.f) c = 1e-38f;                             // scores of (next to) zero, and no 0 * infinity
+            if (top >= 0x7F80u) f = __uint_as_float(0x7FC00000u);  // a row that is not finite: scores of NaN
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                uint32_t o[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    o[x] = pack_f16(__uint_as_float(w[x] << 16) * f, __uint_as_float(w[x] & 0xFFFF0000u) * f);
+                *reinterpret_cast<uint4 *>(&sm.q[tile][i >> 3][r * 128 + (((i & 7) ^ (r & 7)) << 4)]) =
+                    make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        }
+        fence_async();
+        __syncthreads();  // (1) Q is there
+        if (tile < tiles) {
+            float ref = -INFINITY, l = 0.f;  // exponents of two; l: 2^8 times the sum
+            bool ok = true;
+            for (int it = 0; it < steps; ++it) {
+                if (!mbar_wait(smem_u32(&sm.s_full[tile]), it & 1, a.wait_limit)) ok = false;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const int k0 = k_first + it * BK;
+                const uint32_t s_at = tmem + lanes + s_col(tile), p_at = tmem + lanes + p_col<D>(tile);
+                const uint32_t have = *reinterpret_cast<const volatile uint32_t *>(sm.have[it & 3]);
+                const bool all = __all_sync(0xffffffffu, !valid || (k0 + BK <= my_hi && k0 >= my_lo)) && have == 0x03030303u;
+                // pass 1: the maximum
+                float top = -INFINITY;
+#pragma unroll
+                for (int ch = 0; ch < BK / 32; ++ch) {
+                    uint32_t s[32];
+                    tmem_ld32(s_at + 32 * ch, s);
+                    tmem_ld_wait();
+                    if (all) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(s[i]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int j = k0 + 32 * ch + i;
+                            if (j < my_hi && j >= my_lo && (have >> (8 * ch + (i >> 4)) & 1)) top = fmaxf(top, __uint_as_float(s[i]));
+                        }
+                    }
+                }
+                const float e = top == -INFINITY ? -INFINITY : top * c;
+                // the reference follows a maximum that has outgrown it; O and the sum with it
+                const bool grow = e > ref + LAZY || (ref == -INFINITY && e > ref);
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float keep = grow ? exp2_approx(ref - e) : 1.f;
+                    if (grow) ref = e;
+                    l *= keep;
+                    if (it > 0) {
+#pragma unroll
+                        for (int ch = 0; ch < D / 32; ++ch) {
+                            uint32_t o[32];
+                            tmem_ld32(tmem + lanes + o_col(tile) + 32 * ch, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                            tmem_st32(tmem + lanes + o_col(tile) + 32 * ch, o);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+                // pass 2: the probabilities
+                const float base = ref == -INFINITY ? 0.f : 8.f - ref;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ch = 0; ch < BK / 32; ++ch) {
+                    uint32_t s[32];
+                    tmem_ld32(s_at + 32 * ch, s);
+                    tmem_ld_wait();
+                    float p[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) p[i] = exp2_approx(fmaf(__uint_as_float(s[i]), c, base));
+                    if (!all) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int j = k0 + 32 * ch + i;
+                            if (!(j < my_hi && j >= my_lo && (have >> (8 * ch + (i >> 4)) & 1))) p[i] = 0.f;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) sum[i & 3] += p[i];
+                    // in the order of V^T's columns: t, block of the pair, tokens 2t, 2t+1, 2t+8, 2t+9
+                    uint32_t o[16];
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        const int j = (x >> 1 & 1) * 16 + (x & 1) * 8 + (x >> 2) * 2;
+                        o[x] = pack_f16(p[j], p[j + 1]);
+                    }
+                    tmem_st16(p_at + 16 * ch, o);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_plain(smem_u32(&sm.p_full[tile]));
+            }
+            // ---- the rows' results ----
+            if (ok && steps > 0) {
+                if (!mbar_wait(smem_u32(&sm.o_full[tile]), 0, a.wait_limit)) ok = false;
+                ok = __all_sync(0xffffffffu, ok);
+            }
+            if (!ok) {
+                if (lane == 0) atomicOr(a.status, PQE_STATUS_TIMEOUT);
+            } else {
+                tc_fence_after();
+                uint32_t nan = 0;  // blocks of channels where the row sees a NaN
+                if (sm.v_nan && valid) {
+                    for (int j = my_lo; j < my_hi; ++j) {
+                        const int page = table[j >> a.c.page_shift];
+                        if (page < 0 || page >= a.c.n_pages) continue;
+                        const uint8_t *blk = block_of<D>(a.c, page, j & page_mask, head);
+#pragma unroll
+                        for (int G = 0; G < D / 32; ++G) nan |= (blk[v_scale<D>(j & 15, G)] == 255 ? 1u : 0u) << G;
+                    }
+                }
+                const float inv = l == 0.f ? 0.f : unweight(v_top) / l;
+#pragma unroll
+                for (int ch = 0; ch < D / 32; ++ch) {
+                    uint32_t o[32];
+                    if (steps > 0) {
+                        tmem_ld32(tmem + lanes + o_col(tile) + 32 * ch, o);
+                        tmem_ld_wait();
+                    }
+                    if (valid) {
+                        const float f = nan >> ch & 1 ? __uint_as_float(0x7FC00000u) : inv;
+                        uint4 *dst = reinterpret_cast<uint4 *>(a.out + out_row * D + 32 * ch);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            uint32_t u[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const int i = 8 * x + 2 * y;
+                                const float v0 = l == 0.f ? 0.f : __uint_as_float(o[i]) * f;
+                                const float v1 = l == 0.f ? 0.f : __uint_as_float(o[i + 1]) * f;
+                                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[y]) : "f"(v1), "f"(v0));
+                            }
+                            dst[x] = make_uint4(u[0], u[1], u[2], u[3]);
+                        }
+                    }
+                }
+                if (valid && a.lse) a.lse[out_row] = l == 0.f ? -INFINITY : (ref + log2f(l) - 8.f) * 0.693147180559945309f;
+            }
+        }
+    } else if (warp < MMA_WARP) {
+        // ================= conversion: warp w takes a step's blocks 2w and 2w + 1 =================
+        __syncthreads();  // (1)
+        const int w = warp - SOFT_WARPS;
+        constexpr int NK = D / 32;  // 16-byte pieces of K a thread takes
+        constexpr int NV = D / 64;  // planes of V
+        uint4 kr[NK], vr[NV][2];
+        uint32_t ks[NK], vs[NV][2][2];
+        int pages[2];
+        auto look = [&](int it) {  // table entries of the warp's two blocks
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int j = k_first + it * BK + (2 * w + i) * BLOCK;
+                pages[i] = j < k_end && j + BLOCK > lo ? table[j >> a.c.page_shift] : -1;
+            }
+        };
+        // a K piece's token: rows 0..7 of a block to a warp's lanes so that a quarter warp's stores meet eight banks
+        const int g = lane >> 2, t = lane & 3;
+        const int tok8 = ((lane >> 2) & 1) * 4 + (lane >> 3);  // D = 128: 8 tokens x 4 pieces of 16 bytes
+        const int tok16 = ((lane >> 1) & 1) * 4 + ((lane >> 2) & 3) + (lane >> 4) * 8;  // D = 64: 16 tokens x 2 pieces
+        auto load = [&](int it) -> uint32_t {
+            uint32_t have = 0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int j = k_first + it * BK + (2 * w + i) * BLOCK;
+                const bool in = pages[i] >= 0 && pages[i] < a.c.n_pages;
+                if (in) have |= 1u << i;
+                const uint8_t *blk = block_of<D>(a.c, in ? pages[i] : 0, in ? j & page_mask : 0, head);
+                const int left = k_end - j;  // tokens of the block that count
+                if constexpr (D == 128) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int tok = tok8 + 8 * h;
+                        kr[2 * i + h] = *reinterpret_cast<const uint4 *>(blk + tok * 64 + t * 16);
+                        ks[2 * i + h] = *reinterpret_cast<const uint32_t *>(blk + 16 * D + tok * 4);
+                    }
+                } else {
+                    kr[i] = *reinterpret_cast<const uint4 *>(blk + tok16 * 32 + (lane & 1) * 16);
+                    ks[i] = *reinterpret_cast<const uint16_t *>(blk + 16 * D + tok16 * 2);
+                }
+#pragma unroll
+                for (int q2 = 0; q2 < NV; ++q2) {
+                    vr[q2][i] = *reinterpret_cast<const uint4 *>(blk + 8 * D + q2 * 512 + lane * 16);
+                    const uint2 s = *reinterpret_cast<const uint2 *>(blk + 16 * D + D / 2 + t * (D / 8) + q2 * 8);
+                    vs[q2][i][0] = s.x;
+                    vs[q2][i][1] = s.y;
+                }
+                if (!in || left < BLOCK) {
+                    // tokens that are not there: V of zero (bytes of scale 0, codes 0)
+                    const uint32_t tk[4] = {2u * t, 2u * t + 1, 2u * t + 8, 2u * t + 9};
+                    uint32_t keep = 0;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) keep |= (in && (int)tk[x] < left ? 0xFFu : 0u) << (8 * x);
+#pragma unroll
+                    for (int q2 = 0; q2 < NV; ++q2) {
+                        vs[q2][i][0] &= keep;
+                        vs[q2][i][1] &= keep;
+                        uint4 &v = vr[q2][i];
+                        v = make_uint4(keep & 1u ? v.x : 0u, keep & 0x100u ? v.y : 0u, keep & 0x10000u ? v.z : 0u,
+                                       keep & 0x1000000u ? v.w : 0u);
+                    }
+                }
+            }
+            return have;
+        };
+        bool ok = true;
+        uint32_t have = 0;
+        if (steps > 0) {
+            look(0);
+            have = load(0);
+            if (steps > 1) look(1);
+        }
+        for (int it = 0; it < steps; ++it) {
+            const int s = it & 1;
+            const uint32_t parity = ((uint32_t)(it >> 1) & 1u) ^ 1u;
+            if (!mbar_wait(smem_u32(&sm.k_empty[s]), parity, a.wait_limit)) ok = false;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            // K: eight codes of a word are 16 bytes of a row
+#pragma unroll
+            for (int p = 0; p < NK; ++p) {
+                const uint32_t wd[4] = {kr[p].x, kr[p].y, kr[p].z, kr[p].w};
+                const int tok = D == 128 ? (2 * w + (p >> 1)) * BLOCK + tok8 + 8 * (p & 1) : (2 * w + p) * BLOCK + tok16;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int G = D == 128 ? x : x & 1, piece = D == 128 ? t : 2 * (lane & 1) + (x >> 1);
+                    const uint32_t sb = ks[p] >> (8 * G) & 255u;
+                    const uint32_t f = sb == 255u ? 0x7E007E00u : weight(sb, k_top);
+                    uint32_t h[4];
+                    e2m1x8_to_f16(wd[x], h);
+                    *reinterpret_cast<uint4 *>(&sm.k[s][G >> 1][tok * 128 + ((((G & 1) * 4 + piece) ^ (tok & 7)) << 4)]) =
+                        make_uint4(mul_f16x2(h[0], f), mul_f16x2(h[1], f), mul_f16x2(h[2], f), mul_f16x2(h[3], f));
+                }
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) {
+                *(volatile uint8_t *)&sm.have[it & 3][w] = (uint8_t)have;
+                mbar_arrive_plain(smem_u32(&sm.k_full[s]));
+            }
+            if (!mbar_wait(smem_u32(&sm.v_empty[s]), parity, a.wait_limit)) ok = false;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            // V: four tokens a block and eight channels a thread; two blocks make 16 bytes of a channel's row
+#pragma unroll
+            for (int q2 = 0; q2 < NV; ++q2) {
+                uint32_t c0[2][4], c1[2][4], c2[2][4], c3[2][4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint4 v = vr[q2][i];
+                    e2m1x8_to_f16((v.x & 0x0F0F0F0Fu) | ((v.y << 4) & 0xF0F0F0F0u), c0[i]);
+                    e2m1x8_to_f16(((v.x >> 4) & 0x0F0F0F0Fu) | (v.y & 0xF0F0F0F0u), c1[i]);
+                    e2m1x8_to_f16((v.z & 0x0F0F0F0Fu) | ((v.w << 4) & 0xF0F0F0F0u), c2[i]);
+                    e2m1x8_to_f16(((v.z >> 4) & 0x0F0F0F0Fu) | (v.w & 0xF0F0F0F0u), c3[i]);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t f[2][2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const uint32_t x = vs[q2][i][h] >> (16 * y), b0 = x & 255u, b1 = x >> 8 & 255u;
+                            f[i][y] = ((b0 == 255u ? 0u : weight(b0, v_top)) & 0xFFFFu) |
+                                      ((b1 == 255u ? 0u : weight(b1, v_top)) & 0xFFFF0000u);
+                        }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int d = 64 * q2 + 32 * h + 4 * g + e, x = 2 * h + (e >> 1);
+                        const uint4 o = make_uint4(
+                            mul_f16x2(e & 1 ? c1[0][x] : c0[0][x], f[0][0]), mul_f16x2(e & 1 ? c3[0][x] : c2[0][x], f[0][1]),
+                            mul_f16x2(e & 1 ? c1[1][x] : c0[1][x], f[1][0]), mul_f16x2(e & 1 ? c3[1][x] : c2[1][x], f[1][1]));
+                        *reinterpret_cast<uint4 *>(&sm.v[s][w >> 1][d * 128 + ((((w & 1) * 4 + t) ^ (d & 7)) << 4)]) = o;
+                    }
+                }
+            }
+            if (it + 1 < steps) {
+                have = load(it + 1);
+                if (it + 2 < steps) look(it + 2);
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_plain(smem_u32(&sm.v_full[s]));
+        }
+        if (!ok && lane == 0) atomicOr(a.status, PQE_STATUS_TIMEOUT);
+    } else {
+        // ================= MMA =================
+        __syncthreads();  // (1)
+        if (lane == 0 && steps > 0) {
+            tc_fence_after();
+            bool ok = true;
+            auto wait = [&](uint64_t &bar, uint32_t parity) {
+                if (ok && !mbar_wait(smem_u32(&bar), parity, a.wait_limit)) ok = false;
+                tc_fence_after();
+                return ok;
+            };
+            auto scores = [&](int tile, int s) {
+                const uint32_t q = smem_u32(sm.q[tile][0]), k = smem_u32(sm.k[s][0]);
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x)
+                    umma_ss(tmem + s_col(tile), sw128_desc(q + (x >> 2) * CHUNK + (x & 3) * 32),
+                            sw128_desc(k + (x >> 2) * CHUNK + (x & 3) * 32), IDESC_S, x != 0);
+                umma_commit(smem_u32(&sm.s_full[tile]));
+            };
+            if (wait(sm.k_full[0], 0)) {
+                for (int tile = 0; tile < tiles; ++tile) scores(tile, 0);
+                umma_commit(smem_u32(&sm.k_empty[0]));
+            }
+            for (int it = 0; it < steps && ok; ++it) {
+                const int s = it & 1;
+                const bool more = it + 1 < steps;
+                if (!wait(sm.v_full[s], (uint32_t)(it >> 1) & 1u)) break;
+                for (int tile = 0; tile < tiles; ++tile) {
+                    if (!wait(sm.p_full[tile], it & 1)) break;
+                    const uint32_t v = smem_u32(sm.v[s][0]);
+#pragma unroll
+                    for (int x = 0; x < BK / 16; ++x)
+                        umma_ts(tmem + o_col(tile), tmem + p_col<D>(tile) + 8 * x,
+                                sw128_desc(v + (x >> 2) * (D * 128) + (x & 3) * 32), IDESC_O, (it | x) != 0);
+                    if (more) {
+                        if (tile == 0 && !wait(sm.k_full[s ^ 1], (uint32_t)((it + 1) >> 1) & 1u)) break;
+                        scores(tile, s ^ 1);
+                    } else {
+                        umma_commit(smem_u32(&sm.o_full[tile]));
+                    }
+                }
+                if (!ok) break;
+                umma_commit(smem_u32(&sm.v_empty[s]));
+                if (more) umma_commit(smem_u32(&sm.k_empty[s ^ 1]));
+            }
+            // every MMA has finished before TMEM is released
+            umma_commit(smem_u32(&sm.drained));
+            if (!mbar_wait(smem_u32(&sm.drained), 0, a.wait_limit)) ok = false;
+            if (!ok) atomicOr(a.status, PQE_STATUS_TIMEOUT);
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == MMA_WARP)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+template <int D>
+int launch(const AttnArgs &a, cudaStream_t s) {
+    static bool set[PQE_MAX_DEVICES] = {};
+    int dev = 0, n = 0;
+    const int rc = device_info(dev, n);
+    if (rc != PQE_OK) return rc;
+    constexpr int smem = (int)sizeof(Smem<D>) + 1024;
+    if (!set[dev]) {
+        PQE_CUDA_TRY(cudaFuncSetAttribute(attn_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+        set[dev] = true;
+    }
+    // no sequence has more tiles than its rows fill, and one that they do not: a bound that needs no lengths here
+    const int64_t ctas = ((int64_t)a.total_q * (a.n_q / a.c.n_kv) / (BM * TILES) + a.B) * a.c.n_kv;
+    PQE_CHECK_ARG(ctas <= INT32_MAX);
+    return launch_pdl(attn_prompt_kernel<D>, dim3((unsigned)ctas), dim3(THREADS), smem, s, a);
+}
+
+}  // namespace prompt
+
+int attn_prompt(const pqe_kv_cache *cache, const AttnArgs &a, cudaStream_t s) {
+    return cache->d == 128 ? prompt::launch<128>(a, s) : prompt::launch<64>(a, s);
+}
+
+}  // namespace kv
+}  // namespace pqe

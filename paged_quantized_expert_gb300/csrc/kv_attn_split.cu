@@ -78,7 +78,7 @@ constexpr int OPEN = 1;
 
 // a sequence's part of the line of work
 struct Seq {
-    int first, m, len, t0, T, nrc;
+    int first, m, len, lo, t0, T, nrc;  // lo: the first token that any of its queries sees
     __device__ __forceinline__ int64_t units(int n_kv) const { return T > 0 ? (int64_t)(T + OPEN) * nrc * n_kv : 0; }
 };
 template <int NT>
@@ -86,9 +86,9 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs &a, int b, int group) {
     Seq s;
     sequence_of(a, b, s.first, s.m, s.len);
     s.nrc = (s.m * group + 8 * NT - 1) / (8 * NT);
-    int lo, hi;
-    visible(a, 0, s.m, s.len, lo, hi);
-    s.t0 = min(lo, s.len) / TILE;
+    int hi;
+    visible(a, 0, s.m, s.len, s.lo, hi);
+    s.t0 = min(s.lo, s.len) / TILE;
     s.T = s.m > 0 ? (s.len + TILE - 1) / TILE - s.t0 : 0;
     return s;
 }
@@ -147,9 +147,10 @@ __device__ __forceinline__ int tile_blocks(const Cursor &c) {
 
 // The table entry that this lane's copy of the cursor's tile needs. Asked for a tile early, so that fetch() does not wait.
 __device__ __forceinline__ int table_entry(const AttnArgs &a, const Cursor &c, int lane) {
-    const int blk = lane << blocks_shift(a);
+    const int blk = lane << blocks_shift(a), j = (c.s.t0 + c.tile) * TILE + blk * BLOCK;
     if (blk >= tile_blocks(c)) return -1;
-    return a.block_table[(size_t)c.b * a.max_pages + (((c.s.t0 + c.tile) * TILE + blk * BLOCK) >> a.c.page_shift)];
+    if (j + (BLOCK << blocks_shift(a)) <= c.s.lo) return -2;  // before the window: the page may be gone
+    return max(a.block_table[(size_t)c.b * a.max_pages + (j >> a.c.page_shift)], -1);
 }
 
 // Starts the copies of the cursor's tile into a stage; returns the bit mask of
@@ -168,7 +169,7 @@ __device__ __forceinline__ uint32_t fetch(const AttnArgs &a, const Cursor &c, in
             src = block_of<D>(a.c, page, j & ((1 << a.c.page_shift) - 1), c.head);
             bytes = n * block_bytes(D);
             mask = ((1u << n) - 1) << blk;
-        } else {
+        } else if (page != -2) {
             atomicOr(a.status, PQE_STATUS_BAD_PAGE);
         }
     }

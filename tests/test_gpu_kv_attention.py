@@ -321,3 +321,29 @@ def test_max_q_only_chooses_the_kernel(cuda_lib):
     for max_q in (40, 1000):
         out, lse = c.run(max_q=max_q)
         compare(out, lse, o, a, l)
+
+
+@pytest.mark.parametrize("m", [1, 4, 100])
+def test_pages_before_the_window_may_be_gone(cuda_lib, m):
+    c = Case(cuda_lib, [m, m], [700, 333], 8, 2, 128, 16)
+    want, _ = c.run(window=50)
+    c.table[0, :(700 - m - 50 + 1) // 16] = -1
+    c.table[1, :(333 - m - 50 + 1) // 16] = 1 << 29
+    c.check(window=50)
+    out, _ = c.run(window=50)
+    assert torch.equal(out, want) and c.status.item() == 0
+
+
+def test_few_and_many_rows_agree(cuda_lib):
+    """The same queries as one call of 40 a sequence and as calls of one: two kernels, one bound."""
+    c = Case(cuda_lib, [40, 40], [300, 70], 8, 2, 64, 16)
+    o, a, l = ref.attend(c.q, c.ms, c.lens, c.kv(), c.scale)
+    out, lse = c.run()
+    compare(out, lse, o, a, l, floor(c.kv()))
+    single = Case(cuda_lib, [1, 1], [300, 70], 8, 2, 64, 16)
+    for i in (0, 17, 39):
+        single.q = c.q[[i, 40 + i]].contiguous()
+        single.kv_lens.copy_(torch.tensor([300 - 39 + i, 70 - 39 + i]))
+        single.mem, single.cache, single.table = c.mem, c.cache, c.table
+        got, gl = single.run()
+        compare(got, gl, o[[i, 40 + i]], a[[i, 40 + i]], l[[i, 40 + i]], floor(c.kv()))
