@@ -38,7 +38,11 @@ constexpr int BK = 128;           // tokens of a step
 constexpr int SOFT_WARPS = 8;     // four per tile
 constexpr int CONV_WARPS = 4;
 constexpr int MMA_WARP = SOFT_WARPS + CONV_WARPS;
-constexpr int THREADS = 32 * (MMA_WARP + 1);
+constexpr int THREADS = 32 * (MMA_WARP + 4);  // the last warpgroup holds the MMA warp alone
+// registers a thread, by warpgroup: the softmax warps take what the others give up of the 128 each that 512 threads are
+// launched with
+constexpr int LAUNCH_REGS = 128, SOFT_REGS = 168, CONV_REGS = 112, MMA_REGS = 64;
+static_assert((2 * SOFT_REGS + CONV_REGS + MMA_REGS) * 128 <= LAUNCH_REGS * THREADS, "above the launch's total");
 constexpr int CHUNK = 128 * 128;  // bytes of 128 rows of 64 f16
 constexpr float LAZY = 7.f;       // growth of a maximum that its reference does not follow
 
@@ -64,17 +68,34 @@ struct Smem {
     alignas(4) uint8_t have[4][CONV_WARPS];
 };
 
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+// One lane issues (`leader`), but all of its warp runs the code around it: descriptors then stay in uniform registers,
+// where the instruction takes them from. (With the loop inside a branch of one lane an MMA took some 130 clocks to issue.)
+template <bool ACCUM>
+__device__ __forceinline__ void umma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accum)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t@q tcgen05.mma.cta_group::1.kind::f16 "
+        "[%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "n"(ACCUM ? 1 : 0), "r"(leader)
         : "memory");
 }
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+__device__ __forceinline__ void umma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accum)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t@q tcgen05.mma.cta_group::1.kind::f16 "
+        "[%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accum), "r"(leader)
         : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t leader, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 "
+        "[%0];\n\t}" ::"r"(bar),
+        "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t elect() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
@@ -93,6 +114,38 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float &x, float &y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -230,6 +283,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
     const int k_top = sm.k_top, v_top = sm.v_top;
 
     if (warp < SOFT_WARPS) {
+        more_registers<SOFT_REGS>();
         // ================= softmax: a row per thread =================
         const int tile = warp >> 2, r = tid & (BM - 1), row = row0 + tile * BM + r;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -287,74 +341,122 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
                 const uint32_t s_at = tmem + lanes + s_col(tile), p_at = tmem + lanes + p_col<D>(tile);
                 const uint32_t have = *reinterpret_cast<const volatile uint32_t *>(sm.have[it & 3]);
                 const bool all = __all_sync(0xffffffffu, !valid || (k0 + BK <= my_hi && k0 >= my_lo)) && have == 0x03030303u;
-                // pass 1: the maximum
-                float top = -INFINITY;
+                bool done = false;
+                if (all && __all_sync(0xffffffffu, ref != -INFINITY)) {
+                    // Every token is seen, and the reference will most likely stand: one pass, the probabilities held
+                    // back until the maximum is known.
+                    uint32_t p[BK / 2], s[2][32];
+                    const uint64_t c2 = pair(c, c), base2 = pair(8.f - ref, 8.f - ref);
+                    uint64_t sum2[2] = {0, 0};
+                    float top0 = -INFINITY, top1 = -INFINITY;
+                    tmem_ld32(s_at, s[0]);
 #pragma unroll
-                for (int ch = 0; ch < BK / 32; ++ch) {
-                    uint32_t s[32];
-                    tmem_ld32(s_at + 32 * ch, s);
-                    tmem_ld_wait();
-                    if (all) {
+                    for (int ch = 0; ch < BK / 32; ++ch) {
+                        tmem_ld_wait();
+                        if (ch + 1 < BK / 32) tmem_ld32(s_at + 32 * (ch + 1), s[(ch + 1) & 1]);
+                        const uint32_t(&u)[32] = s[ch & 1];
+                        float e[32];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(s[i]));
-                    } else {
+                        for (int i = 0; i < 32; i += 4) {
+                            const float s0 = __uint_as_float(u[i]), s1 = __uint_as_float(u[i + 1]);
+                            const float s2 = __uint_as_float(u[i + 2]), s3 = __uint_as_float(u[i + 3]);
+                            top0 = max3(top0, s0, s1);
+                            top1 = max3(top1, s2, s3);
+                            unpair(fma2(pair(s0, s1), c2, base2), e[i], e[i + 1]);
+                            unpair(fma2(pair(s2, s3), c2, base2), e[i + 2], e[i + 3]);
+                        }
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int j = k0 + 32 * ch + i;
-                            if (j < my_hi && j >= my_lo && (have >> (8 * ch + (i >> 4)) & 1)) top = fmaxf(top, __uint_as_float(s[i]));
+                        for (int i = 0; i < 32; ++i) e[i] = exp2_approx(e[i]);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            sum2[0] = add2(sum2[0], pair(e[i], e[i + 1]));
+                            sum2[1] = add2(sum2[1], pair(e[i + 2], e[i + 3]));
+                        }
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) {
+                            const int j = (x >> 1 & 1) * 16 + (x & 1) * 8 + (x >> 2) * 2;
+                            p[16 * ch + x] = pack_f16(e[j], e[j + 1]);
                         }
                     }
-                }
-                const float e = top == -INFINITY ? -INFINITY : top * c;
-                // the reference follows a maximum that has outgrown it; O and the sum with it
-                const bool grow = e > ref + LAZY || (ref == -INFINITY && e > ref);
-                if (__any_sync(0xffffffffu, grow)) {
-                    const float keep = grow ? exp2_approx(ref - e) : 1.f;
-                    if (grow) ref = e;
-                    l *= keep;
-                    if (it > 0) {
-#pragma unroll
-                        for (int ch = 0; ch < D / 32; ++ch) {
-                            uint32_t o[32];
-                            tmem_ld32(tmem + lanes + o_col(tile) + 32 * ch, o);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-                            tmem_st32(tmem + lanes + o_col(tile) + 32 * ch, o);
-                        }
-                        tmem_st_wait();
+                    if (!__any_sync(0xffffffffu, fmaxf(top0, top1) * c > ref + LAZY)) {
+                        tmem_st32(p_at, *reinterpret_cast<const uint32_t(*)[32]>(p));
+                        tmem_st32(p_at + 32, *reinterpret_cast<const uint32_t(*)[32]>(p + 32));
+                        float x, y;
+                        unpair(add2(sum2[0], sum2[1]), x, y);
+                        l += x + y;
+                        done = true;
                     }
                 }
-                // pass 2: the probabilities
-                const float base = ref == -INFINITY ? 0.f : 8.f - ref;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                if (!done) {
+                    // pass 1: the maximum
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int ch = 0; ch < BK / 32; ++ch) {
+                        uint32_t s[32];
+                        tmem_ld32(s_at + 32 * ch, s);
+                        tmem_ld_wait();
+                        if (all) {
 #pragma unroll
-                for (int ch = 0; ch < BK / 32; ++ch) {
-                    uint32_t s[32];
-                    tmem_ld32(s_at + 32 * ch, s);
-                    tmem_ld_wait();
-                    float p[32];
+                            for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(s[i]));
+                        } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) p[i] = exp2_approx(fmaf(__uint_as_float(s[i]), c, base));
-                    if (!all) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int j = k0 + 32 * ch + i;
-                            if (!(j < my_hi && j >= my_lo && (have >> (8 * ch + (i >> 4)) & 1))) p[i] = 0.f;
+                            for (int i = 0; i < 32; ++i) {
+                                const int j = k0 + 32 * ch + i;
+                                if (j < my_hi && j >= my_lo && (have >> (8 * ch + (i >> 4)) & 1)) top = fmaxf(top, __uint_as_float(s[i]));
+                            }
                         }
                     }
+                    const float e = top == -INFINITY ? -INFINITY : top * c;
+                    // the reference follows a maximum that has outgrown it; O and the sum with it
+                    const bool grow = e > ref + LAZY || (ref == -INFINITY && e > ref);
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float keep = grow ? exp2_approx(ref - e) : 1.f;
+                        if (grow) ref = e;
+                        l *= keep;
+                        if (it > 0) {
+#pragma unroll 1
+                            for (int ch = 0; ch < D / 32; ++ch) {
+                                uint32_t o[32];
+                                tmem_ld32(tmem + lanes + o_col(tile) + 32 * ch, o);
+                                tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) sum[i & 3] += p[i];
-                    // in the order of V^T's columns: t, block of the pair, tokens 2t, 2t+1, 2t+8, 2t+9
-                    uint32_t o[16];
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) {
-                        const int j = (x >> 1 & 1) * 16 + (x & 1) * 8 + (x >> 2) * 2;
-                        o[x] = pack_f16(p[j], p[j + 1]);
+                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                                tmem_st32(tmem + lanes + o_col(tile) + 32 * ch, o);
+                            }
+                            tmem_st_wait();
+                        }
                     }
-                    tmem_st16(p_at + 16 * ch, o);
+                    // pass 2: the probabilities
+                    const float base = ref == -INFINITY ? 0.f : 8.f - ref;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                    for (int ch = 0; ch < BK / 32; ++ch) {
+                        uint32_t s[32];
+                        tmem_ld32(s_at + 32 * ch, s);
+                        tmem_ld_wait();
+                        float p[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) p[i] = exp2_approx(fmaf(__uint_as_float(s[i]), c, base));
+                        if (!all) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const int j = k0 + 32 * ch + i;
+                                if (!(j < my_hi && j >= my_lo && (have >> (8 * ch + (i >> 4)) & 1))) p[i] = 0.f;
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) sum[i & 3] += p[i];
+                        // in the order of V^T's columns: t, block of the pair, tokens 2t, 2t+1, 2t+8, 2t+9
+                        uint32_t o[16];
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) {
+                            const int j = (x >> 1 & 1) * 16 + (x & 1) * 8 + (x >> 2) * 2;
+                            o[x] = pack_f16(p[j], p[j + 1]);
+                        }
+                        tmem_st16(p_at + 16 * ch, o);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -408,6 +510,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
             }
         }
     } else if (warp < MMA_WARP) {
+        fewer_registers<CONV_REGS>();
         // ================= conversion: warp w takes a step's blocks 2w and 2w + 1 =================
         __syncthreads();  // (1)
         const int w = warp - SOFT_WARPS;
@@ -553,54 +656,67 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
         }
         if (!ok && lane == 0) atomicOr(a.status, PQE_STATUS_TIMEOUT);
     } else {
+        fewer_registers<MMA_REGS>();
         // ================= MMA =================
         __syncthreads();  // (1)
-        if (lane == 0 && steps > 0) {
+        if (warp == MMA_WARP && steps > 0) {
             tc_fence_after();
+            const uint32_t one = elect();
             bool ok = true;
-            auto wait = [&](uint64_t &bar, uint32_t parity) {
-                if (ok && !mbar_wait(smem_u32(&bar), parity, a.wait_limit)) ok = false;
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                if (!mbar_wait(bar, parity, a.wait_limit)) ok = false;
+                ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();
                 return ok;
             };
-            auto scores = [&](int tile, int s) {
-                const uint32_t q = smem_u32(sm.q[tile][0]), k = smem_u32(sm.k[s][0]);
+            const uint64_t q_desc = sw128_desc(smem_u32(sm.q[0][0])), k_desc = sw128_desc(smem_u32(sm.k[0][0])),
+                           v_desc = sw128_desc(smem_u32(sm.v[0][0]));
+            constexpr uint64_t QK_STAGE = sizeof(sm.k[0]) / 16, V_STAGE = sizeof(sm.v[0]) / 16;  // a tile of Q is as large
+            const uint32_t k_full = smem_u32(&sm.k_full[0]), k_empty = smem_u32(&sm.k_empty[0]);
+            const uint32_t v_full = smem_u32(&sm.v_full[0]), v_empty = smem_u32(&sm.v_empty[0]);
+            const uint32_t s_full = smem_u32(&sm.s_full[0]), p_full = smem_u32(&sm.p_full[0]), o_full = smem_u32(&sm.o_full[0]);
+            auto scores = [&](int tile, uint64_t k) {
+                const uint64_t q = q_desc + tile * QK_STAGE;
+                umma_ss<false>(one, tmem + s_col(tile), q, k, IDESC_S);
 #pragma unroll
-                for (int x = 0; x < D / 16; ++x)
-                    umma_ss(tmem + s_col(tile), sw128_desc(q + (x >> 2) * CHUNK + (x & 3) * 32),
-                            sw128_desc(k + (x >> 2) * CHUNK + (x & 3) * 32), IDESC_S, x != 0);
-                umma_commit(smem_u32(&sm.s_full[tile]));
+                for (int x = 1; x < D / 16; ++x) {
+                    const uint64_t at = (x >> 2) * (CHUNK / 16) + (x & 3) * 2;
+                    umma_ss<true>(one, tmem + s_col(tile), q + at, k + at, IDESC_S);
+                }
+                commit(one, s_full + 8 * tile);
             };
-            if (wait(sm.k_full[0], 0)) {
-                for (int tile = 0; tile < tiles; ++tile) scores(tile, 0);
-                umma_commit(smem_u32(&sm.k_empty[0]));
+            if (wait(k_full, 0)) {
+                scores(0, k_desc);
+                if (tiles > 1) scores(1, k_desc);
+                commit(one, k_empty);
             }
             for (int it = 0; it < steps && ok; ++it) {
                 const int s = it & 1;
                 const bool more = it + 1 < steps;
-                if (!wait(sm.v_full[s], (uint32_t)(it >> 1) & 1u)) break;
-                for (int tile = 0; tile < tiles; ++tile) {
-                    if (!wait(sm.p_full[tile], it & 1)) break;
-                    const uint32_t v = smem_u32(sm.v[s][0]);
+                const uint64_t v = v_desc + s * V_STAGE, k = k_desc + (s ^ 1) * QK_STAGE;
+                if (!wait(v_full + 8 * s, (uint32_t)(it >> 1) & 1u)) break;
+                if (more && !wait(k_full + 8 * (s ^ 1), (uint32_t)((it + 1) >> 1) & 1u)) break;
+#pragma unroll
+                for (int tile = 0; tile < TILES; ++tile) {
+                    if (tile >= tiles) break;
+                    if (!wait(p_full + 8 * tile, it & 1)) break;
 #pragma unroll
                     for (int x = 0; x < BK / 16; ++x)
-                        umma_ts(tmem + o_col(tile), tmem + p_col<D>(tile) + 8 * x,
-                                sw128_desc(v + (x >> 2) * (D * 128) + (x & 3) * 32), IDESC_O, (it | x) != 0);
-                    if (more) {
-                        if (tile == 0 && !wait(sm.k_full[s ^ 1], (uint32_t)((it + 1) >> 1) & 1u)) break;
-                        scores(tile, s ^ 1);
-                    } else {
-                        umma_commit(smem_u32(&sm.o_full[tile]));
-                    }
+                        umma_ts(one, tmem + o_col(tile), tmem + p_col<D>(tile) + 8 * x,
+                                v + (x >> 2) * (D * 128 / 16) + (x & 3) * 2, IDESC_O, x == 0 ? it != 0 : 1);
+                    if (more)
+                        scores(tile, k);
+                    else
+                        commit(one, o_full + 8 * tile);
                 }
                 if (!ok) break;
-                umma_commit(smem_u32(&sm.v_empty[s]));
-                if (more) umma_commit(smem_u32(&sm.k_empty[s ^ 1]));
+                commit(one, v_empty + 8 * s);
+                if (more) commit(one, k_empty + 8 * (s ^ 1));
             }
             // every MMA has finished before TMEM is released
-            umma_commit(smem_u32(&sm.drained));
+            commit(one, smem_u32(&sm.drained));
             if (!mbar_wait(smem_u32(&sm.drained), 0, a.wait_limit)) ok = false;
-            if (!ok) atomicOr(a.status, PQE_STATUS_TIMEOUT);
+            if (!ok && lane == 0) atomicOr(a.status, PQE_STATUS_TIMEOUT);
         }
         __syncwarp();
     }
@@ -618,6 +734,10 @@ int launch(const AttnArgs &a, cudaStream_t s) {
     if (rc != PQE_OK) return rc;
     constexpr int smem = (int)sizeof(Smem<D>) + 1024;
     if (!set[dev]) {
+        // the split of the registers waits forever where the block is launched with fewer than it counts on
+        cudaFuncAttributes at;
+        PQE_CUDA_TRY(cudaFuncGetAttributes(&at, attn_prompt_kernel<D>));
+        if (at.numRegs != LAUNCH_REGS) return PQE_ERR_UNSUPPORTED;
         PQE_CUDA_TRY(cudaFuncSetAttribute(attn_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
         set[dev] = true;
     }
