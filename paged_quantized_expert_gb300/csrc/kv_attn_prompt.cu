@@ -236,30 +236,55 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
     {
         int kt = 0, vt = 0, nan = 0;
         constexpr int PIECES = D / 16;  // 16-byte pieces of a block's scales: K's, then V's
-        const int n_blk = (k_end - k_first + BLOCK - 1) / BLOCK;
-        for (int i = tid; i < n_blk * PIECES; i += THREADS) {
-            const int j = k_first + i / PIECES * BLOCK, piece = i % PIECES;
-            if (j + BLOCK <= lo) continue;  // before the window: its page may be gone
-            const int page = table[j >> a.c.page_shift];
-            if (page < 0 || page >= a.c.n_pages) {
-                atomicOr(a.status, PQE_STATUS_BAD_PAGE);
-                continue;
-            }
-            const uint4 u = *reinterpret_cast<const uint4 *>(block_of<D>(a.c, page, j & page_mask, head) + 16 * D + 16 * piece);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-            const bool is_v = piece >= PIECES / 2;
+        const int n_pieces = (k_end - k_first + BLOCK - 1) / BLOCK * PIECES;
+        constexpr int AHEAD = 4;  // loads in flight: table entries, then scales
+        for (int i0 = tid; i0 < n_pieces; i0 += AHEAD * THREADS) {
+            int page[AHEAD];
+            uint4 u[AHEAD];
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-                // the token that the byte belongs to: K [token][G], V [t][G][j]
-                const int at = (piece % (PIECES / 2)) * 16 + x;
-                const int tok = is_v ? 2 * (at / (D / 8)) + (x & 1) + 8 * (x >> 1 & 1) : at / (D / 32);
-                const int s = j + tok < k_end ? (int)(w[x >> 2] >> (8 * (x & 3)) & 255u) : 0;
-                if (s == 255)
-                    nan |= is_v;
-                else if (is_v)
-                    vt = max(vt, s);
+            for (int y = 0; y < AHEAD; ++y) {
+                const int i = i0 + y * THREADS, j = k_first + i / PIECES * BLOCK;
+                // before the window a page may be gone
+                page[y] = i < n_pieces && j + BLOCK > lo ? max(table[j >> a.c.page_shift], -1) : -2;
+            }
+#pragma unroll
+            for (int y = 0; y < AHEAD; ++y) {
+                const int i = i0 + y * THREADS, j = k_first + i / PIECES * BLOCK;
+                u[y] = make_uint4(0, 0, 0, 0);
+                if (page[y] >= 0 && page[y] < a.c.n_pages)
+                    u[y] = *reinterpret_cast<const uint4 *>(block_of<D>(a.c, page[y], j & page_mask, head) + 16 * D +
+                                                            16 * (i % PIECES));
+                else if (page[y] != -2)
+                    atomicOr(a.status, PQE_STATUS_BAD_PAGE);
+            }
+#pragma unroll
+            for (int y = 0; y < AHEAD; ++y) {
+                const int i = i0 + y * THREADS, j = k_first + i / PIECES * BLOCK, piece = i % PIECES;
+                const uint32_t w[4] = {u[y].x, u[y].y, u[y].z, u[y].w};
+                const bool is_v = piece >= PIECES / 2;
+                uint32_t two = 0;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) two = __vmaxu2(two, __vmaxu2(w[x] & 0x00FF00FFu, (w[x] >> 8) & 0x00FF00FFu));
+                int top = (int)max(two & 0xFFFFu, two >> 16);
+                if (top == 255 || j + BLOCK > k_end) {
+                    // byte by byte: some are NaN, or of tokens that are not there
+                    top = 0;
+                    for (int x = 0; x < 16; ++x) {
+                        // the token that the byte belongs to: K [token][G], V [t][G][j]
+                        const int at = (piece % (PIECES / 2)) * 16 + x;
+                        const int tok = is_v ? 2 * (at / (D / 8)) + (x & 1) + 8 * (x >> 1 & 1) : at / (D / 32);
+                        const uint32_t word = x < 4 ? w[0] : x < 8 ? w[1] : x < 12 ? w[2] : w[3];
+                        const int s = j + tok < k_end ? (int)(word >> (8 * (x & 3)) & 255u) : 0;
+                        if (s == 255)
+                            nan |= is_v;
+                        else
+                            top = max(top, s);
+                    }
+                }
+                if (is_v)
+                    vt = max(vt, top);
                 else
-                    kt = max(kt, s);
+                    kt = max(kt, top);
             }
         }
         kt = __reduce_max_sync(0xffffffffu, kt);
