@@ -5,126 +5,389 @@
 // RNE_e2m1(v / X). X is a power of two, so v / X is exact in fp32 and the only
 // rounding is the code's own. Both kernels move bytes and do next to no
 // arithmetic: bound by memory once there are enough tokens, by latency below.
+// The lanes' shares are those of the cache's byte order, so that what a warp
+// writes or reads of a block is contiguous: K by rows, V by places.
 #include "kv_layout.cuh"
 
 namespace pqe {
 namespace kv {
 
-struct Codes {
-    uint32_t word;   // eight codes, the first in the low nibble
-    uint32_t scale;  // E8M0 byte of the 32 values
-};
+// bits of |v| of two bf16: they order as the values do; a NaN or an infinity ends at or above 0x7F80
+__device__ __forceinline__ uint32_t top_of(uint32_t a, uint32_t b) { return __vmaxu2(a & 0x7FFF7FFFu, b & 0x7FFF7FFFu); }
+__device__ __forceinline__ uint32_t top_of(uint32_t two) { return max(two & 0xFFFFu, two >> 16); }
 
-// Eight of the 32 values of a block, the other 24 in the three neighbouring
-// lanes (four lanes, aligned): their codes and the block's scale. All 32 lanes
-// call it.
-__device__ __forceinline__ Codes quantize8(const uint4 &raw) {
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    // |v| of bf16 compares as its bits do; a NaN or an infinity ends at or above 0x7F80
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t a = w[i] & 0x7FFF7FFFu;
-        top = max(top, max(a & 0xFFFFu, a >> 16));
+// E8M0 byte of a block of 32 with largest |v| `top` (bf16 bits), and 1 / X; 255 and 0 for one that is not finite
+__device__ __forceinline__ uint32_t block_scale(uint32_t top, float &inv) {
+    // floor(log2 amax) + 127 is the exponent field; subnormal values end at byte 0
+    const uint32_t s = (uint32_t)max((int)(top >> 7) - 2, 0);
+    inv = __uint_as_float((254u - s) << 23);  // 2^(127 - s): s is at most 252 for finite values
+    if (top >= 0x7F80u) {
+        inv = 0.f;
+        return 255;
     }
+    return s;
+}
+
+// two bf16 to a byte of two codes; zero where inv is (v may then be NaN)
+__device__ __forceinline__ uint32_t code2(uint32_t v, float inv) {
+    const uint32_t b = f32x2_to_e2m1x2(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xFFFF0000u) * inv);
+    return inv == 0.f ? 0u : b;
+}
+
+// four codes (two bytes, low nibble first) times s, as bf16
+__device__ __forceinline__ uint2 values4(uint32_t codes, float s) {
+    uint2 o;
+    const float2 x = e2m1x2_to_f32x2((uint8_t)codes), y = e2m1x2_to_f32x2((uint8_t)(codes >> 8));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o.x) : "f"(x.y * s), "f"(x.x * s));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o.y) : "f"(y.y * s), "f"(y.x * s));
+    return o;
+}
+
+// ---- few tokens: a thread per eight values, the shortest way from a row to its bytes ----
+
+// Token, head, first channel and K or V of eight values; 2 * n_kv * D / 8 threads a token, K before V, four neighbouring
+// lanes for a block of 32.
+struct Eight {
+    int tok, head, e;
+    bool is_v, in;
+};
+template <int D>
+__device__ __forceinline__ Eight eight_of(const Cache &c, int n) {
+    const uint32_t i = blockIdx.x * 256 + threadIdx.x, per = 2 * c.n_kv * (D / 8);
+    Eight x;
+    x.tok = (int)(i / per);
+    x.in = x.tok < n;
+    const uint32_t r = i % per;
+    x.is_v = r >= per / 2;
+    const uint32_t rr = x.is_v ? r - per / 2 : r;
+    x.head = (int)(rr / (D / 8));
+    x.e = (int)(rr % (D / 8)) * 8;
+    return x;
+}
+// the token's slot, -1 if it has none
+__device__ __forceinline__ int64_t slot_of(const Cache &c, const int64_t *slots, const Eight &x, int32_t *status) {
+    if (!x.in) return -1;
+    const int64_t slot = slots[x.tok];
+    if (slot >> c.page_shift < c.n_pages) return slot;
+    if (!x.is_v && x.head == 0 && x.e == 0) atomicOr(status, PQE_STATUS_BAD_PAGE);
+    return -1;
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) kv_write_few_kernel(const Cache c, const uint16_t *__restrict__ k,
+                                                           const uint16_t *__restrict__ v, int64_t k_stride,
+                                                           int64_t v_stride, const int64_t *__restrict__ slots, int n,
+                                                           int32_t *status) {
+    pdl_acquire();
+    const Eight x = eight_of<D>(c, n);
+    // the row is asked for beside its slot
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (x.in) raw = *reinterpret_cast<const uint4 *>((x.is_v ? v + x.tok * v_stride : k + x.tok * k_stride) + x.head * D + x.e);
+    const int64_t slot = slot_of(c, slots, x, status);
+    uint32_t top = top_of(__vmaxu2(top_of(raw.x, raw.y), top_of(raw.z, raw.w)));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    Codes c{0, 255};
-    if (top < 0x7F80u) {
-        // floor(log2 amax) + 127 is the exponent field; subnormal values end at scale byte 0
-        const int e = (int)(top >> 7) - 2;
-        c.scale = (uint32_t)max(e, 0);
-        const float inv = __uint_as_float((254u - c.scale) << 23);  // 2^(127 - scale): 2^-127 is never asked for
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float lo = bf16_to_f32((uint16_t)(w[i] & 0xFFFFu)), hi = bf16_to_f32((uint16_t)(w[i] >> 16));
-            c.word |= (uint32_t)f32x2_to_e2m1x2(lo * inv, hi * inv) << (8 * i);
-        }
+    float inv;
+    const uint32_t scale = block_scale(top, inv);
+    const uint32_t word = code2(raw.x, inv) | code2(raw.y, inv) << 8 | code2(raw.z, inv) << 16 | code2(raw.w, inv) << 24;
+    if (slot < 0) return;
+    const int at = (int)(slot & ((1 << c.page_shift) - 1)), t = at & 15;
+    uint8_t *b = block_of<D>(c, slot >> c.page_shift, at, x.head);
+    if (!x.is_v) {
+        *reinterpret_cast<uint32_t *>(b + k_code<D>(t, x.e)) = word;
+        if (x.e % 32 == 0) b[k_scale<D>(t, x.e / 32)] = (uint8_t)scale;
+    } else {
+        *reinterpret_cast<uint16_t *>(b + v_code<D>(t, x.e)) = (uint16_t)word;
+        *reinterpret_cast<uint16_t *>(b + v_code<D>(t, x.e + 4)) = (uint16_t)(word >> 16);
+        if (x.e % 32 == 0) b[v_scale<D>(t, x.e / 32)] = (uint8_t)scale;
     }
-    return c;
 }
 
-// One thread per eight values of a token's row: 2 * n_kv * D / 8 threads a
-// token, K before V.
 template <int D>
-__global__ void __launch_bounds__(256) kv_write_kernel(const Cache c, const uint16_t *__restrict__ k,
-                                                       const uint16_t *__restrict__ v, int64_t k_stride,
-                                                       int64_t v_stride, const int64_t *__restrict__ slots, int n,
-                                                       int32_t *status) {
+__global__ void __launch_bounds__(256) kv_read_few_kernel(const Cache c, const int64_t *__restrict__ slots, int n,
+                                                          uint16_t *k, uint16_t *v, int32_t *status) {
     pdl_acquire();
-    const int per = 2 * c.n_kv * (D / 8);
-    const int64_t total = (int64_t)n * per;  // a multiple of four: the lanes of a block of 32 act together
-    for (int64_t i0 = (int64_t)blockIdx.x * 256; i0 < total; i0 += (int64_t)gridDim.x * 256) {
-        const int64_t i = i0 + threadIdx.x;
-        const bool in = i < total;
-        const int tok = in ? (int)(i / per) : 0, r = in ? (int)(i % per) : 0;
-        const bool is_v = r >= per / 2;
-        const int rr = is_v ? r - per / 2 : r, h = rr / (D / 8), e = (rr % (D / 8)) * 8;
-        int64_t slot = in ? slots[tok] : -1;
-        if (slot >> c.page_shift >= c.n_pages) {
-            if (r == 0) atomicOr(status, PQE_STATUS_BAD_PAGE);
-            slot = -1;
-        }
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (slot >= 0)
-            raw = *reinterpret_cast<const uint4 *>((is_v ? v + tok * v_stride : k + tok * k_stride) + h * D + e);
-        const Codes q = quantize8(raw);
-        if (slot < 0) continue;
+    const Eight x = eight_of<D>(c, n);
+    const int64_t slot = slot_of(c, slots, x, status);
+    uint16_t *out = x.is_v ? v : k;
+    if (!x.in || !out) return;
+    uint32_t word = 0;
+    float s = 0.f;
+    if (slot >= 0) {
         const int at = (int)(slot & ((1 << c.page_shift) - 1)), t = at & 15;
-        uint8_t *b = block_of<D>(c, slot >> c.page_shift, at, h);
-        if (!is_v) {
-            *reinterpret_cast<uint32_t *>(b + k_code<D>(t, e)) = q.word;
-            if (e % 32 == 0) b[k_scale<D>(t, e / 32)] = (uint8_t)q.scale;
+        const uint8_t *b = block_of<D>(c, slot >> c.page_shift, at, x.head);
+        if (!x.is_v) {
+            word = *reinterpret_cast<const uint32_t *>(b + k_code<D>(t, x.e));
+            s = scale_value(b[k_scale<D>(t, x.e / 32)]);
         } else {
-            *reinterpret_cast<uint16_t *>(b + v_code<D>(t, e)) = (uint16_t)q.word;
-            *reinterpret_cast<uint16_t *>(b + v_code<D>(t, e + 4)) = (uint16_t)(q.word >> 16);
-            if (e % 32 == 0) b[v_scale<D>(t, e / 32)] = (uint8_t)q.scale;
+            word = (uint32_t)*reinterpret_cast<const uint16_t *>(b + v_code<D>(t, x.e)) |
+                   (uint32_t)*reinterpret_cast<const uint16_t *>(b + v_code<D>(t, x.e + 4)) << 16;
+            s = scale_value(b[v_scale<D>(t, x.e / 32)]);
         }
     }
+    const uint2 lo = values4(word, s), hi = values4(word >> 16, s);
+    *reinterpret_cast<uint4 *>(out + ((size_t)x.tok * c.n_kv + x.head) * D + x.e) = make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
 
-// eight codes (the first in the low nibble) times 2^(scale - 127), as bf16
-__device__ __forceinline__ uint4 values8(uint32_t word, uint32_t scale) {
-    const float s = scale_value(scale);
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = e2m1x2_to_f32x2((uint8_t)(word >> (8 * i)));
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(f.y * s), "f"(f.x * s));
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
-}
+// ---- many tokens ----
+
+constexpr int WARPS = 8;
+// Groups an SM below which a thread for each eight values is faster. (Write and read of a run of 4096 tokens of 8 heads of
+// 128, 27 groups an SM: 7.5 + 6.6 us that way, 6.8 + 6.9 by groups; 1024 tokens: 3.2 + 2.9 and 4.3 + 3.2; 16384: 25.5 +
+// 23.6 and 20.5 + 14.6.)
+constexpr int FEW_WARPS = 26;
+
+// The 16 rows that a warp takes of one head of K or V: consecutive rows of the
+// call. Where they go is told per row, so they may lie in 16 blocks; a prompt's
+// rows lie in one block, or in two when the call begins inside one.
+struct Group {
+    const uint8_t *blk[16];  // the row's block in the cache (of this head), NULL: no row, or one that is skipped
+    int8_t tok[16];          // its place in the block
+    int8_t row[16];          // V: the row that the lanes of place p take. Where the rows' places are all different, that is
+                             // the row of place p, and a lane's four rows then lie side by side in a block's bytes
+};
 
 template <int D>
-__global__ void __launch_bounds__(256) kv_read_kernel(const Cache c, const int64_t *__restrict__ slots, int n,
-                                                      uint16_t *k, uint16_t *v, int32_t *status) {
-    pdl_acquire();
-    const int per = 2 * c.n_kv * (D / 8);
-    const int64_t total = (int64_t)n * per;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int tok = (int)(i / per), r = (int)(i % per);
-        const bool is_v = r >= per / 2;
-        uint16_t *out = is_v ? v : k;
-        const int rr = is_v ? r - per / 2 : r, h = rr / (D / 8), e = (rr % (D / 8)) * 8;
-        int64_t slot = slots[tok];
-        if (slot >> c.page_shift >= c.n_pages) {
-            if (r == 0) atomicOr(status, PQE_STATUS_BAD_PAGE);
-            slot = -1;
-        }
-        if (!out) continue;
-        uint4 val = make_uint4(0, 0, 0, 0);
-        if (slot >= 0) {
-            const int at = (int)(slot & ((1 << c.page_shift) - 1)), t = at & 15;
-            const uint8_t *b = block_of<D>(c, slot >> c.page_shift, at, h);
-            if (!is_v)
-                val = values8(*reinterpret_cast<const uint32_t *>(b + k_code<D>(t, e)), b[k_scale<D>(t, e / 32)]);
-            else
-                val = values8((uint32_t)*reinterpret_cast<const uint16_t *>(b + v_code<D>(t, e)) |
-                                  (uint32_t)*reinterpret_cast<const uint16_t *>(b + v_code<D>(t, e + 4)) << 16,
-                              b[v_scale<D>(t, e / 32)]);
-        }
-        *reinterpret_cast<uint4 *>(out + ((size_t)tok * c.n_kv + h) * D + e) = val;
+__device__ __forceinline__ void group_of(const Cache &c, const int64_t *__restrict__ slots, int n, int first, int head,
+                                         int lane, Group &g, int32_t *status, bool report) {
+    const int r = lane & 15;
+    int64_t slot = first + r < n ? slots[first + r] : -1;
+    if (slot >> c.page_shift >= c.n_pages) {
+        if (report && lane < 16) atomicOr(status, PQE_STATUS_BAD_PAGE);
+        slot = -1;
     }
+    const int at = (int)(slot & ((1 << c.page_shift) - 1)), tok = at & 15;
+    const uint32_t place = slot >= 0 ? 1u << tok : 0u;
+    // all places different: as many bits as rows
+    const uint32_t places = __reduce_or_sync(0xffffffffu, place);
+    const bool apart = __popc(places) == __popc(__ballot_sync(0xffffffffu, slot >= 0) & 0xFFFFu);
+    if (lane < 16) {
+        g.blk[r] = slot >= 0 ? block_of<D>(c, slot >> c.page_shift, at, head) : nullptr;
+        g.tok[r] = (int8_t)tok;
+        if (!apart || !(places >> r & 1)) g.row[r] = apart ? (int8_t)-1 : (int8_t)r;
+    }
+    __syncwarp();
+    if (lane < 16 && apart && slot >= 0) g.row[tok] = (int8_t)r;
+    __syncwarp();
+}
+
+// K and V of one group and head by one warp each.
+template <int D>
+__global__ void __launch_bounds__(32 * WARPS) kv_write_kernel(const Cache c, const uint16_t *__restrict__ k,
+                                                              const uint16_t *__restrict__ v, int64_t k_stride,
+                                                              int64_t v_stride, const int64_t *__restrict__ slots, int n,
+                                                              int32_t *status) {
+    __shared__ Group groups[WARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t unit = blockIdx.x * WARPS + warp, per = 2 * c.n_kv, which = unit % per;
+    const int first = (int)(unit / per) * 16, head = which >> 1;
+    pdl_acquire();
+    if (first >= n) return;
+    Group &G = groups[warp];
+    group_of<D>(c, slots, n, first, head, lane, G, status, which == 0);
+    constexpr int NB = D / 32;
+    if (!(which & 1)) {
+        // K: four lanes a row, eight channels of each block a lane
+        const int t = lane & 3;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = (lane >> 2) + 8 * h;
+            uint8_t *blk = const_cast<uint8_t *>(G.blk[r]);
+            uint4 raw[NB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                raw[b] = blk ? *reinterpret_cast<const uint4 *>(k + (first + r) * k_stride + head * D + 32 * b + 8 * t)
+                             : make_uint4(0, 0, 0, 0);
+            uint32_t word[NB], scales = 0;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                uint32_t top = top_of(__vmaxu2(top_of(raw[b].x, raw[b].y), top_of(raw[b].z, raw[b].w)));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                float inv;
+                scales |= block_scale(top, inv) << (8 * b);
+                word[b] = code2(raw[b].x, inv) | code2(raw[b].y, inv) << 8 | code2(raw[b].z, inv) << 16 |
+                          code2(raw[b].w, inv) << 24;
+            }
+            if (!blk) continue;
+            const int tok = G.tok[r];
+            if constexpr (D == 128) {
+                *reinterpret_cast<uint4 *>(blk + tok * 64 + t * 16) = make_uint4(word[0], word[1], word[2], word[3]);
+                if (t == 0) *reinterpret_cast<uint32_t *>(blk + 16 * D + tok * 4) = scales;
+            } else {
+                *reinterpret_cast<uint2 *>(blk + tok * 32 + t * 8) = make_uint2(word[0], word[1]);
+                if (t == 0) *reinterpret_cast<uint16_t *>(blk + 16 * D + tok * 2) = (uint16_t)scales;
+            }
+        }
+    } else {
+        // V: lane (g, t) has the rows of places 2t, 2t+1, 2t+8, 2t+9, four channels of each block; the eight lanes of a
+        // place hold a block's 32 channels
+        const int g = lane >> 2, t = lane & 3;
+        int row[4];
+        uint8_t *blk[4];
+        uint2 raw[NB][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            row[j] = G.row[2 * t + (j & 1) + 8 * (j >> 1)];
+            blk[j] = row[j] >= 0 ? const_cast<uint8_t *>(G.blk[row[j]]) : nullptr;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                raw[b][j] = blk[j] ? *reinterpret_cast<const uint2 *>(v + (first + row[j]) * v_stride + head * D + 32 * b + 4 * g)
+                                   : make_uint2(0, 0);
+        }
+        uint32_t word[NB / 2][4] = {}, scales[NB] = {};  // codes of two blocks; four rows' scale bytes
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t top = top_of(top_of(raw[b][j].x, raw[b][j].y));
+#pragma unroll
+                for (int o = 4; o <= 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                float inv;
+                scales[b] |= block_scale(top, inv) << (8 * j);
+                word[b >> 1][j] |= (code2(raw[b][j].x, inv) | code2(raw[b][j].y, inv) << 8) << (16 * (b & 1));
+            }
+        // side by side: the four rows in one block, each at its own place
+        bool together = blk[0] != nullptr;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            together = together && blk[j] == blk[0] && G.tok[row[j]] == 2 * t + (j & 1) + 8 * (j >> 1);
+        if (together) {
+#pragma unroll
+            for (int q = 0; q < NB / 2; ++q)
+                *reinterpret_cast<uint4 *>(blk[0] + 8 * D + q * 512 + lane * 16) =
+                    make_uint4(word[q][0], word[q][1], word[q][2], word[q][3]);
+            if (g < NB) {
+                uint32_t s = scales[0];
+#pragma unroll
+                for (int b = 1; b < NB; ++b) s = g == b ? scales[b] : s;
+                *reinterpret_cast<uint32_t *>(blk[0] + 16 * D + D / 2 + t * (D / 8) + g * 4) = s;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (!blk[j]) continue;
+                const int tok = G.tok[row[j]];
+#pragma unroll
+                for (int q = 0; q < NB / 2; ++q)
+                    *reinterpret_cast<uint32_t *>(blk[j] + v_code<D>(tok, 64 * q + 4 * g)) = word[q][j];
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                    if (g == b) blk[j][v_scale<D>(tok, b)] = (uint8_t)(scales[b] >> (8 * j));
+            }
+        }
+    }
+}
+
+// The same shares as the write's: a group, a head, K or V a warp.
+template <int D>
+__global__ void __launch_bounds__(32 * WARPS) kv_read_kernel(const Cache c, const int64_t *__restrict__ slots, int n,
+                                                             uint16_t *k, uint16_t *v, int32_t *status) {
+    __shared__ Group groups[WARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t unit = blockIdx.x * WARPS + warp, per = 2 * c.n_kv, which = unit % per;
+    const int first = (int)(unit / per) * 16, head = which >> 1;
+    pdl_acquire();
+    if (first >= n) return;
+    Group &G = groups[warp];
+    group_of<D>(c, slots, n, first, head, lane, G, status, which == 0);
+    constexpr int NB = D / 32;
+    if (!(which & 1)) {
+        if (!k) return;
+        const int t = lane & 3;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = (lane >> 2) + 8 * h;
+            if (first + r >= n) continue;
+            uint32_t word[NB] = {}, scales = 0;
+            if (const uint8_t *blk = G.blk[r]) {
+                const int tok = G.tok[r];
+                if constexpr (D == 128) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(blk + tok * 64 + t * 16);
+                    word[0] = u.x, word[1] = u.y, word[2] = u.z, word[3] = u.w;
+                    scales = *reinterpret_cast<const uint32_t *>(blk + 16 * D + tok * 4);
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(blk + tok * 32 + t * 8);
+                    word[0] = u.x, word[1] = u.y;
+                    scales = *reinterpret_cast<const uint16_t *>(blk + 16 * D + tok * 2);
+                }
+            }
+            uint16_t *out = k + ((size_t)(first + r) * c.n_kv + head) * D + 8 * t;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const float s = scale_value(scales >> (8 * b) & 255u);
+                const uint2 lo = values4(word[b], s), hi = values4(word[b] >> 16, s);
+                *reinterpret_cast<uint4 *>(out + 32 * b) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            }
+        }
+    } else {
+        if (!v) return;
+        const int g = lane >> 2, t = lane & 3;
+        int row[4];
+        const uint8_t *blk[4];
+        bool together = true;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int place = 2 * t + (j & 1) + 8 * (j >> 1);
+            row[j] = G.row[place];
+            blk[j] = row[j] >= 0 ? G.blk[row[j]] : nullptr;
+            together = together && blk[j] && blk[j] == blk[0] && G.tok[row[j]] == place;
+        }
+        uint32_t word[NB / 2][4] = {}, scales[NB] = {};
+        if (together) {
+#pragma unroll
+            for (int q = 0; q < NB / 2; ++q) {
+                const uint4 u = *reinterpret_cast<const uint4 *>(blk[0] + 8 * D + q * 512 + lane * 16);
+                word[q][0] = u.x, word[q][1] = u.y, word[q][2] = u.z, word[q][3] = u.w;
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                scales[b] = *reinterpret_cast<const uint32_t *>(blk[0] + 16 * D + D / 2 + t * (D / 8) + b * 4);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (!blk[j]) continue;
+                const int tok = G.tok[row[j]];
+#pragma unroll
+                for (int q = 0; q < NB / 2; ++q)
+                    word[q][j] = *reinterpret_cast<const uint32_t *>(blk[j] + v_code<D>(tok, 64 * q + 4 * g));
+#pragma unroll
+                for (int b = 0; b < NB; ++b) scales[b] |= (uint32_t)blk[j][v_scale<D>(tok, b)] << (8 * j);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (row[j] < 0 || first + row[j] >= n) continue;
+            uint16_t *out = v + ((size_t)(first + row[j]) * c.n_kv + head) * D + 4 * g;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                *reinterpret_cast<uint2 *>(out + 32 * b) =
+                    values4(word[b >> 1][j] >> (16 * (b & 1)), scale_value(scales[b] >> (8 * j) & 255u));
+        }
+        // rows that are skipped: nobody's place where the others' are all different
+        if (lane < 16 && first + lane < n && !G.blk[lane]) {
+            bool mine = false;
+            for (int p = 0; p < 16; ++p) mine = mine || G.row[p] == lane;
+            if (!mine)
+                for (int d = 0; d < D; d += 8)
+                    *reinterpret_cast<uint4 *>(v + ((size_t)(first + lane) * c.n_kv + head) * D + d) = make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+
+// a warp for each 16 rows, head, and K or V
+static int64_t group_units(int n, int n_kv) { return (((int64_t)n + 15) / 16) * 2 * n_kv; }
+
+template <typename... KArgs>
+static int launch_groups(void (*few)(KArgs...), void (*many)(KArgs...), int n, int n_kv, int d, cudaStream_t s,
+                         typename ident<KArgs>::type... args) {
+    int dev = 0, sms = 0;
+    const int rc = device_info(dev, sms);
+    if (rc != PQE_OK) return rc;
+    const int64_t units = group_units(n, n_kv);
+    if (units < FEW_WARPS * sms)
+        return launch_pdl(few, dim3((unsigned)(((int64_t)n * 2 * n_kv * d / 8 + 255) / 256)), dim3(256), 0, s, args...);
+    return launch_pdl(many, dim3((unsigned)((units + WARPS - 1) / WARPS)), dim3(32 * WARPS), 0, s, args...);
 }
 
 }  // namespace kv
@@ -147,14 +410,12 @@ int kv_cache_write(const pqe_kv_cache *cache, const void *k, const void *v, int6
     PQE_CHECK_ARG(k && v && slots && status && aligned(k, 16) && aligned(v, 16) && aligned(slots, 8));
     PQE_CHECK_ARG(k_stride >= row && v_stride >= row && k_stride % 8 == 0 && v_stride % 8 == 0);
     const kv::Cache c = kv::cache_of(cache);
-    int dev = 0, sms = 0;
-    const int rc = device_info(dev, sms);
-    if (rc != PQE_OK) return rc;
-    const int64_t ctas = ((int64_t)n * 2 * row / 8 + 255) / 256, most = (int64_t)sms * 16;
-    const dim3 grid((unsigned)(ctas < most ? ctas : most));
     const uint16_t *kp = static_cast<const uint16_t *>(k), *vp = static_cast<const uint16_t *>(v);
-    return launch_pdl(cache->d == 128 ? kv::kv_write_kernel<128> : kv::kv_write_kernel<64>, grid, dim3(256), 0,
-                      as_stream(stream), c, kp, vp, k_stride, v_stride, slots, n, status);
+    if (cache->d == 128)
+        return kv::launch_groups(kv::kv_write_few_kernel<128>, kv::kv_write_kernel<128>, n, cache->n_kv, 128,
+                                 as_stream(stream), c, kp, vp, k_stride, v_stride, slots, n, status);
+    return kv::launch_groups(kv::kv_write_few_kernel<64>, kv::kv_write_kernel<64>, n, cache->n_kv, 64, as_stream(stream), c,
+                             kp, vp, k_stride, v_stride, slots, n, status);
 }
 
 int kv_cache_read(const pqe_kv_cache *cache, const int64_t *slots, int n, void *k, void *v, int32_t *status,
@@ -163,13 +424,12 @@ int kv_cache_read(const pqe_kv_cache *cache, const int64_t *slots, int n, void *
     if (n == 0) return PQE_OK;
     PQE_CHECK_ARG((k || v) && slots && status && aligned(k, 16) && aligned(v, 16) && aligned(slots, 8));
     const kv::Cache c = kv::cache_of(cache);
-    int dev = 0, sms = 0;
-    const int rc = device_info(dev, sms);
-    if (rc != PQE_OK) return rc;
-    const int64_t ctas = ((int64_t)n * 2 * cache->n_kv * cache->d / 8 + 255) / 256, most = (int64_t)sms * 16;
-    const dim3 grid((unsigned)(ctas < most ? ctas : most));
-    return launch_pdl(cache->d == 128 ? kv::kv_read_kernel<128> : kv::kv_read_kernel<64>, grid, dim3(256), 0,
-                      as_stream(stream), c, slots, n, static_cast<uint16_t *>(k), static_cast<uint16_t *>(v), status);
+    uint16_t *kp = static_cast<uint16_t *>(k), *vp = static_cast<uint16_t *>(v);
+    if (cache->d == 128)
+        return kv::launch_groups(kv::kv_read_few_kernel<128>, kv::kv_read_kernel<128>, n, cache->n_kv, 128, as_stream(stream),
+                                 c, slots, n, kp, vp, status);
+    return kv::launch_groups(kv::kv_read_few_kernel<64>, kv::kv_read_kernel<64>, n, cache->n_kv, 64, as_stream(stream), c,
+                             slots, n, kp, vp, status);
 }
 
 }  // extern "C"
