@@ -6,7 +6,7 @@
 namespace pqe {
 namespace kv {
 
-constexpr int TILE = 64;  // tokens of a tile: what the kernels take of the cache at a time
+constexpr int TILE = 64;  // tokens that the split kernel takes of the cache at a time
 
 struct AttnArgs {
     Cache c;

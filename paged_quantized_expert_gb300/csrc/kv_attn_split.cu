@@ -38,39 +38,17 @@ using namespace ptx;
 
 constexpr int WARPS = 4;
 constexpr int STAGES = 2;
+constexpr int TB = TILE / BLOCK;  // blocks of a tile
+constexpr uint32_t ALL = (1u << TB) - 1;
 
 template <int D>
 constexpr int tile_bytes() {
     return TILE / BLOCK * block_bytes(D);
 }
+// CTAs an SM: what the registers of a warp leave room for
+__host__ __device__ constexpr int ctas(int d, int nt) { return nt == 1 ? 3 : 2; }
 // one partial result: O [rows][D], m [rows], l [rows], all fp32
 __host__ __device__ constexpr int part_floats(int d, int rows) { return rows * (d + 2); }
-
-// what a tile's scale bytes become for the MMAs' lanes
-template <int D>
-struct Factors {
-    float k[TILE][D / 32];        // [token][block]: 2^(scale - 127)
-    uint32_t v[4][4][D / 32][2];  // [16 tokens][t][block]: f16 pairs for tokens 2t, 2t+1 and 2t+8, 2t+9
-};
-
-template <int D, int NT>
-struct Smem {
-    alignas(16) uint8_t ring[WARPS][STAGES][tile_bytes<D>()];  // a warp's last partial takes its ring's place
-    alignas(16) Factors<D> fac[WARPS];
-    alignas(8) uint64_t full[WARPS][STAGES];
-    int64_t scan[WARPS];
-    int64_t start_off[WARPS];
-    int start_b[WARPS];
-    // pieces of (sequence, head, rows) that the warps did not finish alone: two each
-    int64_t seg_start[WARPS][2];
-    int from[WARPS][2], to[WARPS][2], len_t[WARPS][2], b[WARPS][2], head[WARPS][2], chunk[WARPS][2];
-    const float *ptr[WARPS][2];
-};
-
-// unit at which share i of n begins, of `total` units
-__device__ __forceinline__ int64_t share_start(int64_t i, int64_t n, int64_t total) { return i * total / n; }
-// the share that unit u falls into
-__device__ __forceinline__ int64_t share_of(int64_t u, int64_t n, int64_t total) { return ((u + 1) * n - 1) / total; }
 
 // Beginning and ending a (sequence, head, rows) costs about as much as a tile: it counts as one in the line of work,
 // before its first tile. (64 sequences of 1 to 8192 tokens: without it the slowest SM took 1.27 times the mean.)
@@ -110,6 +88,33 @@ __device__ __forceinline__ void next_rows(const AttnArgs &a, Cursor &c, int grou
     }
 }
 
+// what a tile's scale bytes become for the MMAs' lanes
+template <int D>
+struct Factors {
+    float k[TILE][D / 32];        // [token][block]: 2^(scale - 127)
+    uint32_t v[TB][4][D / 32][2];  // [16 tokens][t][block]: f16 pairs for tokens 2t, 2t+1 and 2t+8, 2t+9
+};
+
+template <int D, int NT>
+struct Smem {
+    alignas(16) uint8_t ring[WARPS][STAGES][tile_bytes<D>()];  // a warp's last partial takes its ring's place
+    alignas(16) Factors<D> fac[WARPS];
+    alignas(8) uint64_t full[WARPS][STAGES];
+    Cursor at[WARPS], ahead[WARPS];  // the rows at hand, and those that tiles are fetched for
+    int64_t scan[WARPS];
+    int64_t start_off[WARPS];
+    int start_b[WARPS];
+    // pieces of (sequence, head, rows) that the warps did not finish alone: two each
+    int64_t seg_start[WARPS][2];
+    int from[WARPS][2], to[WARPS][2], len_t[WARPS][2], b[WARPS][2], head[WARPS][2], chunk[WARPS][2];
+    const float *ptr[WARPS][2];
+};
+
+// unit at which share i of n begins, of `total` units
+__device__ __forceinline__ int64_t share_start(int64_t i, int64_t n, int64_t total) { return i * total / n; }
+// the share that unit u falls into
+__device__ __forceinline__ int64_t share_of(int64_t u, int64_t n, int64_t total) { return ((u + 1) * n - 1) / total; }
+
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(bar)
@@ -139,44 +144,53 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return r;
 }
 
-// A tile's copies: lane i's takes the blocks from i << shift on, of one page.
-__device__ __forceinline__ int blocks_shift(const AttnArgs &a) { return min(a.c.page_shift - 4, 2); }
-__device__ __forceinline__ int tile_blocks(const Cursor &c) {
-    return min(TILE / BLOCK, (c.s.len - (c.s.t0 + c.tile) * TILE + BLOCK - 1) / BLOCK);
-}
-
-// The table entry that this lane's copy of the cursor's tile needs. Asked for a tile early, so that fetch() does not wait.
-__device__ __forceinline__ int table_entry(const AttnArgs &a, const Cursor &c, int lane) {
-    const int blk = lane << blocks_shift(a), j = (c.s.t0 + c.tile) * TILE + blk * BLOCK;
-    if (blk >= tile_blocks(c)) return -1;
-    if (j + (BLOCK << blocks_shift(a)) <= c.s.lo) return -2;  // before the window: the page may be gone
-    return max(a.block_table[(size_t)c.b * a.max_pages + (j >> a.c.page_shift)], -1);
-}
-
-// Starts the copies of the cursor's tile into a stage; returns the bit mask of
-// its 16-token blocks that the stage will hold (a block of a bad page, or past
-// the end, is not there).
+// What fetching needs of a cursor (the rest of it waits in shared memory), and of the lane: lane i of the first few copies the
+// blocks from blk on, of one page.
+struct Feed {
+    const int32_t *table;  // the sequence's
+    const uint8_t *head;   // the head's part of page 0
+    int j, len, lo;        // j: the first token that the lane copies
+};
+__device__ __forceinline__ int blocks_shift(const AttnArgs &a) { return min(a.c.page_shift - 4, TB == 4 ? 2 : 1); }
 template <int D>
-__device__ __forceinline__ uint32_t fetch(const AttnArgs &a, const Cursor &c, int page, uint32_t dst, uint32_t bar,
-                                          int lane) {
-    const int nblk = tile_blocks(c), blk = lane << blocks_shift(a);
-    uint32_t bytes = 0, mask = 0;
-    const uint8_t *src = nullptr;
-    if (blk < nblk) {
-        if (page >= 0 && page < a.c.n_pages) {
-            const int n = min(1 << blocks_shift(a), nblk - blk);
-            const int j = (c.s.t0 + c.tile) * TILE + blk * BLOCK;
-            src = block_of<D>(a.c, page, j & ((1 << a.c.page_shift) - 1), c.head);
-            bytes = n * block_bytes(D);
-            mask = ((1u << n) - 1) << blk;
-        } else if (page != -2) {
-            atomicOr(a.status, PQE_STATUS_BAD_PAGE);
-        }
+__device__ __forceinline__ Feed feed_of(const AttnArgs &a, const Cursor &c, int lane) {
+    const int blk = lane << blocks_shift(a);
+    return {a.block_table + (size_t)c.b * a.max_pages, block_of<D>(a.c, 0, 0, c.head),
+            blk < TB ? (c.s.t0 + c.tile) * TILE + blk * BLOCK : INT32_MAX / 2, c.s.len, c.s.lo};
+}
+
+// The table entry that this lane's copy of the tile needs. Asked for a tile early, so that fetch() does not wait.
+__device__ __forceinline__ int table_entry(const AttnArgs &a, const Feed &f) {
+    if (f.j >= f.len) return -3;                                    // no tokens
+    if (f.j + (BLOCK << blocks_shift(a)) <= f.lo) return -2;  // before the window: the page may be gone
+    return max(f.table[f.j >> a.c.page_shift], -1);
+}
+
+// Starts the copies of a tile into a stage; returns the bit mask of its 16-token
+// blocks that the stage will hold (a block of a bad page, or past the end, is
+// not there).
+template <int D>
+__device__ __forceinline__ uint32_t fetch(const AttnArgs &a, const Feed &f, int page, uint32_t dst, uint32_t bar, int lane) {
+    const int sh = blocks_shift(a), copies = TB >> sh;  // lanes that copy
+    const bool good = (uint32_t)page < (uint32_t)a.c.n_pages;
+    const uint8_t *src = f.head + (size_t)(uint32_t)page * a.c.page_stride +
+                         ((f.j & ((1 << a.c.page_shift) - 1)) >> 4) * block_bytes(D);
+    dst += (lane << sh) * block_bytes(D);
+    if (__all_sync(0xffffffffu, lane >= copies || (good && f.j + (BLOCK << sh) <= f.len))) {
+        if (lane == 0) mbar_expect_tx(bar, TB * block_bytes(D));
+        __syncwarp();
+        if (lane < copies) bulk_copy(dst, src, block_bytes(D) << sh, bar);
+        return ALL;
     }
-    mask = __reduce_or_sync(0xffffffffu, mask);
+    uint32_t n = 0;  // blocks that this lane copies
+    if (good)
+        n = min(1 << sh, (f.len - f.j + BLOCK - 1) / BLOCK);
+    else if (page == -1 || page >= a.c.n_pages)
+        atomicOr(a.status, PQE_STATUS_BAD_PAGE);
+    const uint32_t mask = __reduce_or_sync(0xffffffffu, n ? ((1u << n) - 1) << (lane << sh) : 0u);
     if (lane == 0) mbar_expect_tx(bar, __popc(mask) * block_bytes(D));
     __syncwarp();
-    if (bytes) bulk_copy(dst + blk * block_bytes(D), src, bytes, bar);
+    if (n) bulk_copy(dst, src, n * block_bytes(D), bar);
     return mask;
 }
 
@@ -283,12 +297,12 @@ __device__ __forceinline__ void begin_rows(const AttnArgs &a, const Cursor &c, i
 // O += codes . (p * factors) of one tile. NANS: some V scale of it is 255.
 template <int D, int NT, bool NANS>
 __device__ __forceinline__ void add_values(const uint8_t *tile, const Factors<D> &fac, int lane,
-                                           const uint32_t (&p)[4][NT][2], Rows<D, NT> &R) {
+                                           const uint32_t (&p)[TB][NT][2], Rows<D, NT> &R) {
     const int t = lane & 3;
 #pragma unroll
     for (int q2 = 0; q2 < D / 64; ++q2) {
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
+        for (int mt = 0; mt < TB; ++mt) {
             // four tokens (2t, 2t+1, 2t+8, 2t+9) x channels 4g.. of two blocks
             const uint4 w = *reinterpret_cast<const uint4 *>(tile + mt * block_bytes(D) + 8 * D + q2 * 512 + lane * 16);
             const uint4 vf = *reinterpret_cast<const uint4 *>(fac.v[mt][t][2 * q2]);
@@ -316,7 +330,7 @@ __device__ __forceinline__ void add_values(const uint8_t *tile, const Factors<D>
 template <int D, int NT>
 __device__ __forceinline__ void add_tile(uint8_t *tile, Factors<D> &fac, int j0, uint32_t have, int lane, Rows<D, NT> &R) {
     const int g = lane >> 2, t = lane & 3;
-    const bool part = have != 0xFu || j0 + TILE > R.min_hi || j0 < R.max_lo;  // some row does not see all of it
+    const bool part = have != ALL || j0 + TILE > R.min_hi || j0 < R.max_lo;  // some row does not see all of it
     if (part) {
         // V of tokens that no row sees may hold anything: scale bytes of zero
         for (int i = lane; i < TILE; i += 32) {
@@ -331,55 +345,64 @@ __device__ __forceinline__ void add_tile(uint8_t *tile, Factors<D> &fac, int j0,
     // The scale bytes as the factors that the lanes take. Each would otherwise be made by the four lanes (K) or eight
     // (V) that use it, on the integer pipe that the code conversions fill.
     uint32_t top = 0;
+    bool nans;
     {
-        const uint8_t *sc = tile + (lane >> 4) * block_bytes(D) + 16 * D;  // of tokens lane and lane + 32
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float f[D / 32];
-            const uint8_t *at = sc + 2 * h * block_bytes(D) + (lane & 15) * (D / 32);
+        for (int h = 0; h < TILE / 32; ++h) {
+            // of tokens lane and lane + 32
+            const uint8_t *at = tile + ((lane >> 4) + 2 * h) * block_bytes(D) + 16 * D + (lane & 15) * (D / 32);
             const uint32_t w = D == 128 ? *reinterpret_cast<const uint32_t *>(at) : *reinterpret_cast<const uint16_t *>(at);
+            float f[D / 32];
             // byte into the exponent: 255 gives infinity, and NaN on the zero codes that go with it; 0 gives 0
 #pragma unroll
-            for (int G = 0; G < D / 32; ++G) f[G] = __uint_as_float(w << (23 - 8 * G > 0 ? 23 - 8 * G : 0) >> (G == 3 ? 1 : 0) & 0x7F800000u);
+            for (int G = 0; G < D / 32; ++G) f[G] = __uint_as_float(w << (G < 3 ? 23 - 8 * G : 0) >> (G < 3 ? 0 : 1) & 0x7F800000u);
             if constexpr (D == 128)
                 *reinterpret_cast<float4 *>(fac.k[lane + 32 * h]) = make_float4(f[0], f[1], f[2], f[3]);
             else
                 *reinterpret_cast<float2 *>(fac.k[lane + 32 * h]) = make_float2(f[0], f[1]);
         }
-        uint32_t w[D / 64];  // D/64 of the tile's words [16 tokens][t][block]
+        // V: words [16 tokens][t][block] of four tokens' scales, WORDS a lane
+        constexpr int WORDS = TB * (D / 32) / 8;
+        uint32_t w[WORDS], two = 0;
+        const uint8_t *vs = tile + lane * WORDS / (D / 8) * block_bytes(D) + 16 * D + D / 2 + lane * WORDS % (D / 8) * 4;
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-            w[i] = *reinterpret_cast<const uint32_t *>(tile + (lane >> 3) * block_bytes(D) + 16 * D + D / 2 +
-                                                       (lane & 7) * (D / 16) + 4 * i);
-            top = max(top, max(max(w[i] & 255u, w[i] >> 8 & 255u), max(w[i] >> 16 & 255u, w[i] >> 24)));
+        for (int i = 0; i < WORDS; ++i) {
+            w[i] = *reinterpret_cast<const uint32_t *>(vs + 4 * i);
+            two = __vmaxu2(two, __vmaxu2(w[i] & 0x00FF00FFu, (w[i] >> 8) & 0x00FF00FFu));
         }
-        top = __reduce_max_sync(0xffffffffu, top);
-        if (top == 255) {
-            uint32_t u = 0;
+        top = __reduce_max_sync(0xffffffffu, max(two & 0xFFFFu, two >> 16));
+        nans = top == 255;
+        if (nans) {
+            top = 0;
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i)
+            for (int i = 0; i < WORDS; ++i)
 #pragma unroll
-                for (int j = 0; j < 32; j += 8) u = max(u, (w[i] >> j & 255u) == 255 ? 0u : w[i] >> j & 255u);
-            top = __reduce_max_sync(0xffffffffu, u) | 256u;  // the bit: there are some
+                for (int j = 0; j < 32; j += 8) top = max(top, (w[i] >> j & 255u) == 255 ? 0u : w[i] >> j & 255u);
+            top = __reduce_max_sync(0xffffffffu, top);
         }
-        const bool nans = top > 255;
-        top = max(top & 255u, R.top) | (nans ? 256u : 0u);
-        uint32_t *vf = &fac.v[0][0][0][0] + lane * (D / 32);
-        uint32_t o[D / 32];
+        top = max(top, R.top);
+        // f16 pairs of 2^(scale - top + 7): 0 from 22 below top on
+        const uint32_t least = (uint32_t)max((int)top - 22, 0) * 0x10001u, off = (uint32_t)((int)top - 22) * (1024u * 0x10001u);
+        uint32_t o[2 * WORDS];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            const uint32_t x = w[i >> 1] >> (16 * (i & 1));
-            o[i] = v_weight(x & 255u, top & 255u) | v_weight(x >> 8 & 255u, top & 255u) << 16;
+        for (int i = 0; i < 2 * WORDS; ++i) {
+            const uint32_t x = __byte_perm(w[i >> 1], 0, i & 1 ? 0x4342 : 0x4140);
+            o[i] = __vmaxu2(x, least) * 1024u - off;
+            if (nans) {
+                const uint32_t lo = x & 0xFFFFu, hi = x >> 16;
+                o[i] = v_weight(lo, top) | v_weight(hi, top) << 16;
+            }
         }
-        if constexpr (D == 128)
+        uint32_t *vf = &fac.v[0][0][0][0] + lane * 2 * WORDS;
+        if constexpr (WORDS == 2)
             *reinterpret_cast<uint4 *>(vf) = make_uint4(o[0], o[1], o[2], o[3]);
         else
             *reinterpret_cast<uint2 *>(vf) = make_uint2(o[0], o[1]);
     }
     __syncwarp();
-    float x[4][NT][4];  // S^T, then exponents, then p: tokens 16 * mt + g (+ 8), rows 8 * nt + 2t (+ 1)
+    float x[TB][NT][4];  // S^T, then exponents, then p: tokens 16 * mt + g (+ 8), rows 8 * nt + 2t (+ 1)
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
+    for (int mt = 0; mt < TB; ++mt) {
         const uint8_t *blk = tile + mt * block_bytes(D);
         uint32_t k0[D / 32], k1[D / 32];
         float f0[D / 32], f1[D / 32];
@@ -422,7 +445,7 @@ __device__ __forceinline__ void add_tile(uint8_t *tile, Factors<D> &fac, int j0,
     }
     if (part) {
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
+        for (int mt = 0; mt < TB; ++mt)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -433,15 +456,15 @@ __device__ __forceinline__ void add_tile(uint8_t *tile, Factors<D> &fac, int j0,
     }
     // the running maximum; rows' values lie in the eight lanes of equal t
     float keep[NT][2];
-    bool moved = (top & 255u) != R.top;
-    const float shrink = moved ? exp2_approx((float)(int)(R.top - (top & 255u))) : 1.f;
+    bool moved = top != R.top;
+    const float shrink = moved ? exp2_approx((float)(int)(R.top - top)) : 1.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             float m = R.m[nt][i];
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) m = fmaxf(m, fmaxf(x[mt][nt][i], x[mt][nt][i + 2]));
+            for (int mt = 0; mt < TB; ++mt) m = fmaxf(m, fmaxf(x[mt][nt][i], x[mt][nt][i + 2]));
 #pragma unroll
             for (int o = 4; o <= 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             const float c = R.c[nt][i], base = m == -INFINITY ? -8.f : fmaf(m, c, -8.f);
@@ -451,7 +474,7 @@ __device__ __forceinline__ void add_tile(uint8_t *tile, Factors<D> &fac, int j0,
             R.m[nt][i] = m;
             float sum = 0.f;
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
+            for (int mt = 0; mt < TB; ++mt)
 #pragma unroll
                 for (int h = 0; h < 4; h += 2) {
                     const float p = exp2_approx(fmaf(x[mt][nt][i + h], c, -base));
@@ -469,17 +492,17 @@ __device__ __forceinline__ void add_tile(uint8_t *tile, Factors<D> &fac, int j0,
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) R.o[G][e][nt][i] *= keep[nt][i & 1];
-        R.top = top & 255u;
+        R.top = top;
     }
-    uint32_t p[4][NT][2];
+    uint32_t p[TB][NT][2];
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
+    for (int mt = 0; mt < TB; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             p[mt][nt][0] = transpose8x8(pack_f16(x[mt][nt][0], x[mt][nt][1]));
             p[mt][nt][1] = transpose8x8(pack_f16(x[mt][nt][2], x[mt][nt][3]));
         }
-    if (top < 256)
+    if (!nans)
         add_values<D, NT, false>(tile, fac, lane, p, R);
     else
         add_values<D, NT, true>(tile, fac, lane, p, R);
@@ -535,7 +558,7 @@ __device__ __forceinline__ void end_rows(const AttnArgs &a, const Cursor &c, int
 __host__ __device__ inline size_t prefix_bytes(int B) { return round_up(((size_t)B + 1) * 8, 256); }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 3 : 2) attn_split_kernel(const AttnArgs a, uint8_t *ws) {
+__global__ void __launch_bounds__(WARPS * 32, ctas(D, NT)) attn_split_kernel(const AttnArgs a, uint8_t *ws) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     auto &sm = *reinterpret_cast<Smem<D, NT> *>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -612,47 +635,67 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 3 : 2) attn_split_kernel
     const int64_t u1 = share_start((int64_t)blockIdx.x * WARPS + warp + 1, nw, total);
     const int64_t cta0 = share_start((int64_t)blockIdx.x * WARPS, nw, total);
     if (u0 < u1) {
-        Cursor c;  // of the tile at hand
-        c.b = sm.start_b[warp];
-        c.s = load_seq<NT>(a, c.b, group);
-        const int per_rows = c.s.T + OPEN, nth = (int)(sm.start_off[warp] / per_rows);
-        int skip = (int)(sm.start_off[warp] % per_rows) - OPEN;
-        c.head = nth / c.s.nrc;
-        c.chunk = nth % c.s.nrc;
-        c.tile = max(skip, 0);
-        int64_t u = u0 - min(skip, 0), fu = u;  // the unit at hand and the next one to fetch: never one of OPEN
-        Cursor f = c;
+        int left = (int)(u1 - u0), ahead = 0;  // units to do, and to fetch: from a tile on, never from one of OPEN
+        int rows_end = 0;                      // what is left to fetch when the rows' last tile has been
+        Feed f;
+        {
+            Cursor c;
+            c.b = sm.start_b[warp];
+            c.s = load_seq<NT>(a, c.b, group);
+            const int per_rows = c.s.T + OPEN, nth = (int)(sm.start_off[warp] / per_rows);
+            const int skip = (int)(sm.start_off[warp] % per_rows) - OPEN;
+            c.head = nth / c.s.nrc;
+            c.chunk = nth % c.s.nrc;
+            c.tile = max(skip, 0);
+            left += min(skip, 0);
+            ahead = left;
+            rows_end = left - (c.s.T - c.tile);
+            f = feed_of<D>(a, c, lane);
+            if (lane == 0) sm.at[warp] = sm.ahead[warp] = c;
+            __syncwarp();
+        }
         const uint32_t ring = smem_u32(sm.ring[warp][0]), bar = smem_u32(&sm.full[warp][0]);
         uint32_t have[STAGES] = {};
-        int page = fu < u1 ? table_entry(a, f, lane) : -1;
+        int page = ahead > 0 ? table_entry(a, f) : -1;
         auto fetch_next = [&](int s) {
             const uint32_t h = fetch<D>(a, f, page, ring + s * tile_bytes<D>(), bar + 8 * s, lane);
-            ++fu;
-            if (++f.tile == f.s.T) {
-                next_rows<NT>(a, f, group);
-                fu += OPEN;
+            f.j += TILE;
+            if (--ahead == rows_end && ahead > 0) {
+                ahead -= OPEN;
+                Cursor c = sm.ahead[warp];
+                if (ahead > 0) next_rows<NT>(a, c, group);
+                f = feed_of<D>(a, c, lane);
+                rows_end = ahead - c.s.T;
+                __syncwarp();
+                if (lane == 0) sm.ahead[warp] = c;
+                __syncwarp();
             }
-            if (fu < u1) page = table_entry(a, f, lane);
+            if (ahead > 0) page = table_entry(a, f);
             return h;
         };
-        if (fu < u1) have[0] = fetch_next(0);
-        if (fu < u1) have[1] = fetch_next(1);
+        if (ahead > 0) have[0] = fetch_next(0);
+        if (ahead > 0) have[1] = fetch_next(1);
         Rows<D, NT> R;
         bool ok = true;
-        int it = 0;
-        while (u < u1 && ok) {
+        uint32_t it = 0;
+        while (left > 0 && ok) {
             // the tiles of one (sequence, head, rows)
-            begin_rows<D, NT>(a, c, group, lane, R);
-            const int from = c.tile, to = (int)min((int64_t)c.s.T, c.tile + (u1 - u));
-            for (; c.tile < to; ++c.tile, ++it) {
+            int j0, j_end, tiles;
+            {
+                const Cursor c = sm.at[warp];
+                begin_rows<D, NT>(a, c, group, lane, R);
+                tiles = min(c.s.T - c.tile, left);
+                j0 = (c.s.t0 + c.tile) * TILE;
+                j_end = j0 + tiles * TILE;
+            }
+            for (; j0 < j_end; j0 += TILE, ++it) {
                 const int s = it & 1;
-                if (!mbar_wait(bar + 8 * s, (uint32_t)(it >> 1) & 1u, a.wait_limit)) ok = false;
+                if (!mbar_wait(bar + 8 * s, it >> 1 & 1u, a.wait_limit)) ok = false;
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                const int j0 = (c.s.t0 + c.tile) * TILE;
                 if (j0 < R.max_hi)  // else no row of the chunk sees it
                     add_tile<D, NT>(sm.ring[warp][s], sm.fac[warp], j0, s ? have[1] : have[0], lane, R);
-                if (fu < u1) {
+                if (ahead > 0) {
                     const uint32_t h = fetch_next(s);
                     if (s)
                         have[1] = h;
@@ -660,15 +703,17 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 3 : 2) attn_split_kernel
                         have[0] = h;
                 }
             }
-            const int64_t seg_start = u - from - OPEN;
-            u += to - from;
+            Cursor c = sm.at[warp];
+            const int from = c.tile, to = from + tiles;
+            const int64_t seg_start = u1 - left - from - OPEN;
+            left -= tiles;
             const bool ended = to == c.s.T, whole = from == 0 && ended;
-            if (ended) u += OPEN;
+            if (ended) left -= OPEN;
             float *part = nullptr;
             if (!whole) {
                 // the last piece stays in shared memory, in the ring that nothing is fetched into any more; an
                 // earlier one, of which there is at most one, goes through memory
-                const int k = u >= u1 ? 1 : 0;
+                const int k = left <= 0 ? 1 : 0;
                 part = k ? reinterpret_cast<float *>(sm.ring[warp][0]) : scratch + ((size_t)blockIdx.x * WARPS + warp) * PART;
                 if (lane == 0) {
                     sm.seg_start[warp][k] = seg_start;
@@ -683,7 +728,12 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 3 : 2) attn_split_kernel
                 __syncwarp();
             }
             if (ok) end_rows<D, NT>(a, c, group, lane, R, whole, part);
-            if (u < u1) next_rows<NT>(a, c, group);
+            if (left > 0) {
+                next_rows<NT>(a, c, group);
+                __syncwarp();
+                if (lane == 0) sm.at[warp] = c;
+                __syncwarp();
+            }
         }
         if (!ok) {
             // the copies in flight land before the block ends (bounded)
@@ -825,7 +875,7 @@ int launch(const AttnArgs &a, int max_q, int sms, void *ws, cudaStream_t s) {
     const int64_t nrc = ((int64_t)max_q * group + 8 * NT - 1) / (8 * NT);
     const int64_t tiles = (((int64_t)a.max_pages << a.c.page_shift) + TILE - 1) / TILE;
     const double most = (double)a.B * a.c.n_kv * nrc * (tiles + OPEN) / WARPS + 1;
-    int grid = sms * (NT == 1 ? 3 : 2);
+    int grid = sms * ctas(D, NT);
     if (most < grid) grid = (int)most;
     static bool set[PQE_MAX_DEVICES] = {};
     int dev = 0, n = 0;
@@ -851,7 +901,7 @@ size_t attn_split_ws(int B, int max_q, int group, int d) {
     int dev = 0, sms = 0;
     if (device_info(dev, sms) != PQE_OK) sms = 160;  // without a device: an upper bound
     return split::prefix_bytes(B) +
-           (size_t)sms * (NT == 1 ? 3 : 2) * (2 + split::WARPS) * split::part_floats(d, 8 * NT) * sizeof(float);
+           (size_t)sms * split::ctas(d, NT) * (2 + split::WARPS) * split::part_floats(d, 8 * NT) * sizeof(float);
 }
 
 int attn_split(const pqe_kv_cache *cache, const AttnArgs &a, int max_q, int sms, void *ws, cudaStream_t s) {
