@@ -18,10 +18,10 @@
 // it in one line is cut into equal shares, one per warp of the grid, whatever
 // the lengths are (they are read on the device). A warp fetches its tiles
 // with bulk copies into its own ring of shared memory, two ahead; it meets no
-// other warp until its share is done. A share's first and last piece may
-// belong to a (sequence, head, rows) that others share: the CTA's four warps
-// join theirs in shared memory, CTAs leave theirs in the workspace, and a
-// second kernel joins those in a fixed order.
+// other warp. A (sequence, head, rows) that lies in one share
+// goes straight out; of one that shares divide between them each leaves a
+// partial in the workspace, two at most, and a second kernel joins them in the
+// order of the cache.
 //
 // Bound by the cache's bytes when there are many (4.25 bits a value: 43 values a
 // clock and SM at the memory's rate, at about one instruction a value), by
@@ -50,9 +50,10 @@ __host__ __device__ constexpr int ctas(int d, int nt) { return nt == 1 ? 3 : 2; 
 // one partial result: O [rows][D], m [rows], l [rows], all fp32
 __host__ __device__ constexpr int part_floats(int d, int rows) { return rows * (d + 2); }
 
-// Beginning and ending a (sequence, head, rows) costs about as much as a tile: it counts as one in the line of work,
-// before its first tile. (64 sequences of 1 to 8192 tokens: without it the slowest SM took 1.27 times the mean.)
-constexpr int OPEN = 1;
+// Beginning and ending a (sequence, head, rows) costs about as much as two tiles: it counts as two in the line of work, before
+// its first tile. (64 sequences of 1 to 8192 tokens: 40.4 us with one, 39.3 with two; five rows of four heads over windows of
+// 1024: 24.5 and 22.3 us.)
+constexpr int OPEN = 2;
 
 // a sequence's part of the line of work
 struct Seq {
@@ -97,19 +98,20 @@ struct Factors {
 
 template <int D, int NT>
 struct Smem {
-    alignas(16) uint8_t ring[WARPS][STAGES][tile_bytes<D>()];  // a warp's last partial takes its ring's place
+    alignas(16) uint8_t ring[WARPS][STAGES][tile_bytes<D>()];
     alignas(16) Factors<D> fac[WARPS];
     alignas(8) uint64_t full[WARPS][STAGES];
     Cursor at[WARPS], ahead[WARPS];  // the rows at hand, and those that tiles are fetched for
     int64_t scan[WARPS];
-    int64_t start_off[WARPS];
-    int start_b[WARPS];
-    // pieces of (sequence, head, rows) that the warps did not finish alone: two each
-    int64_t seg_start[WARPS][2];
-    int from[WARPS][2], to[WARPS][2], len_t[WARPS][2], b[WARPS][2], head[WARPS][2], chunk[WARPS][2];
-    const float *ptr[WARPS][2];
+    int64_t share[WARPS + 1];  // units at which the warps' shares begin
+    int64_t first[WARPS];      // unit at which the sequence begins that a share begins in
 };
 
+// shares that `total` units are cut into: at least one unit each
+__host__ __device__ __forceinline__ int64_t shares(int64_t total, int ctas) {
+    const int64_t most = (int64_t)ctas * WARPS;
+    return total < most ? (total > 0 ? total : 1) : most;
+}
 // unit at which share i of n begins, of `total` units
 __device__ __forceinline__ int64_t share_start(int64_t i, int64_t n, int64_t total) { return i * total / n; }
 // the share that unit u falls into
@@ -553,8 +555,7 @@ __device__ __forceinline__ void end_rows(const AttnArgs &a, const Cursor &c, int
         }
 }
 
-// Workspace: prefix [B + 1] of the sequences' units, then per CTA two partials for the joining kernel and one per
-// warp for a first piece that is not its last
+// Workspace: prefix [B + 1] of the sequences' units, then two partials per warp
 __host__ __device__ inline size_t prefix_bytes(int B) { return round_up(((size_t)B + 1) * 8, 256); }
 
 template <int D, int NT>
@@ -566,11 +567,9 @@ __global__ void __launch_bounds__(WARPS * 32, ctas(D, NT)) attn_split_kernel(con
     constexpr int PART = part_floats(D, 8 * NT);
     int64_t *prefix = reinterpret_cast<int64_t *>(ws);
     float *parts = reinterpret_cast<float *>(ws + prefix_bytes(a.B));
-    float *scratch = parts + (size_t)gridDim.x * 2 * PART;
 
     if (lane == 0)
         for (int s = 0; s < STAGES; ++s) mbar_init(smem_u32(&sm.full[warp][s]), 1);
-    if (lane < 2) sm.ptr[warp][lane] = nullptr;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     pdl_acquire();
@@ -579,10 +578,11 @@ __global__ void __launch_bounds__(WARPS * 32, ctas(D, NT)) attn_split_kernel(con
     const int per = (a.B + WARPS * 32 - 1) / (WARPS * 32);
     const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
     int64_t mine = 0;
+    Cursor c = {};  // the sequence at hand: with one a thread it is not read again below
     for (int b = b0; b < b1; ++b) {
-        const Seq s = load_seq<NT>(a, b, group);
-        mine += s.units(a.c.n_kv);
-        if (blockIdx.x == 0 && a.kv_lens[b] > s.len) atomicOr(a.status, PQE_STATUS_BAD_PAGE);
+        c.s = load_seq<NT>(a, b, group);
+        mine += c.s.units(a.c.n_kv);
+        if (blockIdx.x == 0 && a.kv_lens[b] > c.s.len) atomicOr(a.status, PQE_STATUS_BAD_PAGE);
     }
     int64_t incl = mine;
 #pragma unroll
@@ -599,51 +599,38 @@ __global__ void __launch_bounds__(WARPS * 32, ctas(D, NT)) attn_split_kernel(con
         total += sm.scan[w];
     }
     before += incl - mine;
-    // shares of at least a tile a warp
-    const int64_t n_cta = min((int64_t)gridDim.x, (total + WARPS - 1) / WARPS);
-    if (blockIdx.x == 0) {
-        int64_t at = before;
-        for (int b = b0; b < b1; ++b) {
-            prefix[b] = at;
-            const Seq s = load_seq<NT>(a, b, group);
-            at += s.units(a.c.n_kv);
-        }
-        if (tid == 0) prefix[a.B] = total;
-    }
-    if (blockIdx.x >= n_cta) return;
-    const int64_t nw = n_cta * WARPS;
-    for (int w = 0; w < WARPS; ++w) {
-        const int64_t u = share_start((int64_t)blockIdx.x * WARPS + w, nw, total);
-        if (u >= before && u < before + mine) {
-            int64_t at = before;
-            for (int b = b0; b < b1; ++b) {
-                const Seq s = load_seq<NT>(a, b, group);
-                const int64_t n = s.units(a.c.n_kv);
-                if (u < at + n) {
-                    sm.start_b[w] = b;
-                    sm.start_off[w] = u - at;
-                    break;
-                }
-                at += n;
+    const int64_t nw = shares(total, gridDim.x);
+    if (tid <= WARPS) sm.share[tid] = share_start(min((int64_t)blockIdx.x * WARPS + tid, nw), nw, total);
+    __syncthreads();
+    int64_t at = before;
+    for (int b = b0; b < b1; ++b) {
+        if (per > 1) c.s = load_seq<NT>(a, b, group);
+        const int64_t n = c.s.units(a.c.n_kv);
+        c.b = b;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w)
+            if (sm.share[w] >= at && sm.share[w] < at + n) {
+                sm.at[w] = c;
+                sm.first[w] = at;
             }
-        }
+        if (blockIdx.x == 0) prefix[b] = at;
+        at += n;
     }
+    if (blockIdx.x == 0 && tid == 0) prefix[a.B] = total;
     __syncthreads();
 
     // ---- this warp's share ----
-    const int64_t u0 = share_start((int64_t)blockIdx.x * WARPS + warp, nw, total);
-    const int64_t u1 = share_start((int64_t)blockIdx.x * WARPS + warp + 1, nw, total);
-    const int64_t cta0 = share_start((int64_t)blockIdx.x * WARPS, nw, total);
+    const int64_t u0 = sm.share[warp], u1 = sm.share[warp + 1];
     if (u0 < u1) {
         int left = (int)(u1 - u0), ahead = 0;  // units to do, and to fetch: from a tile on, never from one of OPEN
         int rows_end = 0;                      // what is left to fetch when the rows' last tile has been
         Feed f;
         {
-            Cursor c;
-            c.b = sm.start_b[warp];
-            c.s = load_seq<NT>(a, c.b, group);
-            const int per_rows = c.s.T + OPEN, nth = (int)(sm.start_off[warp] / per_rows);
-            const int skip = (int)(sm.start_off[warp] % per_rows) - OPEN;
+            Cursor c = sm.at[warp];
+            const uint32_t per_rows = c.s.T + OPEN;
+            const int64_t off = u0 - sm.first[warp];
+            const int nth = off >> 32 ? (int)(off / per_rows) : (int)((uint32_t)off / per_rows);
+            const int skip = (int)(off - (int64_t)nth * per_rows) - OPEN;
             c.head = nth / c.s.nrc;
             c.chunk = nth % c.s.nrc;
             c.tile = max(skip, 0);
@@ -651,6 +638,7 @@ __global__ void __launch_bounds__(WARPS * 32, ctas(D, NT)) attn_split_kernel(con
             ahead = left;
             rows_end = left - (c.s.T - c.tile);
             f = feed_of<D>(a, c, lane);
+            __syncwarp();
             if (lane == 0) sm.at[warp] = sm.ahead[warp] = c;
             __syncwarp();
         }
@@ -709,24 +697,8 @@ __global__ void __launch_bounds__(WARPS * 32, ctas(D, NT)) attn_split_kernel(con
             left -= tiles;
             const bool ended = to == c.s.T, whole = from == 0 && ended;
             if (ended) left -= OPEN;
-            float *part = nullptr;
-            if (!whole) {
-                // the last piece stays in shared memory, in the ring that nothing is fetched into any more; an
-                // earlier one, of which there is at most one, goes through memory
-                const int k = left <= 0 ? 1 : 0;
-                part = k ? reinterpret_cast<float *>(sm.ring[warp][0]) : scratch + ((size_t)blockIdx.x * WARPS + warp) * PART;
-                if (lane == 0) {
-                    sm.seg_start[warp][k] = seg_start;
-                    sm.from[warp][k] = from;
-                    sm.to[warp][k] = to;
-                    sm.len_t[warp][k] = c.s.T;
-                    sm.b[warp][k] = c.b;
-                    sm.head[warp][k] = c.head;
-                    sm.chunk[warp][k] = c.chunk;
-                    sm.ptr[warp][k] = part;
-                }
-                __syncwarp();
-            }
+            // the share's first piece in the first partial, one that begins inside it in the second
+            float *part = parts + ((size_t)2 * (blockIdx.x * WARPS + warp) + (seg_start > u0 ? 1 : 0)) * PART;
             if (ok) end_rows<D, NT>(a, c, group, lane, R, whole, part);
             if (left > 0) {
                 next_rows<NT>(a, c, group);
@@ -744,127 +716,102 @@ __global__ void __launch_bounds__(WARPS * 32, ctas(D, NT)) attn_split_kernel(con
             if (lane == 0) atomicOr(a.status, PQE_STATUS_TIMEOUT);
         }
     }
-    __syncthreads();
-
-    // ---- join the CTA's pieces, in order ----
-    for (int i = 0; i < 2 * WARPS;) {
-        const int w = i >> 1, k = i & 1;
-        if (!sm.ptr[w][k]) {
-            ++i;
-            continue;
-        }
-        int e = i + 1, to = sm.to[w][k];
-        while (e < 2 * WARPS && (!sm.ptr[e >> 1][e & 1] || sm.seg_start[e >> 1][e & 1] == sm.seg_start[w][k])) {
-            if (sm.ptr[e >> 1][e & 1]) to = sm.to[e >> 1][e & 1];
-            ++e;
-        }
-        const bool whole = sm.from[w][k] == 0 && to == sm.len_t[w][k];
-        const Seq s = load_seq<NT>(a, sm.b[w][k], group);
-        const int head = sm.head[w][k], r0 = sm.chunk[w][k] * 8 * NT;
-        float *part = parts + ((size_t)blockIdx.x * 2 + (sm.seg_start[w][k] > cta0 ? 1 : 0)) * PART;
-        for (int item = tid; item < 8 * NT * D / 4; item += WARPS * 32) {
-            const int r = item / (D / 4), d = item % (D / 4) * 4;
-            float m = -INFINITY, l = 0.f;
-            for (int x = i; x < e; ++x)
-                if (const float *p = sm.ptr[x >> 1][x & 1]) m = fmaxf(m, p[8 * NT * D + r]);
-            const float base = m == -INFINITY ? 0.f : m;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int x = i; x < e; ++x)
-                if (const float *p = sm.ptr[x >> 1][x & 1]) {
-                    const float f = exp2_approx(p[8 * NT * D + r] - base);
-                    const float4 v = *reinterpret_cast<const float4 *>(p + r * D + d);
-                    l = fmaf(p[8 * NT * D + 8 * NT + r], f, l);
-                    o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
-                }
-            if (whole) {
-                if (r0 + r < s.m * group) store_out(a, row_index(a, s, head, group, r0 + r), D, d, o, m, l);
-            } else {
-                *reinterpret_cast<float4 *>(part + r * D + d) = o;
-                if (d == 0) {
-                    part[8 * NT * D + r] = m;
-                    part[8 * NT * D + 8 * NT + r] = l;
-                }
-            }
-        }
-        i = e;
-    }
 }
 
-// One CTA per (query token, head): joins the partials of a row that more than
-// one CTA took part in; the warps take every fourth each, and the four sums
-// are added in order. Also writes the rows of sequences with no token to see.
-constexpr int JOIN_WARPS = 4;
+// Joins the partials of the (sequence, KV head, rows) that more than one share
+// took part in, and writes the rows of sequences with no token to see. A CTA
+// has some rows of one of them (blockIdx.x; rows blockIdx.y * blockDim.z on),
+// W = blockDim.y warps a row: each takes every W-th partial, JOIN_AHEAD loads at
+// a time, and their results are joined in order. (The partials are fresh from
+// other SMs: a round of loads takes some 2 us, and so few of them is what counts.)
+constexpr int JOIN_WARPS = 16, JOIN_AHEAD = 6;
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * JOIN_WARPS) attn_join_kernel(const AttnArgs a, const uint8_t *ws, int split_ctas) {
+__global__ void __launch_bounds__(32 * JOIN_WARPS)
+    attn_join_kernel(const AttnArgs a, const uint8_t *ws, int split_ctas, int chunks) {
     constexpr int PART = part_floats(D, 8 * NT), E = D / 32;
-    __shared__ float sh_l[JOIN_WARPS];
+    __shared__ float sh_m[JOIN_WARPS], sh_l[JOIN_WARPS];
     __shared__ __align__(16) float sh_o[JOIN_WARPS][D];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = a.n_q / a.c.n_kv;
-    const int64_t row = blockIdx.x;
-    const int tok = (int)(row / a.n_q), h = (int)(row % a.n_q);
-    // The call's own inputs were complete before the split kernel let this one start. The token's sequence: a guess that
-    // holds where all have the same number of tokens, else the last that begins at or before it (a sequence without
-    // tokens begins where the next one does).
-    int lo = (int)((int64_t)tok * a.B / a.total_q);
-    if (a.q_offsets[lo] > tok || a.q_offsets[lo + 1] <= tok) {
-        lo = 0;
-        int hi = a.B;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (a.q_offsets[mid] <= tok)
-                lo = mid;
-            else
-                hi = mid;
-        }
-    }
-    const Seq s = load_seq<NT>(a, lo, group);
+    const int lane = threadIdx.x, warp = threadIdx.y, W = blockDim.y, group = a.n_q / a.c.n_kv;
+    const int r = blockIdx.y * blockDim.z + threadIdx.z;  // of the 8 * NT
+    const int b = blockIdx.x / (a.c.n_kv * chunks), head = blockIdx.x / chunks % a.c.n_kv;
+    // the call's own inputs were complete before the split kernel let this one start
+    const Seq s = load_seq<NT>(a, b, group);
     pdl_acquire();
-    if (tok < s.first || tok >= s.first + s.m) return;  // a row of no sequence
-    if (s.T == 0) {
-        if (threadIdx.x < D / 4)
-            store_out(a, row, D, threadIdx.x * 4, make_float4(0.f, 0.f, 0.f, 0.f), 0.f, 0.f);
-        return;
-    }
-    const int64_t *prefix = reinterpret_cast<const int64_t *>(ws);
-    const float *parts = reinterpret_cast<const float *>(ws + prefix_bytes(a.B));
-    const int64_t total = prefix[a.B], n_cta = min((int64_t)split_ctas, (total + WARPS - 1) / WARPS);
-    const int rr = (tok - s.first) * group + h % group, r = rr % (8 * NT);
-    const int64_t s0 = prefix[lo] + ((int64_t)(h / group) * s.nrc + rr / (8 * NT)) * (s.T + OPEN);
-    const int64_t nw = n_cta * WARPS;
-    const int c0 = (int)(share_of(s0 + OPEN, nw, total) / WARPS);
-    const int c1 = (int)(share_of(s0 + OPEN + s.T - 1, nw, total) / WARPS);
-    if (c0 == c1) return;  // that CTA wrote it
-    // the first CTA's partial is its second one if the row begins inside its share
-    const bool inside = s0 > share_start((int64_t)c0 * WARPS, nw, total);
-    auto at = [&](int c) { return parts + (size_t)(2 * c + (c == c0 && inside ? 1 : 0)) * PART; };
-    float m = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, at(c)[8 * NT * D + r]);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float base = m == -INFINITY ? 0.f : m;
-    float o[E] = {}, l = 0.f;
-#pragma unroll 4
-    for (int c = c0 + warp; c <= c1; c += JOIN_WARPS) {
-        const float *p = at(c);
-        const float f = exp2_approx(p[8 * NT * D + r] - base);
-        l = fmaf(p[8 * NT * D + 8 * NT + r], f, l);
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(p[r * D + lane * E + e], f, o[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) sh_o[warp][lane * E + e] = o[e];
-    if (lane == 0) sh_l[warp] = l;
-    __syncthreads();
-    if (threadIdx.x < D / 4) {
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        l = 0.f;
-#pragma unroll
-        for (int w = 0; w < JOIN_WARPS; ++w) {
-            const float4 v = *reinterpret_cast<const float4 *>(&sh_o[w][threadIdx.x * 4]);
-            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
-            l += sh_l[w];
+    const int n = s.m * group;
+    // (one chunk, unless a sequence has more queries than the call said)
+    for (int r0 = (int)(blockIdx.x % chunks) * 8 * NT; r0 < n; r0 += chunks * 8 * NT) {
+        const bool mine = r < 8 * NT && r0 + r < n;
+        const int64_t row = mine ? row_index(a, s, head, group, r0 + r) : 0;
+        if (s.T == 0) {
+            if (mine && warp == 0 && lane < D / 4)
+                store_out(a, row, D, lane * 4, make_float4(0.f, 0.f, 0.f, 0.f), 0.f, 0.f);
+            continue;
         }
-        store_out(a, row, D, threadIdx.x * 4, sum, m, l);
+        const int64_t *prefix = reinterpret_cast<const int64_t *>(ws);
+        const float *parts = reinterpret_cast<const float *>(ws + prefix_bytes(a.B));
+        const int64_t total = prefix[a.B], nw = shares(total, split_ctas);
+        const int64_t s0 = prefix[b] + ((int64_t)head * s.nrc + r0 / (8 * NT)) * (s.T + OPEN);
+        const int w0 = (int)share_of(s0 + OPEN, nw, total), w1 = (int)share_of(s0 + OPEN + s.T - 1, nw, total);
+        if (w0 == w1) continue;  // that share's warp wrote it
+        // the first share's partial is its second one if the row begins inside it
+        const bool inside = s0 > share_start(w0, nw, total);
+        float m = -INFINITY, l = 0.f, o[E] = {};
+        for (int w = w0 + warp; mine && w <= w1; w += W * JOIN_AHEAD) {
+            float pm[JOIN_AHEAD], pl[JOIN_AHEAD], po[JOIN_AHEAD][E];
+#pragma unroll
+            for (int y = 0; y < JOIN_AHEAD; ++y) {
+                const int x = w + y * W;
+                const float *p = parts + ((size_t)2 * x + (x == w0 && inside ? 1 : 0)) * PART;
+                pm[y] = x <= w1 ? p[8 * NT * D + r] : -INFINITY;
+                pl[y] = x <= w1 ? p[8 * NT * D + 8 * NT + r] : 0.f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) po[y][e] = 0.f;
+                if (x <= w1) {
+                    if constexpr (E == 4)
+                        *reinterpret_cast<float4 *>(po[y]) = *reinterpret_cast<const float4 *>(p + r * D + lane * E);
+                    else
+                        *reinterpret_cast<float2 *>(po[y]) = *reinterpret_cast<const float2 *>(p + r * D + lane * E);
+                }
+            }
+            float now = m;
+#pragma unroll
+            for (int y = 0; y < JOIN_AHEAD; ++y) now = fmaxf(now, pm[y]);
+            const float base = now == -INFINITY ? 0.f : now, keep = exp2_approx(m - base);
+            l *= keep;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] *= keep;
+#pragma unroll
+            for (int y = 0; y < JOIN_AHEAD; ++y) {
+                const float f = exp2_approx(pm[y] - base);
+                l = fmaf(pl[y], f, l);
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = fmaf(po[y][e], f, o[e]);
+            }
+            m = now;
+        }
+        const int slot = threadIdx.z * W;
+#pragma unroll
+        for (int e = 0; e < E; ++e) sh_o[slot + warp][lane * E + e] = o[e];
+        if (lane == 0) {
+            sh_m[slot + warp] = m;
+            sh_l[slot + warp] = l;
+        }
+        __syncthreads();
+        if (mine && warp == 0 && lane < D / 4) {
+            m = -INFINITY;
+            for (int w = 0; w < W; ++w) m = fmaxf(m, sh_m[slot + w]);
+            const float base = m == -INFINITY ? 0.f : m;
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+            l = 0.f;
+            for (int w = 0; w < W; ++w) {
+                const float f = exp2_approx(sh_m[slot + w] - base);
+                const float4 v = *reinterpret_cast<const float4 *>(&sh_o[slot + w][lane * 4]);
+                sum.x = fmaf(v.x, f, sum.x), sum.y = fmaf(v.y, f, sum.y), sum.z = fmaf(v.z, f, sum.z), sum.w = fmaf(v.w, f, sum.w);
+                l = fmaf(sh_l[slot + w], f, l);
+            }
+            store_out(a, row, D, lane * 4, sum, m, l);
+        }
+        __syncthreads();
     }
 }
 
@@ -875,6 +822,8 @@ int launch(const AttnArgs &a, int max_q, int sms, void *ws, cudaStream_t s) {
     const int64_t nrc = ((int64_t)max_q * group + 8 * NT - 1) / (8 * NT);
     const int64_t tiles = (((int64_t)a.max_pages << a.c.page_shift) + TILE - 1) / TILE;
     const double most = (double)a.B * a.c.n_kv * nrc * (tiles + OPEN) / WARPS + 1;
+    const int64_t units = (int64_t)a.B * a.c.n_kv * nrc;
+    PQE_CHECK_ARG(units <= INT32_MAX);
     int grid = sms * ctas(D, NT);
     if (most < grid) grid = (int)most;
     static bool set[PQE_MAX_DEVICES] = {};
@@ -889,25 +838,36 @@ int launch(const AttnArgs &a, int max_q, int sms, void *ws, cudaStream_t s) {
     rc = launch_pdl(attn_split_kernel<D, NT>, dim3((unsigned)grid), dim3(WARPS * 32), smem, s, a,
                     static_cast<uint8_t *>(ws));
     if (rc != PQE_OK) return rc;
-    return launch_pdl(attn_join_kernel<D, NT>, dim3((unsigned)((int64_t)a.total_q * a.n_q)), dim3(32 * JOIN_WARPS), 0, s, a,
-                      static_cast<const uint8_t *>(ws), grid);
+    // as few warps a row as take a mean number of partials in one round; eight warps a CTA, or one row's
+    const int64_t per_row = (int64_t)grid * WARPS / units + 1;
+    const int W = (int)(per_row < 5 * JOIN_WARPS ? (per_row + 4) / 5 : JOIN_WARPS), rows = W < 8 ? 8 / W : 1;
+    return launch_pdl(attn_join_kernel<D, NT>, dim3((unsigned)units, (unsigned)((8 * NT + rows - 1) / rows)), dim3(32, W, rows),
+                      0, s, a, static_cast<const uint8_t *>(ws), grid, (int)nrc);
 }
 
 }  // namespace split
 
-// Rows of a KV head taken together: 8 where a step has no more, else 16.
+// Rows of a KV head taken together, in eights: as few as hold a step's, and what registers allow. A sequence's cache is read
+// once for each such set of its rows.
+static int eights(int max_q, int group, int d) {
+    const int64_t rows = (int64_t)max_q * group;
+    return rows <= 8 ? 1 : rows <= 16 || d == 128 ? 2 : rows <= 24 ? 3 : 2;
+}
+
 size_t attn_split_ws(int B, int max_q, int group, int d) {
-    const int NT = (int64_t)max_q * group <= 8 ? 1 : 2;
+    const int NT = eights(max_q, group, d);
     int dev = 0, sms = 0;
     if (device_info(dev, sms) != PQE_OK) sms = 160;  // without a device: an upper bound
     return split::prefix_bytes(B) +
-           (size_t)sms * split::ctas(d, NT) * (2 + split::WARPS) * split::part_floats(d, 8 * NT) * sizeof(float);
+           (size_t)sms * split::ctas(d, NT) * 2 * split::WARPS * split::part_floats(d, 8 * NT) * sizeof(float);
 }
 
 int attn_split(const pqe_kv_cache *cache, const AttnArgs &a, int max_q, int sms, void *ws, cudaStream_t s) {
-    const bool one = (int64_t)max_q * (a.n_q / a.c.n_kv) <= 8;
-    if (cache->d == 128) return one ? split::launch<128, 1>(a, max_q, sms, ws, s) : split::launch<128, 2>(a, max_q, sms, ws, s);
-    return one ? split::launch<64, 1>(a, max_q, sms, ws, s) : split::launch<64, 2>(a, max_q, sms, ws, s);
+    const int NT = eights(max_q, a.n_q / a.c.n_kv, cache->d);
+    if (cache->d == 128) return NT == 1 ? split::launch<128, 1>(a, max_q, sms, ws, s) : split::launch<128, 2>(a, max_q, sms, ws, s);
+    return NT == 1   ? split::launch<64, 1>(a, max_q, sms, ws, s)
+           : NT == 2 ? split::launch<64, 2>(a, max_q, sms, ws, s)
+                     : split::launch<64, 3>(a, max_q, sms, ws, s);
 }
 
 }  // namespace kv
