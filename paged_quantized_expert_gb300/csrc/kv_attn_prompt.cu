@@ -61,6 +61,7 @@ struct Smem {
     uint8_t v[2][2][D * 128];  // V^T: D rows of 64 tokens, two a step
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], drained;
     uint32_t tmem;
+    int scan[THREADS / 32];
     int seq, tile;             // what the CTA works on
     int k_top, v_top, v_nan;
     // of a step's 16-token blocks, two bits from each converting warp: those that are there. Four steps' worth: a
@@ -188,32 +189,40 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
     pdl_acquire();
 
     // ---- this CTA's sequence and rows: tiles of all sequences in one line, the last first (they see the most) ----
-    if (warp == 0) {
-        int total = 0;
-        for (int b0 = 0; b0 < a.B; b0 += 32) {
-            int first, m = 0, len;
-            if (b0 + lane < a.B) sequence_of(a, b0 + lane, first, m, len);
-            total += __reduce_add_sync(0xffffffffu, (int)(((int64_t)m * group + BM * TILES - 1) / (BM * TILES)));
+    {
+        const int per = (a.B + THREADS - 1) / THREADS, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+        auto tiles_of = [&](int b) {
+            int first, m, len;
+            sequence_of(a, b, first, m, len);
+            return (int)(((int64_t)m * group + BM * TILES - 1) / (BM * TILES));
+        };
+        int mine = 0;
+        for (int b = b0; b < b1; ++b) mine += tiles_of(b);
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        if (lane == 31) sm.scan[warp] = incl;
+        __syncthreads();
+        int total = 0, before = incl - mine;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) {
+            if (w < warp) before += sm.scan[w];
+            total += sm.scan[w];
         }
         const int want = total - 1 - (int)(blockIdx.x / a.c.n_kv);
-        int before = 0;
-        for (int b0 = 0; want >= 0 && b0 < a.B; b0 += 32) {
-            int first, m = 0, len;
-            if (b0 + lane < a.B) sequence_of(a, b0 + lane, first, m, len);
-            const int n = (int)(((int64_t)m * group + BM * TILES - 1) / (BM * TILES));
-            int incl = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int up = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += up;
+        if (want >= before && want < before + mine)
+            for (int b = b0; b < b1; ++b) {
+                const int n = per > 1 ? tiles_of(b) : mine;
+                if (want < before + n) {
+                    sm.seq = b;
+                    sm.tile = want - before;
+                    break;
+                }
+                before += n;
             }
-            if (want >= before + incl - n && want < before + incl) {
-                sm.seq = b0 + lane;
-                sm.tile = want - (before + incl - n);
-            }
-            before += __shfl_sync(0xffffffffu, incl, 31);
-            if (before > want) break;
-        }
     }
     __syncthreads();
     const int b = sm.seq;
@@ -740,7 +749,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
             }
             // every MMA has finished before TMEM is released
             commit(one, smem_u32(&sm.drained));
-            if (!mbar_wait(smem_u32(&sm.drained), 0, a.wait_limit)) ok = false;
+            if (!mbar_wait(smem_u32(&sm.drained), 0, DEFAULT_WAIT_LIMIT)) ok = false;  // whatever the limit of the others is
             if (!ok && lane == 0) atomicOr(a.status, PQE_STATUS_TIMEOUT);
         }
         __syncwarp();

@@ -645,7 +645,9 @@ __global__ void __launch_bounds__(WARPS * 32, ctas(D, NT)) attn_split_kernel(con
         const uint32_t ring = smem_u32(sm.ring[warp][0]), bar = smem_u32(&sm.full[warp][0]);
         uint32_t have[STAGES] = {};
         int page = ahead > 0 ? table_entry(a, f) : -1;
+        uint32_t fetched = 0;
         auto fetch_next = [&](int s) {
+            ++fetched;
             const uint32_t h = fetch<D>(a, f, page, ring + s * tile_bytes<D>(), bar + 8 * s, lane);
             f.j += TILE;
             if (--ahead == rows_end && ahead > 0) {
@@ -708,10 +710,11 @@ __global__ void __launch_bounds__(WARPS * 32, ctas(D, NT)) attn_split_kernel(con
             }
         }
         if (!ok) {
-            // the copies in flight land before the block ends (bounded)
+            // the copies in flight land before the block ends (bounded, whatever the limit of the other waits is)
+#pragma unroll
             for (int s = 0; s < STAGES; ++s) {
-                mbar_wait(bar + 8 * s, 0, a.wait_limit);
-                mbar_wait(bar + 8 * s, 1, a.wait_limit);
+                const uint32_t n = (fetched + STAGES - 1 - s) / STAGES;  // copies into this stage
+                if (n) mbar_wait(bar + 8 * s, (n - 1) & 1u, DEFAULT_WAIT_LIMIT);
             }
             if (lane == 0) atomicOr(a.status, PQE_STATUS_TIMEOUT);
         }

@@ -347,3 +347,33 @@ def test_few_and_many_rows_agree(cuda_lib):
         single.mem, single.cache, single.table = c.mem, c.cache, c.table
         got, gl = single.run()
         compare(got, gl, o[[i, 40 + i]], a[[i, 40 + i]], l[[i, 40 + i]], floor(c.kv()))
+
+
+@pytest.mark.parametrize("m", [1, 3, 100])
+def test_waits_that_run_out(cuda_lib, m):
+    """With a limit of one poll the waits for data give up before it is there (or, rarely, just find it): the call comes back,
+    says so in its status, and the next call is right."""
+    pqe = cuda_lib
+    c = Case(pqe, [m, m], [2000, 3000], 8, 2, 128, 16)
+    want, l = c.run()
+    try:
+        assert pqe.lib().pqe_set_wait_limit(1) == 0
+        out, _ = c.run()
+        torch.cuda.synchronize()
+    finally:
+        pqe.lib().pqe_set_wait_limit(0)
+    assert c.status.item() in (0, pqe.PQE_STATUS_TIMEOUT)
+    if c.status.item() == 0:
+        assert torch.equal(out, want)
+    c.status.zero_()
+    again, l2 = c.run()
+    assert c.status.item() == 0 and torch.equal(again, want) and torch.equal(l2, l)
+
+
+def test_many_prompts_in_one_call(cuda_lib):
+    """More sequences than a block has threads, with and without queries, in the kernel for many rows."""
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 60, (1100,), generator=g).tolist()
+    ms = [min(int(x), n) if i % 3 else 0 for i, (x, n) in enumerate(zip(torch.randint(0, 40, (1100,), generator=g), lens))]
+    ms[500], lens[500] = 70, 80
+    Case(cuda_lib, ms, lens, 2, 1, 64, 16).check()
