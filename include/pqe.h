@@ -677,8 +677,9 @@ PQE_API int kv_cache_read(const pqe_kv_cache *cache, const int64_t *slots, int n
  *          16-byte aligned, q_stride a multiple of 8 and at least n_q * d
  * q_offsets device int32 [B + 1], ascending from 0 or more, at most total_q
  * kv_lens  device int32 [B]; block_table device int32 [B, max_pages]
- * max_q    the largest m (it chooses the kernel; the lengths themselves are
- *          read on the device, so a captured call follows them)
+ * max_q    the largest m (it chooses the kernel and sizes the launch; the
+ *          lengths themselves are read on the device, so a captured call
+ *          follows them)
  * out      device bf16 [total_q, n_q, d], 16-byte aligned; rows of no
  *          sequence are left as they are
  * lse      device fp32 [total_q, n_q] or NULL: ln sum_j exp(s_j)
@@ -690,6 +691,11 @@ PQE_API int kv_cache_read(const pqe_kv_cache *cache, const int64_t *slots, int n
  *          (cut); PQE_STATUS_TIMEOUT as elsewhere
  * Limits: n_q a multiple of n_kv, n_q <= 1024; B >= 0, total_q >= 0 (either 0:
  * a no-op); total_q * n_q and max_pages * page_size below 2^31; scale finite. */
+/* (pqe_test_set_attention_kernel: a test hook, which kernel the call takes
+ * whatever its sizes: 1 the one for few query rows, 2 the one for many, 0 the
+ * default choice. Both compute the same; only rounding differs, inside the
+ * stated precision. Process-wide, read at each call and workspace query.) */
+PQE_API int pqe_test_set_attention_kernel(int kind);
 PQE_API size_t kv_paged_attention_workspace_size(int B, int total_q, int max_q, int n_q, int n_kv, int d);
 PQE_API int kv_paged_attention(const pqe_kv_cache *cache, const void *q, int64_t q_stride, const int32_t *q_offsets,
                                const int32_t *kv_lens, const int32_t *block_table, int max_pages, int B, int total_q,

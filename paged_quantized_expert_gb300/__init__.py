@@ -143,6 +143,7 @@ _SIGS = {
     "pqe_kv_page_bytes": (SZ, [I32, I32, I32]),
     "kv_cache_write": (I32, [C.POINTER(pqe_kv_cache), P, P, C.c_int64, C.c_int64, P, I32, P, P]),
     "kv_cache_read": (I32, [C.POINTER(pqe_kv_cache), P, I32, P, P, P, P]),
+    "pqe_test_set_attention_kernel": (I32, [I32]),
     "kv_paged_attention_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32]),
     "kv_paged_attention": (I32, [C.POINTER(pqe_kv_cache), P, C.c_int64, P, P, P, I32, I32, I32, I32, I32, C.c_float,
                                  I32, I32, P, P, P, SZ, P, P]),
@@ -400,6 +401,11 @@ def kv_cache_read(cache: pqe_kv_cache, slots, k, v, status, stream=None):
     vp = None if v is None else _typed(v, torch.bfloat16, "v", size)
     _check("kv_cache_read", lib().kv_cache_read(C.byref(cache), _typed(slots, torch.int64, "slots", n), n, kp, vp,
                                                 _ptr(status), _stream(stream)))
+
+
+def pqe_test_set_attention_kernel(kind: int):
+    """Test hook: 1 the kernel for few query rows, 2 the one for many, 0 the default choice."""
+    _check("pqe_test_set_attention_kernel", lib().pqe_test_set_attention_kernel(int(kind)))
 
 
 def kv_paged_attention_workspace_size(B: int, total_q: int, max_q: int, n_q: int, n_kv: int, d: int) -> int:

@@ -19,7 +19,13 @@ struct AttnArgs {
     float *lse;
     int32_t *status;
     uint32_t wait_limit;
+    int rows_min, rows_max;  // sequences with that many query rows (m * group) are this kernel's; the others are skipped
 };
+
+__device__ __forceinline__ bool is_ours(const AttnArgs &a, int m) {
+    const int64_t rows = (int64_t)m * (a.n_q / a.c.n_kv);
+    return rows >= a.rows_min && rows <= a.rows_max;
+}
 
 // sequence b's first query row, query tokens and cached tokens, held to what
 // the arguments describe

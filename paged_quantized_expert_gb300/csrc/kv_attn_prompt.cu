@@ -194,6 +194,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
         auto tiles_of = [&](int b) {
             int first, m, len;
             sequence_of(a, b, first, m, len);
+            if (!is_ours(a, m)) return 0;
             return (int)(((int64_t)m * group + BM * TILES - 1) / (BM * TILES));
         };
         int mine = 0;

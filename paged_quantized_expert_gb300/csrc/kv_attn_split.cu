@@ -68,7 +68,7 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs &a, int b, int group) {
     int hi;
     visible(a, 0, s.m, s.len, s.lo, hi);
     s.t0 = min(s.lo, s.len) / TILE;
-    s.T = s.m > 0 ? (s.len + TILE - 1) / TILE - s.t0 : 0;
+    s.T = is_ours(a, s.m) ? (s.len + TILE - 1) / TILE - s.t0 : 0;
     return s;
 }
 
@@ -740,7 +740,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS)
     // the call's own inputs were complete before the split kernel let this one start
     const Seq s = load_seq<NT>(a, b, group);
     pdl_acquire();
-    const int n = s.m * group;
+    const int n = is_ours(a, s.m) ? s.m * group : 0;
     // (one chunk, unless a sequence has more queries than the call said)
     for (int r0 = (int)(blockIdx.x % chunks) * 8 * NT; r0 < n; r0 += chunks * 8 * NT) {
         const bool mine = r < 8 * NT && r0 + r < n;

@@ -17,6 +17,20 @@ DEV = "cuda"
 U = 2.0 ** -8
 
 
+@pytest.fixture(autouse=True, params=["few", "many", "choice"])
+def kernel(request, cuda_lib):
+    """Every case on the kernel for few query rows, on the one for many, and on the library's choice."""
+    if request.param == "choice" and request.node.originalname not in CHOSEN:
+        pytest.skip("the two kernels themselves cover it")
+    cuda_lib.pqe_test_set_attention_kernel({"few": 1, "many": 2, "choice": 0}[request.param])
+    yield request.param
+    cuda_lib.pqe_test_set_attention_kernel(0)
+
+
+CHOSEN = ("test_single_tokens_beside_a_prompt", "test_other_stream_and_graph_follow_the_lengths", "test_many_sequences",
+          "test_max_q_only_chooses_the_kernel")
+
+
 class Case:
     """Sequences in a paged cache whose every other byte is 0xFF: scales of NaN where no token was written."""
 
@@ -334,8 +348,8 @@ def test_pages_before_the_window_may_be_gone(cuda_lib, m):
     assert torch.equal(out, want) and c.status.item() == 0
 
 
-def test_few_and_many_rows_agree(cuda_lib):
-    """The same queries as one call of 40 a sequence and as calls of one: two kernels, one bound."""
+def test_one_call_and_single_tokens_agree(cuda_lib):
+    """The same queries as one call of 40 a sequence and as calls of one."""
     c = Case(cuda_lib, [40, 40], [300, 70], 8, 2, 64, 16)
     o, a, l = ref.attend(c.q, c.ms, c.lens, c.kv(), c.scale)
     out, lse = c.run()
@@ -377,3 +391,18 @@ def test_many_prompts_in_one_call(cuda_lib):
     ms = [min(int(x), n) if i % 3 else 0 for i, (x, n) in enumerate(zip(torch.randint(0, 40, (1100,), generator=g), lens))]
     ms[500], lens[500] = 70, 80
     Case(cuda_lib, ms, lens, 2, 1, 64, 16).check()
+
+
+@pytest.mark.parametrize("n_q,n_kv,d", [(8, 2, 128), (16, 1, 64), (4, 4, 64)])
+def test_single_tokens_beside_a_prompt(cuda_lib, n_q, n_kv, d):
+    """One call with a prompt's chunk and sequences of one and a few tokens, of long and empty ones. (On the library's choice:
+    both kernels, each with its own sequences.)"""
+    ms = [1, 1050, 1, 0, 2, 1, 1, 17, 1, 3, 1, 1]
+    lens = [700, 1100, 1, 30, 65, 0, 1300, 17, 64, 2, 129, 512]
+    Case(cuda_lib, ms, lens, n_q, n_kv, d, 16, seed=d).check()
+    Case(cuda_lib, ms, lens, n_q, n_kv, d, 32, seed=d + 1).check(window=100)
+
+
+def test_kernel_hook_rejects_unknown_kind(cuda_lib):
+    with pytest.raises(cuda_lib.PqeError):
+        cuda_lib.pqe_test_set_attention_kernel(3)
