@@ -16,23 +16,30 @@ static std::atomic<int> g_kernel{0};  // pqe_test_set_attention_kernel
 struct Choice {
     bool few, many;
     int few_rows, few_q;  // the split kernel's bounds on rows and on m
+    int splits;           // the prompt kernel's parts of a tile pair
 };
+constexpr int MIXED_ROWS = 64;
+static int mixed_q(int64_t group) { return (int)(MIXED_ROWS / group > 0 ? MIXED_ROWS / group : 1); }
 
-// The split kernel's time goes with the 16-row sets of all (sequence, head), whose tiles it spreads over all SMs; the prompt
-// kernel's with the CTAs of 256 rows that an SM gets, each a whole sequence long. Measured at equal lengths: a set's tile
-// of 64 tokens takes 1/430 us of the chip (heads of 64: 1/630), a CTA's step of 128 tokens 1.9 us, so that the split
-// kernel is faster below sets * 16 = 5700 (8400) rows for each CTA of an SM. (1 sequence of 8192 tokens, 4 heads of 128,
-// 256 rows: 30 us and 130 us; 8 of 2000, 4 heads, 128 rows: 33 and 36, 192 rows: 43 and 43; 64 of 4000, 4 heads, 48 rows:
-// 130 and 127, 64 rows: 167 and 127; 32 of 4000, 8 heads of 64, 48 rows: 87 and 94, 64 rows: 112 and 94.)
-static Choice choose(int B, int total_q, int max_q, int n_q, int n_kv, int d, int sms) {
-    const int64_t group = n_q / n_kv, rows = (int64_t)max_q * group, most = d == 128 ? 5700 : 8400;
-    const int64_t pairs = (int64_t)B * n_kv, per_sm = (pairs * ((rows + 255) / 256) + sms - 1) / sms;
+// Estimates in us, for sequences as long as the block table describes, from the measurements below. The split kernel: 10,
+// and 1/400 for each 16 rows and 64 tokens of a (sequence, head), which it spreads over all SMs (heads of 64: 1/550). The
+// prompt kernel: 11, 9 more where its tile pairs are cut into parts, and 1.9 for each of an SM's steps of 128 tokens (1.5
+// where a sequence has one tile of 128 rows); a prompt's own tokens see half of each other.
+// (m queries over L tokens of B sequences; split kernel, prompt kernel: 1 x 8192, 4 heads of 128, 128 rows: 22, 27; 256
+// rows: 30, 32; 512: 48, 36. 8 x 2000, 4 of 128, 64 rows: 22, 26; 128: 33, 27. 64 x 4000, 4 of 128, 32 rows: 92, 138; 64:
+// 167, 140. 32 x 4000, 8 of 64, 32 rows: 60, 96; 64: 111, 97. 1 x 1000, 4 of 128, 256 rows: 15, 26; 2048: 39, 25.)
+static Choice choose(int B, int total_q, int max_q, int n_q, int n_kv, int d, int64_t tokens, int sms) {
+    const int64_t group = n_q / n_kv, rows = (int64_t)max_q * group, pairs = (int64_t)B * n_kv;
     const int kind = g_kernel.load(std::memory_order_relaxed);
-    if (kind == 2) return {false, true, 0, 0};
-    const bool many = kind == 0 && rows > 16 && pairs * rows > most * per_sm;
-    const bool mixed = many && (int64_t)total_q * 4 < (int64_t)B * max_q;
-    if (!many) return {true, false, INT32_MAX, max_q};
-    return {mixed, true, 64, (int)(64 / group > 0 ? 64 / group : 1)};
+    const int splits = prompt_splits(B, total_q, n_q, n_kv, tokens, sms);
+    if (kind == 2) return {false, true, 0, 0, splits};
+    if (kind == 1 || rows <= 16) return {true, false, INT32_MAX, max_q, 1};
+    const double t_split = 10 + (double)pairs * ((rows + 15) / 16) * ((double)tokens / 64) / (d == 128 ? 400 : 550);
+    const int64_t per_sm = (pairs * ((rows + 255) / 256) * splits + sms - 1) / sms;
+    const double seen = 1 - 0.5 * (max_q < tokens ? (double)max_q / tokens : 1);
+    const double t_prompt = 11 + (splits > 1 ? 9 : 0) + (double)per_sm * tokens / 128 / splits * seen * (rows > 128 ? 1.9 : 1.5);
+    if (t_split <= t_prompt) return {true, false, INT32_MAX, max_q, 1};
+    return {(int64_t)total_q * 4 < (int64_t)B * max_q, true, MIXED_ROWS, mixed_q(group), splits};
 }
 
 }  // namespace kv
@@ -53,8 +60,16 @@ size_t kv_paged_attention_workspace_size(int B, int total_q, int max_q, int n_q,
         return 0;
     int dev = 0, sms = 0;
     if (device_info(dev, sms) != PQE_OK) sms = 152;
-    const kv::Choice use = kv::choose(B, total_q, max_q, n_q, n_kv, d, sms);
-    return use.few ? kv::attn_split_ws(B, use.few_q, n_q / n_kv, d) : 256;
+    // whatever the call chooses; where it takes both kernels, one runs after the other
+    const int64_t group = n_q / n_kv;
+    size_t n = kv::attn_split_ws(B, max_q, (int)group, d);
+    if (max_q * group > 16 || kv::g_kernel.load(std::memory_order_relaxed) == 2) {
+        const size_t mixed = kv::attn_split_ws(B, kv::mixed_q(group), (int)group, d);
+        const size_t many = kv::attn_prompt_ws(B, total_q, n_q, n_kv, d, sms);
+        n = n > mixed ? n : mixed;
+        n = n > many ? n : many;
+    }
+    return n;
 }
 
 int kv_paged_attention(const pqe_kv_cache *cache, const void *q, int64_t q_stride, const int32_t *q_offsets,
@@ -73,13 +88,14 @@ int kv_paged_attention(const pqe_kv_cache *cache, const void *q, int64_t q_strid
     int dev = 0, sms = 0;
     const int rc = device_info(dev, sms);
     if (rc != PQE_OK) return rc;
-    const kv::Choice use = kv::choose(B, total_q, max_q, n_q, cache->n_kv, cache->d, sms);
+    const kv::Choice use =
+        kv::choose(B, total_q, max_q, n_q, cache->n_kv, cache->d, (int64_t)max_pages * cache->page_size, sms);
     kv::AttnArgs a{kv::cache_of(cache), static_cast<const uint16_t *>(q), q_stride, q_offsets, kv_lens, block_table, max_pages,
                    B, total_q, n_q, causal, window, scale * 1.44269504088896341f, static_cast<uint16_t *>(out), lse, status,
                    wait_limit(), 1, INT32_MAX};
     if (use.many) {
         if (use.few) a.rows_min = use.few_rows + 1;
-        const int rc2 = kv::attn_prompt(cache, a, as_stream(stream));
+        const int rc2 = kv::attn_prompt(cache, a, use.splits, ws, as_stream(stream));
         if (rc2 != PQE_OK || !use.few) return rc2;
         a.rows_min = 1;
         a.rows_max = use.few_rows;

@@ -84,7 +84,9 @@ __device__ __forceinline__ float v_factor(uint32_t r) {
 }
 
 int attn_split(const pqe_kv_cache *cache, const AttnArgs &a, int max_q, int sms, void *ws, cudaStream_t s);
-int attn_prompt(const pqe_kv_cache *cache, const AttnArgs &a, cudaStream_t s);
+int attn_prompt(const pqe_kv_cache *cache, const AttnArgs &a, int splits, void *ws, cudaStream_t s);
+size_t attn_prompt_ws(int B, int total_q, int n_q, int n_kv, int d, int sms);
+int prompt_splits(int B, int total_q, int n_q, int n_kv, int64_t tokens, int sms);
 size_t attn_split_ws(int B, int max_q, int group, int d);
 
 }  // namespace kv

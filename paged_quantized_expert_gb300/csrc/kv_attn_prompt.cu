@@ -20,6 +20,10 @@
 // tokens have: exact while a scale is within 21 of it. Both tiles use what is
 // converted once.
 //
+// Where the tiles are fewer than SMs, each is cut along the cache into equal
+// parts for several CTAs, which leave theirs in the workspace for a second kernel
+// to join.
+//
 // Bound by the tensor pipe (2 * 1024 clocks a step at d = 128) with the exponentials
 // and the conversions close behind on the issue slots.
 #include <math.h>
@@ -54,6 +58,13 @@ __device__ __forceinline__ constexpr uint32_t p_col(int tile) {  // P: half a co
     return D == 128 ? s_col(tile) : o_col(tile) + 64;
 }
 
+template <int N>
+struct Find {  // find_tiles()'s scratch
+    static_assert(N % 32 == 0, "whole warps");
+    int scan[N / 32];
+    int2 found;
+};
+
 template <int D>
 struct Smem {
     alignas(1024) uint8_t q[TILES][D / 64][CHUNK];  // [128-byte rows of 64 channels]
@@ -61,8 +72,7 @@ struct Smem {
     uint8_t v[2][2][D * 128];  // V^T: D rows of 64 tokens, two a step
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], drained;
     uint32_t tmem;
-    int scan[THREADS / 32];
-    int seq, tile;             // what the CTA works on
+    Find<THREADS> find;
     int k_top, v_top, v_nan;
     // of a step's 16-token blocks, two bits from each converting warp: those that are there. Four steps' worth: a
     // step's is rewritten only once the softmax of the step three before has ended.
@@ -161,12 +171,61 @@ __device__ __forceinline__ float unweight(int top) {
     return __uint_as_float(top > 7 ? (uint32_t)(top - 7) << 23 : 1u << (top + 15));
 }
 
-template <int D>
-__global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs a) {
+// The sequence and tile pair of place `at` in the line of all sequences' tile pairs, counted from its end (the last of a
+// sequence see the most tokens, and go first); .x < 0 past its beginning. For all N threads of a block.
+template <int N>
+__device__ __forceinline__ int2 find_tiles(const AttnArgs &a, int at, Find<N> &sm) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = a.n_q / a.c.n_kv;
+    const int per = (a.B + N - 1) / N, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    auto tiles_of = [&](int b) {
+        int first, m, len;
+        sequence_of(a, b, first, m, len);
+        if (!is_ours(a, m)) return 0;
+        return (int)(((int64_t)m * group + BM * TILES - 1) / (BM * TILES));
+    };
+    if (tid == 0) sm.found = make_int2(-1, 0);
+    int mine = 0;
+    for (int b = b0; b < b1; ++b) mine += tiles_of(b);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) sm.scan[warp] = incl;
+    __syncthreads();
+    int total = 0, before = incl - mine;
+#pragma unroll
+    for (int w = 0; w < N / 32; ++w) {
+        if (w < warp) before += sm.scan[w];
+        total += sm.scan[w];
+    }
+    const int want = total - 1 - at;
+    if (want >= before && want < before + mine)
+        for (int b = b0; b < b1; ++b) {
+            const int n = per > 1 ? tiles_of(b) : mine;
+            if (want < before + n) {
+                sm.found = make_int2(b, want - before);
+                break;
+            }
+            before += n;
+        }
+    __syncthreads();
+    return sm.found;
+}
+
+// A part's result for its 256 rows: O as [D / 4][row][4], then m and l of the rows, fp32
+constexpr int ROWS = BM * TILES;
+__host__ __device__ constexpr int part_floats(int d) { return ROWS * (d + 2); }
+
+// SPLIT: of `splits` CTAs of a tile pair each leaves a part (a kernel of its own, so that the other has its registers).
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs a, int n_splits, float *parts) {
+    const int splits = SPLIT ? n_splits : 1;
     extern __shared__ uint8_t smem_raw[];
     Smem<D> &sm = *reinterpret_cast<Smem<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int group = a.n_q / a.c.n_kv, head = blockIdx.x % a.c.n_kv;
+    const int group = a.n_q / a.c.n_kv, part_no = blockIdx.x % splits, head = blockIdx.x / splits % a.c.n_kv;
     constexpr uint32_t IDESC_S = (1u << 4) | ((uint32_t)(BK >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
     constexpr uint32_t IDESC_O = (1u << 4) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
 
@@ -181,64 +240,34 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
             mbar_init(smem_u32(&sm.o_full[i]), 1);
         }
         mbar_init(smem_u32(&sm.drained), 1);
-        sm.seq = -1;
         sm.k_top = sm.v_top = sm.v_nan = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
     pdl_acquire();
 
-    // ---- this CTA's sequence and rows: tiles of all sequences in one line, the last first (they see the most) ----
-    {
-        const int per = (a.B + THREADS - 1) / THREADS, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-        auto tiles_of = [&](int b) {
-            int first, m, len;
-            sequence_of(a, b, first, m, len);
-            if (!is_ours(a, m)) return 0;
-            return (int)(((int64_t)m * group + BM * TILES - 1) / (BM * TILES));
-        };
-        int mine = 0;
-        for (int b = b0; b < b1; ++b) mine += tiles_of(b);
-        int incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += up;
-        }
-        if (lane == 31) sm.scan[warp] = incl;
-        __syncthreads();
-        int total = 0, before = incl - mine;
-#pragma unroll
-        for (int w = 0; w < THREADS / 32; ++w) {
-            if (w < warp) before += sm.scan[w];
-            total += sm.scan[w];
-        }
-        const int want = total - 1 - (int)(blockIdx.x / a.c.n_kv);
-        if (want >= before && want < before + mine)
-            for (int b = b0; b < b1; ++b) {
-                const int n = per > 1 ? tiles_of(b) : mine;
-                if (want < before + n) {
-                    sm.seq = b;
-                    sm.tile = want - before;
-                    break;
-                }
-                before += n;
-            }
-    }
-    __syncthreads();
-    const int b = sm.seq;
+    // ---- this CTA's sequence and rows ----
+    const int2 found = find_tiles<THREADS>(a, (int)(blockIdx.x / ((uint32_t)splits * a.c.n_kv)), sm.find);
+    const int b = found.x;
     if (b < 0) return;
     int first, m, len;
     sequence_of(a, b, first, m, len);
     if (a.kv_lens[b] > len && tid == 0) atomicOr(a.status, PQE_STATUS_BAD_PAGE);
-    const int row0 = sm.tile * (BM * TILES), n_rows = m * group;
+    const int row0 = found.y * (BM * TILES), n_rows = m * group;
     const int tiles = row0 + BM < n_rows ? 2 : 1;
     // the tokens that some row of the CTA sees
     int lo, hi, lo_last, hi_last;
     visible(a, row0 / group, m, len, lo, hi);
     visible(a, (min(row0 + BM * TILES, n_rows) - 1) / group, m, len, lo_last, hi_last);
-    const int k_first = lo / BK * BK, k_end = max(hi_last, 0);
-    const int steps = k_end > k_first ? (k_end - k_first + BK - 1) / BK : 0;
+    int k_first = lo / BK * BK, k_end = max(hi_last, 0);
+    int steps = k_end > k_first ? (k_end - k_first + BK - 1) / BK : 0;
+    if constexpr (SPLIT) {
+        // this part's steps of them
+        const int from = (int)((int64_t)steps * part_no / splits), to = (int)((int64_t)steps * (part_no + 1) / splits);
+        k_end = min(k_end, k_first + to * BK);
+        k_first += from * BK;
+        steps = to - from;
+    }
     const int32_t *table = a.block_table + (size_t)b * a.max_pages;
     const int page_mask = (1 << a.c.page_shift) - 1;
 
@@ -508,7 +537,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
                 tc_fence_after();
                 uint32_t nan = 0;  // blocks of channels where the row sees a NaN
                 if (sm.v_nan && valid) {
-                    for (int j = my_lo; j < my_hi; ++j) {
+                    for (int j = max(my_lo, k_first); j < min(my_hi, k_end); ++j) {
                         const int page = table[j >> a.c.page_shift];
                         if (page < 0 || page >= a.c.n_pages) continue;
                         const uint8_t *blk = block_of<D>(a.c, page, j & page_mask, head);
@@ -516,7 +545,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
                         for (int G = 0; G < D / 32; ++G) nan |= (blk[v_scale<D>(j & 15, G)] == 255 ? 1u : 0u) << G;
                     }
                 }
-                const float inv = l == 0.f ? 0.f : unweight(v_top) / l;
+                const float inv = SPLIT ? unweight(v_top) : l == 0.f ? 0.f : unweight(v_top) / l;
 #pragma unroll
                 for (int ch = 0; ch < D / 32; ++ch) {
                     uint32_t o[32];
@@ -524,7 +553,17 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
                         tmem_ld32(tmem + lanes + o_col(tile) + 32 * ch, o);
                         tmem_ld_wait();
                     }
-                    if (valid) {
+                    if constexpr (SPLIT) {
+                        float4 *part = reinterpret_cast<float4 *>(parts + (size_t)blockIdx.x * part_floats(D));
+                        const float f = nan >> ch & 1 ? __uint_as_float(0x7FC00000u) : inv;
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            float v[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) v[y] = l == 0.f ? 0.f : __uint_as_float(o[4 * x + y]) * f;
+                            part[(8 * ch + x) * ROWS + tile * BM + r] = make_float4(v[0], v[1], v[2], v[3]);
+                        }
+                    } else if (valid) {
                         const float f = nan >> ch & 1 ? __uint_as_float(0x7FC00000u) : inv;
                         uint4 *dst = reinterpret_cast<uint4 *>(a.out + out_row * D + 32 * ch);
 #pragma unroll
@@ -541,7 +580,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
                         }
                     }
                 }
-                if (valid && a.lse) a.lse[out_row] = l == 0.f ? -INFINITY : (ref + log2f(l) - 8.f) * 0.693147180559945309f;
+                if constexpr (SPLIT) {
+                    float *ml = parts + (size_t)blockIdx.x * part_floats(D) + ROWS * D + tile * BM + r;
+                    ml[0] = ref;
+                    ml[ROWS] = l;
+                } else if (valid && a.lse) {
+                    a.lse[out_row] = l == 0.f ? -INFINITY : (ref + log2f(l) - 8.f) * 0.693147180559945309f;
+                }
             }
         }
     } else if (warp < MMA_WARP) {
@@ -761,31 +806,112 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
+// Joins the parts of a tile pair, 32 rows a CTA: a row per lane and an eighth of the channels per warp, then through shared
+// memory so that rows go out whole.
 template <int D>
-int launch(const AttnArgs &a, cudaStream_t s) {
+__global__ void __launch_bounds__(256) prompt_join_kernel(const AttnArgs a, int splits, const float *parts) {
+    constexpr int C4 = D / 32;  // groups of four channels that a warp takes
+    __shared__ Find<256> find;
+    __shared__ __align__(16) uint2 rows[32][D / 4 + 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = a.n_q / a.c.n_kv;
+    const int pair = blockIdx.x / a.c.n_kv, head = blockIdx.x % a.c.n_kv;
+    // the call's own inputs were complete before the first kernel let this one start
+    const int2 found = find_tiles<256>(a, pair, find);
+    pdl_acquire();
+    if (found.x < 0) return;
+    int first, m, len;
+    sequence_of(a, found.x, first, m, len);
+    const int r0 = blockIdx.y * 32, row0 = found.y * ROWS + r0, n_rows = m * group;
+    if (row0 >= n_rows) return;
+    const float *p = parts + (size_t)blockIdx.x * splits * part_floats(D);
+    float top = -INFINITY, l = 0.f;
+    float4 o[C4];
+#pragma unroll
+    for (int x = 0; x < C4; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < splits; ++s) top = fmaxf(top, p[(size_t)s * part_floats(D) + ROWS * D + r0 + lane]);
+    const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+        const float *q = p + (size_t)s * part_floats(D);
+        const float f = exp2_approx(q[ROWS * D + r0 + lane] - base);
+        l = fmaf(q[ROWS * D + ROWS + r0 + lane], f, l);
+#pragma unroll
+        for (int x = 0; x < C4; ++x) {
+            const float4 v = reinterpret_cast<const float4 *>(q)[(warp * C4 + x) * ROWS + r0 + lane];
+            o[x].x = fmaf(v.x, f, o[x].x), o[x].y = fmaf(v.y, f, o[x].y);
+            o[x].z = fmaf(v.z, f, o[x].z), o[x].w = fmaf(v.w, f, o[x].w);
+        }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int x = 0; x < C4; ++x) {
+        uint2 u;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.x) : "f"(o[x].y * inv), "f"(o[x].x * inv));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.y) : "f"(o[x].w * inv), "f"(o[x].z * inv));
+        rows[lane][warp * C4 + x] = u;
+    }
+    if (warp == 0 && a.lse && row0 + lane < n_rows) {
+        const int row = row0 + lane;
+        a.lse[(int64_t)(first + row / group) * a.n_q + head * group + row % group] =
+            l == 0.f ? -INFINITY : (top + log2f(l) - 8.f) * 0.693147180559945309f;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * (D / 4); i += 256) {
+        const int row = row0 + i / (D / 4), c = i % (D / 4);
+        if (row < n_rows)
+            reinterpret_cast<uint2 *>(a.out + ((int64_t)(first + row / group) * a.n_q + head * group + row % group) * D)[c] =
+                rows[i / (D / 4)][c];
+    }
+}
+
+// No sequence has more tile pairs than its rows fill, and one that they do not: a bound that needs no lengths.
+int64_t pairs_bound(int B, int total_q, int n_q, int n_kv) {
+    return ((int64_t)total_q * (n_q / n_kv) / ROWS + B) * n_kv;
+}
+
+template <int D, bool SPLIT>
+int launch(const AttnArgs &a, int splits, void *ws, cudaStream_t s) {
     static bool set[PQE_MAX_DEVICES] = {};
     int dev = 0, n = 0;
-    const int rc = device_info(dev, n);
+    int rc = device_info(dev, n);
     if (rc != PQE_OK) return rc;
     constexpr int smem = (int)sizeof(Smem<D>) + 1024;
     if (!set[dev]) {
         // the split of the registers waits forever where the block is launched with fewer than it counts on
         cudaFuncAttributes at;
-        PQE_CUDA_TRY(cudaFuncGetAttributes(&at, attn_prompt_kernel<D>));
+        PQE_CUDA_TRY(cudaFuncGetAttributes(&at, attn_prompt_kernel<D, SPLIT>));
         if (at.numRegs != LAUNCH_REGS) return PQE_ERR_UNSUPPORTED;
-        PQE_CUDA_TRY(cudaFuncSetAttribute(attn_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+        PQE_CUDA_TRY(cudaFuncSetAttribute(attn_prompt_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
         set[dev] = true;
     }
-    // no sequence has more tiles than its rows fill, and one that they do not: a bound that needs no lengths here
-    const int64_t ctas = ((int64_t)a.total_q * (a.n_q / a.c.n_kv) / (BM * TILES) + a.B) * a.c.n_kv;
-    PQE_CHECK_ARG(ctas <= INT32_MAX);
-    return launch_pdl(attn_prompt_kernel<D>, dim3((unsigned)ctas), dim3(THREADS), smem, s, a);
+    const int64_t ctas = pairs_bound(a.B, a.total_q, a.n_q, a.c.n_kv);
+    PQE_CHECK_ARG(ctas * splits <= INT32_MAX);
+    rc = launch_pdl(attn_prompt_kernel<D, SPLIT>, dim3((unsigned)(ctas * splits)), dim3(THREADS), smem, s, a, splits,
+                    static_cast<float *>(ws));
+    if (rc != PQE_OK || !SPLIT) return rc;
+    return launch_pdl(prompt_join_kernel<D>, dim3((unsigned)ctas, ROWS / 32), dim3(256), 0, s, a, splits,
+                      static_cast<const float *>(ws));
 }
 
 }  // namespace prompt
 
-int attn_prompt(const pqe_kv_cache *cache, const AttnArgs &a, cudaStream_t s) {
-    return cache->d == 128 ? prompt::launch<128>(a, s) : prompt::launch<64>(a, s);
+// Parts that a tile pair is cut into: so many that all of them have an SM, of three steps or more at the longest cache.
+int prompt_splits(int B, int total_q, int n_q, int n_kv, int64_t tokens, int sms) {
+    const int64_t pairs = prompt::pairs_bound(B, total_q, n_q, n_kv), by_steps = tokens / (3 * prompt::BK);
+    int64_t n = pairs > 0 ? sms / pairs : 1;
+    if (n > by_steps) n = by_steps;
+    return n < 1 ? 1 : n > 16 ? 16 : (int)n;
+}
+
+size_t attn_prompt_ws(int B, int total_q, int n_q, int n_kv, int d, int sms) {
+    const int splits = prompt_splits(B, total_q, n_q, n_kv, INT64_MAX, sms);
+    if (splits == 1) return 256;
+    return (size_t)prompt::pairs_bound(B, total_q, n_q, n_kv) * splits * prompt::part_floats(d) * sizeof(float);
+}
+
+int attn_prompt(const pqe_kv_cache *cache, const AttnArgs &a, int splits, void *ws, cudaStream_t s) {
+    if (cache->d == 128) return splits > 1 ? prompt::launch<128, true>(a, splits, ws, s) : prompt::launch<128, false>(a, 1, ws, s);
+    return splits > 1 ? prompt::launch<64, true>(a, splits, ws, s) : prompt::launch<64, false>(a, 1, ws, s);
 }
 
 }  // namespace kv
