@@ -46,7 +46,7 @@ constexpr int tile_bytes() {
     return TILE / BLOCK * block_bytes(D);
 }
 // CTAs an SM: what the registers of a warp leave room for
-__host__ __device__ constexpr int ctas(int d, int nt) { return nt == 1 ? 3 : 2; }
+__host__ __device__ constexpr int ctas(int d, int nt) { return nt == 1 ? (d == 64 ? 4 : 3) : 2; }
 // one partial result: O [rows][D], m [rows], l [rows], all fp32
 __host__ __device__ constexpr int part_floats(int d, int rows) { return rows * (d + 2); }
 

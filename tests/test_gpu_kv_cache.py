@@ -149,3 +149,26 @@ def test_other_stream_and_graph(cuda_lib):
     torch.cuda.synchronize()
     assert torch.equal(ko.double(), ref.values(*ref.mxfp4(k)))
     assert torch.equal(vo.double(), ref.values(*ref.mxfp4(v)))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [16, 6400])
+def test_two_tokens_of_one_slot(cuda_lib, n, d):
+    """Two rows with the same slot among 16 of one block: that place holds either one's bytes, every other place its own
+    token's, and the place that no row has keeps what it held."""
+    n_kv, page = 8, 32
+    slots = torch.arange(n, device=DEV)
+    slots[9::16] = slots[4::16]  # place 9 of each block has no row, place 4 two
+    k, v = _rows(n, n_kv, d, 3), _rows(n, n_kv, d, 4)
+    k[9::16], v[9::16] = k[4::16], v[4::16]  # equal rows: the bytes are then determined
+    mem, cache = cuda_lib.alloc_kv_cache(n // page + 1, page, n_kv, d)
+    mem.fill_(0x5A)
+    want = mem.clone()
+    ref.put(want, slots, k, v, page)
+    status = _status()
+    cuda_lib.kv_cache_write(cache, k, v, slots, status)
+    assert torch.equal(mem, want)
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    cuda_lib.kv_cache_read(cache, slots, ko, vo, status)
+    kr, vr = ref.get(want, slots, page, n_kv, d)
+    assert torch.equal(ko.double(), kr) and torch.equal(vo.double(), vr) and status.item() == 0
