@@ -158,6 +158,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
+// for the softmax and MMA warpgroups; the converting warps begin beside the loads of Q
+__device__ __forceinline__ void q_barrier() {
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS - 32 * CONV_WARPS) : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -392,7 +396,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
             }
         }
         fence_async();
-        __syncthreads();  // (1) Q is there
+        q_barrier();  // Q is there
         if (tile < tiles) {
             float ref = -INFINITY, l = 0.f;  // exponents of two; l: 2^8 times the sum
             bool ok = true;
@@ -592,7 +596,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
     } else if (warp < MMA_WARP) {
         fewer_registers<CONV_REGS>();
         // ================= conversion: warp w takes a step's blocks 2w and 2w + 1 =================
-        __syncthreads();  // (1)
         const int w = warp - SOFT_WARPS;
         constexpr int NK = D / 32;  // 16-byte pieces of K a thread takes
         constexpr int NV = D / 64;  // planes of V
@@ -738,7 +741,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
     } else {
         fewer_registers<MMA_REGS>();
         // ================= MMA =================
-        __syncthreads();  // (1)
+        q_barrier();
         if (warp == MMA_WARP && steps > 0) {
             tc_fence_after();
             const uint32_t one = elect();
