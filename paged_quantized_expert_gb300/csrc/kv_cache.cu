@@ -3,10 +3,15 @@
 //
 // Per block of 32 values along d: amax, X = 2^(floor(log2 amax) - 2), codes
 // RNE_e2m1(v / X). X is a power of two, so v / X is exact in fp32 and the only
-// rounding is the code's own. Both kernels move bytes and do next to no
-// arithmetic: bound by memory once there are enough tokens, by latency below.
-// The lanes' shares are those of the cache's byte order, so that what a warp
-// writes or reads of a block is contiguous: K by rows, V by places.
+// rounding is the code's own. The lanes' shares are those of the cache's byte
+// order, so that what a warp writes or reads of a block is contiguous: K by rows,
+// V by places.
+//
+// Bound by memory once there are many tokens, with the conversions close behind
+// (an instruction for every two values each of expanding, scaling and coding), by
+// latency below. 16384 tokens of 8 heads of 128, 85 MB: write 16.6 us (5.1 TB/s),
+// read 14.4 us (5.9 TB/s); 65537 of 4 heads: read 28.3 us (6.0 TB/s); 64 tokens of
+// 8 heads: 1.7 us each.
 #include "kv_layout.cuh"
 
 namespace pqe {
@@ -28,19 +33,49 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t top, float &inv) {
     return s;
 }
 
-// two bf16 to a byte of two codes; zero where inv is (v may then be NaN)
-__device__ __forceinline__ uint32_t code2(uint32_t v, float inv) {
-    const uint32_t b = f32x2_to_e2m1x2(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xFFFF0000u) * inv);
-    return inv == 0.f ? 0u : b;
+// eight bf16 to their codes, the first in the lowest nibble; zero where inv is (they may then be NaN)
+__device__ __forceinline__ uint32_t codes8(const uint4 &v, float inv) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float lo[4], hi[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        lo[i] = __uint_as_float(w[i] << 16) * inv;
+        hi[i] = __uint_as_float(w[i] & 0xFFFF0000u) * inv;
+    }
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(lo[0]), "f"(hi[0]), "f"(lo[1]), "f"(hi[1]), "f"(lo[2]), "f"(hi[2]), "f"(lo[3]), "f"(hi[3]));
+    return inv == 0.f ? 0u : r;
 }
 
-// four codes (two bytes, low nibble first) times s, as bf16
-__device__ __forceinline__ uint2 values4(uint32_t codes, float s) {
-    uint2 o;
-    const float2 x = e2m1x2_to_f32x2((uint8_t)codes), y = e2m1x2_to_f32x2((uint8_t)(codes >> 8));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o.x) : "f"(x.y * s), "f"(x.x * s));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o.y) : "f"(y.y * s), "f"(y.x * s));
-    return o;
+// What the values of scale byte x come to as bf16 pairs. The bits of an f16 one, shifted to bf16's places, are those of
+// 2^-112 times the value; 2^(x - 15) is left, in two factors where x is above 142. NaN for 255.
+struct Factor {
+    uint32_t a, b;
+};
+__device__ __forceinline__ Factor factor_of(uint32_t x) {
+    Factor f;
+    f.a = x == 255u ? 0x7FC07FC0u : (min(x, 142u) + 112u) * (128u * 0x10001u);
+    f.b = (max(x, 142u) - 15u) * (128u * 0x10001u);
+    return f;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// eight codes to bf16: four of one block, four of another
+__device__ __forceinline__ uint4 values8(uint32_t codes, const Factor &x, const Factor &y) {
+    uint32_t h[4];
+    e2m1x8_to_f16(codes, h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const Factor &f = i < 2 ? x : y;
+        h[i] = mul_bf16x2(mul_bf16x2((h[i] >> 3 & 0x0FFF0FFFu) | (h[i] & 0x80008000u), f.a), f.b);
+    }
+    return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
 // ---- few tokens: a thread per eight values, the shortest way from a row to its bytes ----
@@ -89,7 +124,7 @@ __global__ void __launch_bounds__(256) kv_write_few_kernel(const Cache c, const 
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     float inv;
     const uint32_t scale = block_scale(top, inv);
-    const uint32_t word = code2(raw.x, inv) | code2(raw.y, inv) << 8 | code2(raw.z, inv) << 16 | code2(raw.w, inv) << 24;
+    const uint32_t word = codes8(raw, inv);
     if (slot < 0) return;
     const int at = (int)(slot & ((1 << c.page_shift) - 1)), t = at & 15;
     uint8_t *b = block_of<D>(c, slot >> c.page_shift, at, x.head);
@@ -111,31 +146,30 @@ __global__ void __launch_bounds__(256) kv_read_few_kernel(const Cache c, const i
     const int64_t slot = slot_of(c, slots, x, status);
     uint16_t *out = x.is_v ? v : k;
     if (!x.in || !out) return;
-    uint32_t word = 0;
-    float s = 0.f;
+    uint32_t word = 0, s = 0;
     if (slot >= 0) {
         const int at = (int)(slot & ((1 << c.page_shift) - 1)), t = at & 15;
         const uint8_t *b = block_of<D>(c, slot >> c.page_shift, at, x.head);
         if (!x.is_v) {
             word = *reinterpret_cast<const uint32_t *>(b + k_code<D>(t, x.e));
-            s = scale_value(b[k_scale<D>(t, x.e / 32)]);
+            s = b[k_scale<D>(t, x.e / 32)];
         } else {
             word = (uint32_t)*reinterpret_cast<const uint16_t *>(b + v_code<D>(t, x.e)) |
                    (uint32_t)*reinterpret_cast<const uint16_t *>(b + v_code<D>(t, x.e + 4)) << 16;
-            s = scale_value(b[v_scale<D>(t, x.e / 32)]);
+            s = b[v_scale<D>(t, x.e / 32)];
         }
     }
-    const uint2 lo = values4(word, s), hi = values4(word >> 16, s);
-    *reinterpret_cast<uint4 *>(out + ((size_t)x.tok * c.n_kv + x.head) * D + x.e) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    const Factor f = factor_of(s);
+    *reinterpret_cast<uint4 *>(out + ((size_t)x.tok * c.n_kv + x.head) * D + x.e) = values8(word, f, f);
 }
 
 // ---- many tokens ----
 
 constexpr int WARPS = 8;
-// Groups an SM below which a thread for each eight values is faster. (Write and read of a run of 4096 tokens of 8 heads of
-// 128, 27 groups an SM: 7.5 + 6.6 us that way, 6.8 + 6.9 by groups; 1024 tokens: 3.2 + 2.9 and 4.3 + 3.2; 16384: 25.5 +
-// 23.6 and 20.5 + 14.6.)
-constexpr int FEW_WARPS = 26;
+// Groups an SM below which a thread for each eight values is faster. (Write and read of a run of 1024 tokens of 8 heads of
+// 128, 7 groups an SM: 3.2 + 2.9 us that way, 3.0 + 3.1 by groups; 3000 of 4 heads, 10: 3.8 + 3.3 and 4.0 + 3.7; 2048 of 8, 13:
+// 4.6 + 4.0 and 4.1 + 3.8; 512: 2.3 + 2.1 and 2.9 + 3.0; 16384: 24.7 + 23.5 and 16.6 + 14.4.)
+constexpr int FEW_WARPS = 12;
 
 // The 16 rows that a warp takes of one head of K or V: consecutive rows of the
 // call. Where they go is told per row, so they may lie in 16 blocks; a prompt's
@@ -173,7 +207,8 @@ __device__ __forceinline__ void group_of(const Cache &c, const int64_t *__restri
 
 // K and V of one group and head by one warp each: four lanes a row, eight channels of each block a lane. A K row's bytes go
 // out as they are; those of V, which lie two by two among the other tokens' of their block, meet in shared memory first where
-// the rows fill a block, and go out as the block's bytes do. (16384 tokens of 8 heads of 128: 17.0 us, two bytes at a time 20.5.)
+// the rows fill a block, and go out as the block's bytes do. (16384 tokens of 8 heads of 128:
+// 16.6 us, two bytes at a time 20.5.)
 template <int D>
 __global__ void __launch_bounds__(32 * WARPS) kv_write_kernel(const Cache c, const uint16_t *__restrict__ k,
                                                               const uint16_t *__restrict__ v, int64_t k_stride,
@@ -216,7 +251,7 @@ __global__ void __launch_bounds__(32 * WARPS) kv_write_kernel(const Cache c, con
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
             float inv;
             scales |= block_scale(top, inv) << (8 * b);
-            word[b] = code2(u.x, inv) | code2(u.y, inv) << 8 | code2(u.z, inv) << 16 | code2(u.w, inv) << 24;
+            word[b] = codes8(u, inv);
         }
         if (!blk) continue;
         const int tok = G.tok[r];
@@ -288,9 +323,8 @@ __global__ void __launch_bounds__(32 * WARPS) kv_read_kernel(const Cache c, cons
             uint16_t *out = k + ((size_t)(first + r) * c.n_kv + head) * D + 8 * t;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const float s = scale_value(scales >> (8 * b) & 255u);
-                const uint2 lo = values4(word[b], s), hi = values4(word[b] >> 16, s);
-                *reinterpret_cast<uint4 *>(out + 32 * b) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                const Factor f = factor_of(scales >> (8 * b) & 255u);
+                *reinterpret_cast<uint4 *>(out + 32 * b) = values8(word[b], f, f);
             }
         }
     } else {
@@ -333,9 +367,11 @@ __global__ void __launch_bounds__(32 * WARPS) kv_read_kernel(const Cache c, cons
             if (row[j] < 0 || first + row[j] >= n) continue;
             uint16_t *out = v + ((size_t)(first + row[j]) * c.n_kv + head) * D + 4 * g;
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
-                *reinterpret_cast<uint2 *>(out + 32 * b) =
-                    values4(word[b >> 1][j] >> (16 * (b & 1)), scale_value(scales[b] >> (8 * j) & 255u));
+            for (int b = 0; b < NB; b += 2) {
+                const uint4 u = values8(word[b >> 1][j], factor_of(scales[b] >> (8 * j) & 255u), factor_of(scales[b + 1] >> (8 * j) & 255u));
+                *reinterpret_cast<uint2 *>(out + 32 * b) = make_uint2(u.x, u.y);
+                *reinterpret_cast<uint2 *>(out + 32 * b + 32) = make_uint2(u.z, u.w);
+            }
         }
         // rows that are skipped: nobody's place where the others' are all different
         if (lane < 16 && first + lane < n && !G.blk[lane]) {

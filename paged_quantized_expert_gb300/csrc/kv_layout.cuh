@@ -62,9 +62,12 @@ __device__ __forceinline__ int v_scale(int tok, int G) {
     return 16 * D + D / 2 + ((tok & 7) >> 1) * (D / 8) + G * 4 + (tok & 1) + 2 * (tok >> 3);
 }
 
-// E8M0 byte as fp32; 255 is NaN
-__device__ __forceinline__ float scale_value(uint32_t b) {
-    return b == 255 ? __uint_as_float(0x7FC00000u) : e8m0_to_f32(b);
+// four bytes of two E2M1 codes each to four f16 pairs (a byte's low nibble in the low half)
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&r)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 "
+        "%1, b;\n\tcvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(w));
 }
 
 }  // namespace kv
