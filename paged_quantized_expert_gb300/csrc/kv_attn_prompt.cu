@@ -73,7 +73,7 @@ struct Smem {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], drained;
     uint32_t tmem;
     Find<THREADS> find;
-    int k_top, v_top, v_nan;
+    int k_top, v_top, k_nan, v_nan;
     // of a step's 16-token blocks, two bits from each converting warp: those that are there. Four steps' worth: a
     // step's is rewritten only once the softmax of the step three before has ended.
     alignas(4) uint8_t have[4][CONV_WARPS];
@@ -165,10 +165,13 @@ __device__ __forceinline__ void q_barrier() {
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// f16 pair of 2^(x - top + 7), x an E8M0 byte; zero from 22 below top on
-__device__ __forceinline__ uint32_t weight(uint32_t x, int top) {
-    return (uint32_t)max((int)x - top + 22, 0) * (1024u * 0x10001u);
-}
+// f16 pair of 2^(x - top + 7) for the E8M0 bytes x <= top in the halves of `two`; zero from 22 below top on
+struct Weights {
+    uint32_t least, add;
+    __device__ __forceinline__ explicit Weights(int top)
+        : least((uint32_t)max(top - 22, 0) * 0x10001u), add((uint32_t)(22 - top) * (1024u * 0x10001u)) {}
+    __device__ __forceinline__ uint32_t operator()(uint32_t two) const { return __vmaxu2(two, least) * 1024u + add; }
+};
 
 // 2^(top - 134): what a product with a weighted value lacks to the value's own
 __device__ __forceinline__ float unweight(int top) {
@@ -244,7 +247,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
             mbar_init(smem_u32(&sm.o_full[i]), 1);
         }
         mbar_init(smem_u32(&sm.drained), 1);
-        sm.k_top = sm.v_top = sm.v_nan = 0;
+        sm.k_top = sm.v_top = sm.k_nan = sm.v_nan = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
                         const uint32_t word = x < 4 ? w[0] : x < 8 ? w[1] : x < 12 ? w[2] : w[3];
                         const int s = j + tok < k_end ? (int)(word >> (8 * (x & 3)) & 255u) : 0;
                         if (s == 255)
-                            nan |= is_v;
+                            nan |= is_v ? 1 : 2;
                         else
                             top = max(top, s);
                     }
@@ -336,7 +339,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
         if (lane == 0) {
             atomicMax(&sm.k_top, kt);
             atomicMax(&sm.v_top, vt);
-            if (nan) atomicOr(&sm.v_nan, 1);
+            if (nan & 1) atomicOr(&sm.v_nan, 1);
+            if (nan & 2) atomicOr(&sm.k_nan, 1);
         }
     }
     if (warp == MMA_WARP) {
@@ -641,7 +645,14 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
                     vs[q2][i][1] = s.y;
                 }
                 if (!in || left < BLOCK) {
-                    // tokens that are not there: V of zero (bytes of scale 0, codes 0)
+                    // tokens that are not there: K of scale byte 0, V of zero (bytes of scale 0, codes 0)
+                    if constexpr (D == 128) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (!in || tok8 + 8 * h >= left) ks[2 * i + h] = 0;
+                    } else {
+                        if (!in || tok16 >= left) ks[i] = 0;
+                    }
                     const uint32_t tk[4] = {2u * t, 2u * t + 1, 2u * t + 8, 2u * t + 9};
                     uint32_t keep = 0;
 #pragma unroll
@@ -658,6 +669,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
             }
             return have;
         };
+        const Weights k_weight(k_top), v_weight(v_top);
+        const bool k_nan = sm.k_nan, v_nan = sm.v_nan;
         bool ok = true;
         uint32_t have = 0;
         if (steps > 0) {
@@ -679,8 +692,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const int G = D == 128 ? x : x & 1, piece = D == 128 ? t : 2 * (lane & 1) + (x >> 1);
-                    const uint32_t sb = ks[p] >> (8 * G) & 255u;
-                    const uint32_t f = sb == 255u ? 0x7E007E00u : weight(sb, k_top);
+                    uint32_t f = k_weight(__byte_perm(ks[p], 0, 0x4040 | G * 0x0101));
+                    if (k_nan && (ks[p] >> (8 * G) & 255u) == 255u) f = 0x7E007E00u;
                     uint32_t h[4];
                     e2m1x8_to_f16(wd[x], h);
                     *reinterpret_cast<uint4 *>(&sm.k[s][G >> 1][tok * 128 + ((((G & 1) * 4 + piece) ^ (tok & 7)) << 4)]) =
@@ -696,6 +709,14 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
             if (!mbar_wait(smem_u32(&sm.v_empty[s]), parity, a.wait_limit)) ok = false;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
+            if (v_nan) {  // a block that is not a number counts as zero here; its rows are found at the end
+#pragma unroll
+                for (int q2 = 0; q2 < NV; ++q2)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) vs[q2][i][h] &= ~__vcmpeq4(vs[q2][i][h], 0xFFFFFFFFu);
+            }
             // V: four tokens a block and eight channels a thread; two blocks make 16 bytes of a channel's row
 #pragma unroll
             for (int q2 = 0; q2 < NV; ++q2) {
@@ -712,13 +733,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
                 for (int h = 0; h < 2; ++h) {
                     uint32_t f[2][2];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const uint32_t x = vs[q2][i][h] >> (16 * y), b0 = x & 255u, b1 = x >> 8 & 255u;
-                            f[i][y] = ((b0 == 255u ? 0u : weight(b0, v_top)) & 0xFFFFu) |
-                                      ((b1 == 255u ? 0u : weight(b1, v_top)) & 0xFFFF0000u);
-                        }
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t x = vs[q2][i][h];
+                        f[i][0] = v_weight(__byte_perm(x, 0, 0x4140));
+                        f[i][1] = v_weight(__byte_perm(x, 0, 0x4342));
+                    }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int d = 64 * q2 + 32 * h + 4 * g + e, x = 2 * h + (e >> 1);
