@@ -673,6 +673,9 @@ PQE_API int kv_cache_read(const pqe_kv_cache *cache, const int64_t *slots, int n
  * down to 2^-22 of the row's largest value) and the probabilities scaled by
  * one too: those under 2^-33 of the row's largest count as zero, as do V
  * blocks whose scale is below 2^-21 of the largest they are summed with.
+ * Where there are many query rows, K blocks whose scale is below 2^-21 of the
+ * largest that a tile of them reads give scores of zero; where there are few,
+ * K blocks of scale byte 0 (values under 2^-124) do.
  * q        device bf16, token rows q_stride elements apart, [n_q][d] each;
  *          16-byte aligned, q_stride a multiple of 8 and at least n_q * d
  * q_offsets device int32 [B + 1], ascending from 0 or more, at most total_q

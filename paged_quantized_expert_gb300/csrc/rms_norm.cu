@@ -3,7 +3,14 @@
 //
 // h = x + r, y = h * rsqrt(mean h^2 + eps) * w, codes of y. A row is read once
 // and stays in registers through the sum of squares, the amax and the
-// quantisation, all in fp32; the codes are made from the unrounded y.
+// quantisation, all in fp32; the codes are made from the unrounded y. (The sum of
+// squares is of c h, c a power of two near 1 / sqrt(H), so that it overflows where
+// the mean does and not before.)
+//
+// A warp a row where there are many rows of up to 2560 values, else a CTA a row;
+// bound by memory then (16384 rows of 2560, bf16 sum and codes out: 49.5 us, 5.96
+// TB/s), by the latency of one load, two reductions and a store where there are
+// few (64 rows of 2048: 2.4 us).
 #include "pqe_common.cuh"
 
 namespace pqe {
