@@ -24,15 +24,15 @@
 // parts for several CTAs, which leave theirs in the workspace for a second kernel
 // to join.
 //
-// Two chunks of 2048 tokens over 5000 to 8192 (16 heads, 4 KV heads of 128): 200.7
-// us, 898 TFLOP/s of counted work. A step of both tiles takes some 3650 clocks an
+// Two chunks of 2048 tokens over 5000 to 8192 (16 heads, 4 KV heads of 128): 198.7
+// us, 907 TFLOP/s of counted work. A step of both tiles takes some 3650 clocks an
 // SM: 32 MMAs take 2050 at their peak and about 2600 here, beside the shared
 // memory's own 2050 clocks for their operands and the converted tiles; a tile's
 // chain is 1400 of softmax, two products and the waits between them; the four
 // converting warps need about 3000. None of them is idle for long, and what runs on
 // the issue slots of one runs against the others. Prompts of 17 to 701 tokens
-// (heads of 64): 39.4 us, where a CTA's begin and end (tiles found, scales scanned,
-// Q, the first conversion, the rows out) are two thirds of its 13 us.
+// (heads of 64): 37.3 us, where a CTA's begin and end (tiles found, scales scanned,
+// Q, the first conversion, the rows out) are 7 of its 12 us.
 #include <math.h>
 
 #include "kv_attn.cuh"
@@ -171,6 +171,13 @@ __device__ __forceinline__ void q_barrier() {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Bits of the 32 tokens from j on that lie in [lo, hi) and in one of the two blocks of `have` (a bit each).
+__device__ __forceinline__ uint32_t seen(int j, int lo, int hi, uint32_t have) {
+    const int from = min(max(lo - j, 0), 32), to = min(max(hi - j, 0), 32);
+    const uint32_t below = to < 32 ? (1u << to) - 1u : 0xFFFFFFFFu, before = from < 32 ? (1u << from) - 1u : 0xFFFFFFFFu;
+    return below & ~before & ((have & 1u ? 0x0000FFFFu : 0u) | (have & 2u ? 0xFFFF0000u : 0u));
+}
 
 // f16 pair of 2^(x - top + 7) for the E8M0 bytes x <= top in the halves of `two`; zero from 22 below top on
 struct Weights {
@@ -478,11 +485,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
 #pragma unroll
                             for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(s[i]));
                         } else {
+                            const uint32_t sees = seen(k0 + 32 * ch, my_lo, my_hi, have >> (8 * ch));
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const int j = k0 + 32 * ch + i;
-                                if (j < my_hi && j >= my_lo && (have >> (8 * ch + (i >> 4)) & 1)) top = fmaxf(top, __uint_as_float(s[i]));
-                            }
+                            for (int i = 0; i < 32; ++i)
+                                if (sees >> i & 1) top = fmaxf(top, __uint_as_float(s[i]));
                         }
                     }
                     const float e = top == -INFINITY ? -INFINITY : top * c;
@@ -517,11 +523,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
 #pragma unroll
                         for (int i = 0; i < 32; ++i) p[i] = exp2_approx(fmaf(__uint_as_float(s[i]), c, base));
                         if (!all) {
+                            const uint32_t sees = seen(k0 + 32 * ch, my_lo, my_hi, have >> (8 * ch));
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const int j = k0 + 32 * ch + i;
-                                if (!(j < my_hi && j >= my_lo && (have >> (8 * ch + (i >> 4)) & 1))) p[i] = 0.f;
-                            }
+                            for (int i = 0; i < 32; ++i)
+                                if (!(sees >> i & 1)) p[i] = 0.f;
                         }
 #pragma unroll
                         for (int i = 0; i < 32; ++i) sum[i & 3] += p[i];
