@@ -711,7 +711,7 @@ PQE_API int kv_paged_attention(const pqe_kv_cache *cache, const void *q, int64_t
  * H values, in fp32:
  *   h = x + residual (x alone when residual is NULL);  sum_out = bf16(h)
  *   y = h * (1 / sqrt(mean(h^2) + eps)) * weight;      y_out = bf16(y)
- *   PQE_Q8_ROW: s = max|y| / 448 (1 for an all-zero row) as fp32 [T],
+ *   PQE_Q8_ROW: s = max|y| / 448 (1 where that is 0 in fp32) as fp32 [T],
  *               code = RNE_e4m3(y / s), as pqe_quantize_fp8_rows
  *   PQE_Q8_MX:  per 32 values X = 2^(floor(log2 max|y|) - 8) as E8M0 [T, H/32]
  *               (byte 0 as for kv_cache_write), code = RNE_e4m3(y / X)

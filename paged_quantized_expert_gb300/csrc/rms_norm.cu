@@ -137,7 +137,8 @@ struct Part {
     // the codes with one scale for the row
     __device__ __forceinline__ void codes(const Args &a, int row, int first, int step, uint32_t top) {
         const int nv = a.H / 8;
-        const float s = top > 0x7F800000u ? __uint_as_float(0x7FC00000u) : top == 0 ? 1.f : __uint_as_float(top) / 448.f;
+        float s = top > 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float(top) / 448.f;
+        if (s == 0.f) s = 1.f;  // a row of zeros, or one so small that fp32 does not hold its scale
         if (first == 0) static_cast<float *>(a.q_scale)[row] = s;
 #pragma unroll
         for (int j = 0; j < V; ++j) {

@@ -123,6 +123,19 @@ def test_special_rows(cuda_lib, fmt):
         assert s[2].tolist() == [0, 255, 0, 0]
 
 
+def test_row_scale_below_fp32(cuda_lib):
+    """y so small that max|y| / 448 is 0 in fp32: scale 1 and codes of zero, no 0 / 0."""
+    T, H = 3, 64
+    x = torch.ones((T, H), dtype=torch.bfloat16, device=DEV)
+    x[:, ::2] = 0
+    w = torch.full((H,), 2.0 ** -133, dtype=torch.bfloat16, device=DEV)  # bf16's smallest
+    y = torch.empty((T, H), dtype=torch.bfloat16, device=DEV)
+    q = torch.full((T, H), 0x55, dtype=torch.uint8, device=DEV)
+    s = torch.empty(T, dtype=torch.float32, device=DEV)
+    cuda_lib.add_rms_norm(x, None, w, 1e8, None, y, q, s)  # y = 1e-4 * 2^-133, under 448 * 2^-150
+    assert (y == 0).all() and (s == 1).all() and (q & 0x7F == 0).all()
+
+
 def test_stream_and_graph(cuda_lib):
     pqe = cuda_lib
     T, H = 8, 2048
