@@ -361,9 +361,13 @@ __device__ __forceinline__ void add_tile(uint8_t *tile, Factors<D> &fac, int j0,
             const uint8_t *at = tile + ((lane >> 4) + 2 * h) * block_bytes(D) + 16 * D + (lane & 15) * (D / 32);
             const uint32_t w = D == 128 ? *reinterpret_cast<const uint32_t *>(at) : *reinterpret_cast<const uint16_t *>(at);
             float f[D / 32];
-            // byte into the exponent: 255 gives infinity, and NaN on the zero codes that go with it; 0 gives 0
+            // byte into the exponent; 0 gives 0
 #pragma unroll
             for (int G = 0; G < D / 32; ++G) f[G] = __uint_as_float(w << (G < 3 ? 23 - 8 * G : 0) >> (G < 3 ? 0 : 1) & 0x7F800000u);
+            if (w & 0x80808080u & ((w & 0x7F7F7F7Fu) + 0x01010101u))  // some byte is 255
+#pragma unroll
+                for (int G = 0; G < D / 32; ++G)
+                    if ((w >> (8 * G) & 255u) == 255u) f[G] = __uint_as_float(0x7FC00000u);
             if constexpr (D == 128)
                 *reinterpret_cast<float4 *>(fac.k[lane + 32 * h]) = make_float4(f[0], f[1], f[2], f[3]);
             else

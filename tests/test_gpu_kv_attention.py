@@ -216,6 +216,32 @@ def test_nan_tokens_reach_only_what_sees_them(cuda_lib, m):
         assert torch.isnan(o).any() and not torch.isnan(o).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("m", [1, 4, 90])
+def test_nan_scales_with_any_codes(cuda_lib, m, d):
+    """A scale byte of 255 is NaN whatever the block's codes are (a cache filled elsewhere may hold other ones than zero), also
+    where the block's product with q is below zero."""
+    page, n = 16, 150
+    for which, sign in (("k", 1), ("k", -1), ("v", 1)):
+        c = Case(cuda_lib, [m, m], [n, 40 + m], 8, 2, d, page, seed=5)
+        c.q = (sign * c.q.abs()).bfloat16()
+        bad = n - 1 - m // 2
+        slot = c.slots[0][bad].item()
+        block = slot // page * cuda_lib.pqe_kv_page_bytes(page, 2, d) + 17 * d  # head 1's only block of the page
+        t = slot % page
+        if which == "k":
+            c.mem[block + t * (d // 2):block + (t + 1) * (d // 2)] = 0x77  # codes of 6
+            c.mem[block + 16 * d + t * (d // 32) + 1] = 255
+        else:
+            c.mem[block + 16 * d + d // 2 + (t % 8) // 2 * (d // 8) + 4 + t % 2 + 2 * (t // 8)] = 255
+        kv = c.kv()
+        assert torch.isnan(kv[0][0 if which == "k" else 1][bad, 1, 32:64]).all()
+        out, lse = c.run()
+        o, a, l = ref.attend(c.q, c.ms, c.lens, kv, c.scale)
+        compare(out, lse, o, a, l, floor(kv))
+        assert torch.isnan(o).any() and not torch.isnan(o).all()
+
+
 @pytest.mark.parametrize("m", [1, 70])
 def test_query_that_is_not_finite(cuda_lib, m):
     c = Case(cuda_lib, [m, m], [100, 90], 8, 2, 64, 16)
