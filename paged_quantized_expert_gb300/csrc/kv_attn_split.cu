@@ -25,8 +25,8 @@
 //
 // Bound by the cache's bytes when there are many (4.25 bits a value), by latency
 // when there are few. 64 sequences of 1 to 8192 tokens (4 KV heads of 128, 16
-// query heads, 146 MB): 39.6 us, 3.7 TB/s; 3 of 60001 to 131071 (20 heads): 42.3 us,
-// 3.8 TB/s; one of 517: 8.1 us. Of the 42: 1.5 to set up, 5 until a warp has its
+// query heads, 146 MB): 39.9 us, 3.7 TB/s; 3 of 60001 to 131071 (20 heads): 42.5 us,
+// 3.8 TB/s; one of 517: 8.2 us. Of the 42: 1.5 to set up, 5 until a warp has its
 // first tile, 24.5 of walking them (a warp's share takes 20 to 29), 5 for the join,
 // the rest launches and tails. Within the walk no pipe is full (issue 47%, ALU 45%,
 // MMA 24%): a warp's tile is a chain of some 2 us, and registers leave room for 12
