@@ -35,11 +35,12 @@ __device__ __forceinline__ void sequence_of(const AttnArgs &a, int b, int &first
     len = min(max(a.kv_lens[b], 0), a.max_pages << a.c.page_shift);
 }
 
-// tokens [lo, hi) that query i of m sees
+// tokens [lo, hi) that query i of m sees (pos is below zero where there are more queries than tokens, and the window may be as
+// wide as an int: their difference is taken only where it is not)
 __device__ __forceinline__ void visible(const AttnArgs &a, int i, int m, int len, int &lo, int &hi) {
     const int pos = len - m + i;
     hi = a.causal ? min(pos + 1, len) : len;
-    lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+    lo = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
