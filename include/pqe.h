@@ -693,7 +693,8 @@ PQE_API int kv_cache_read(const pqe_kv_cache *cache, const int64_t *slots, int n
  *          cache (its tokens count as masked) or a length beyond the table
  *          (cut); PQE_STATUS_TIMEOUT as elsewhere
  * Limits: n_q a multiple of n_kv, n_q <= 1024; B >= 0, total_q >= 0 (either 0:
- * a no-op); total_q * n_q and max_pages * page_size below 2^31; scale finite. */
+ * a no-op); total_q * n_q below 2^31; max_pages * page_size at most 2^31 - 2^16;
+ * scale finite. */
 /* (pqe_test_set_attention_kernel: a test hook, which kernel the call takes
  * whatever its sizes: 1 the one for few query rows, 2 the one for many, 0 the
  * default choice. Both compute the same; only rounding differs, inside the

@@ -79,7 +79,7 @@ int kv_paged_attention(const pqe_kv_cache *cache, const void *q, int64_t q_strid
     PQE_CHECK_ARG(kv::cache_ok(cache) && B >= 0 && total_q >= 0 && max_q >= 0 && window >= 0 && max_pages >= 1);
     PQE_CHECK_ARG(n_q >= cache->n_kv && n_q <= 1024 && n_q % cache->n_kv == 0 && isfinite(scale));
     PQE_CHECK_ARG((int64_t)total_q * n_q <= INT32_MAX);
-    PQE_CHECK_ARG((causal || window == 0) && (int64_t)max_pages * cache->page_size <= INT32_MAX);
+    PQE_CHECK_ARG((causal || window == 0) && (int64_t)max_pages * cache->page_size <= kv::MAX_TOKENS);
     if (B == 0 || total_q == 0) return PQE_OK;
     PQE_CHECK_ARG(q && q_offsets && kv_lens && block_table && out && ws && status && max_q >= 1);
     PQE_CHECK_ARG(aligned(q, 16) && aligned(out, 16) && aligned(ws, 256) && aligned(lse, 4));

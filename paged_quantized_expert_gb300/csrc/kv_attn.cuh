@@ -7,6 +7,9 @@ namespace pqe {
 namespace kv {
 
 constexpr int TILE = 64;  // tokens that the split kernel takes of the cache at a time
+// Tokens that a block table may describe: the kernels count them in 32 bits, in steps of up to 2^13 tokens that may begin
+// before the last one and end behind it.
+constexpr int64_t MAX_TOKENS = (1ll << 31) - (1 << 16);
 
 struct AttnArgs {
     Cache c;

@@ -157,19 +157,19 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 struct Feed {
     const int32_t *table;  // the sequence's
     const uint8_t *head;   // the head's part of page 0
-    int j, len, lo;        // j: the first token that the lane copies
+    int j, len, lo;        // j: the first token that the lane copies; of a lane that copies none, below zero, however far it goes
 };
 __device__ __forceinline__ int blocks_shift(const AttnArgs &a) { return min(a.c.page_shift - 4, TB == 4 ? 2 : 1); }
 template <int D>
 __device__ __forceinline__ Feed feed_of(const AttnArgs &a, const Cursor &c, int lane) {
     const int blk = lane << blocks_shift(a);
     return {a.block_table + (size_t)c.b * a.max_pages, block_of<D>(a.c, 0, 0, c.head),
-            blk < TB ? (c.s.t0 + c.tile) * TILE + blk * BLOCK : INT32_MAX / 2, c.s.len, c.s.lo};
+            blk < TB ? (c.s.t0 + c.tile) * TILE + blk * BLOCK : INT32_MIN, c.s.len, c.s.lo};
 }
 
 // The table entry that this lane's copy of the tile needs. Asked for a tile early, so that fetch() does not wait.
 __device__ __forceinline__ int table_entry(const AttnArgs &a, const Feed &f) {
-    if (f.j >= f.len) return -3;                                    // no tokens
+    if ((uint32_t)f.j >= (uint32_t)f.len) return -3;           // no tokens, or not a lane that copies
     if (f.j + (BLOCK << blocks_shift(a)) <= f.lo) return -2;  // before the window: the page may be gone
     return max(f.table[f.j >> a.c.page_shift], -1);
 }
