@@ -207,16 +207,10 @@ __device__ __forceinline__ int64_t row_index(const AttnArgs &a, const Seq &s, in
     return (int64_t)(s.first + r / group) * a.n_q + head * group + r % group;
 }
 
-// f16 bits of V's block factor 2^(x - top + 7), x an E8M0 byte; zero from 22 below top on, NaN for 255
-__device__ __forceinline__ uint32_t v_weight(uint32_t x, uint32_t top) {
-    return x == 255 ? 0x7E00u : (uint32_t)max((int)(x - top) + 22, 0) << 10;
-}
-// p * f where a masked row's p, 0, gives 0 whatever f is
-__device__ __forceinline__ uint32_t weigh_nan(uint32_t p, uint32_t f) {
-    uint32_t r = mul_f16x2(p, f);
-    if (!(p & 0x7FFFu)) r &= 0xFFFF0000u;
-    if (!(p & 0x7FFF0000u)) r &= 0xFFFFu;
-    return r;
+// Bits of the 32 tokens from j on that lie in [lo, hi).
+__device__ __forceinline__ uint32_t tokens_in(int j, int lo, int hi) {
+    const int from = min(max(lo - j, 0), 32), to = min(max(hi - j, 0), 32);
+    return (to < 32 ? (1u << to) - 1u : 0xFFFFFFFFu) & ~(from < 32 ? (1u << from) - 1u : 0xFFFFFFFFu);
 }
 
 // The rows of one (sequence, KV head, chunk) while its tiles pass.
@@ -302,8 +296,29 @@ __device__ __forceinline__ void begin_rows(const AttnArgs &a, const Cursor &c, i
                 for (int i = 0; i < 4; ++i) R.o[G][h][nt][i] = 0.f;
 }
 
-// O += codes . (p * factors) of one tile. NANS: some V scale of it is 255.
-template <int D, int NT, bool NANS>
+// O of the rows that see a token whose V block is not a number turns to NaN in that block's channels, whatever weight the
+// token has, and stays it. (Bytes of tokens that are not there, or that no row sees, are 0 by now.)
+template <int D, int NT>
+__device__ __forceinline__ void add_nans(const uint8_t *tile, int j0, int lane, Rows<D, NT> &R) {
+#pragma unroll
+    for (int G = 0; G < D / 32; ++G)
+#pragma unroll
+        for (int h = 0; h < TILE; h += 32) {
+            const uint32_t bad =
+                __ballot_sync(0xffffffffu, tile[((h + lane) >> 4) * block_bytes(D) + v_scale<D>(lane & 15, G)] == 255);
+            if (!bad) continue;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (bad & tokens_in(j0 + h, R.lo[nt][i], R.hi[nt][i]))
+                        R.o[G][0][nt][i] = R.o[G][0][nt][i + 2] = R.o[G][1][nt][i] = R.o[G][1][nt][i + 2] =
+                            __uint_as_float(0x7FC00000u);
+        }
+}
+
+// O += codes . (p * factors) of one tile
+template <int D, int NT>
 __device__ __forceinline__ void add_values(const uint8_t *tile, const Factors<D> &fac, int lane,
                                            const uint32_t (&p)[TB][NT][2], Rows<D, NT> &R) {
     const int t = lane & 3;
@@ -324,8 +339,7 @@ __device__ __forceinline__ void add_values(const uint8_t *tile, const Factors<D>
                 const uint32_t f0 = h ? vf.z : vf.x, f1 = h ? vf.w : vf.y;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const uint32_t b0 = NANS ? weigh_nan(p[mt][nt][0], f0) : mul_f16x2(p[mt][nt][0], f0);
-                    const uint32_t b1 = NANS ? weigh_nan(p[mt][nt][1], f1) : mul_f16x2(p[mt][nt][1], f1);
+                    const uint32_t b0 = mul_f16x2(p[mt][nt][0], f0), b1 = mul_f16x2(p[mt][nt][1], f1);
                     mma_f16(R.o[2 * q2 + h][0][nt], a0[2 * h], a1[2 * h], a2[2 * h], a3[2 * h], b0, b1);
                     mma_f16(R.o[2 * q2 + h][1][nt], a0[2 * h + 1], a1[2 * h + 1], a2[2 * h + 1], a3[2 * h + 1], b0, b1);
                 }
@@ -384,12 +398,14 @@ __device__ __forceinline__ void add_tile(uint8_t *tile, Factors<D> &fac, int j0,
         }
         top = __reduce_max_sync(0xffffffffu, max(two & 0xFFFFu, two >> 16));
         nans = top == 255;
-        if (nans) {
+        if (nans) {  // a block that is not a number counts as one of zeros; its rows are found below
             top = 0;
 #pragma unroll
-            for (int i = 0; i < WORDS; ++i)
+            for (int i = 0; i < WORDS; ++i) {
+                w[i] &= ~__vcmpeq4(w[i], 0xFFFFFFFFu);
 #pragma unroll
-                for (int j = 0; j < 32; j += 8) top = max(top, (w[i] >> j & 255u) == 255 ? 0u : w[i] >> j & 255u);
+                for (int j = 0; j < 32; j += 8) top = max(top, w[i] >> j & 255u);
+            }
             top = __reduce_max_sync(0xffffffffu, top);
         }
         top = max(top, R.top);
@@ -397,14 +413,8 @@ __device__ __forceinline__ void add_tile(uint8_t *tile, Factors<D> &fac, int j0,
         const uint32_t least = (uint32_t)max((int)top - 22, 0) * 0x10001u, off = (uint32_t)((int)top - 22) * (1024u * 0x10001u);
         uint32_t o[2 * WORDS];
 #pragma unroll
-        for (int i = 0; i < 2 * WORDS; ++i) {
-            const uint32_t x = __byte_perm(w[i >> 1], 0, i & 1 ? 0x4342 : 0x4140);
-            o[i] = __vmaxu2(x, least) * 1024u - off;
-            if (nans) {
-                const uint32_t lo = x & 0xFFFFu, hi = x >> 16;
-                o[i] = v_weight(lo, top) | v_weight(hi, top) << 16;
-            }
-        }
+        for (int i = 0; i < 2 * WORDS; ++i)
+            o[i] = __vmaxu2(__byte_perm(w[i >> 1], 0, i & 1 ? 0x4342 : 0x4140), least) * 1024u - off;
         uint32_t *vf = &fac.v[0][0][0][0] + lane * 2 * WORDS;
         if constexpr (WORDS == 2)
             *reinterpret_cast<uint4 *>(vf) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -514,10 +524,8 @@ __device__ __forceinline__ void add_tile(uint8_t *tile, Factors<D> &fac, int j0,
             p[mt][nt][0] = transpose8x8(pack_f16(x[mt][nt][0], x[mt][nt][1]));
             p[mt][nt][1] = transpose8x8(pack_f16(x[mt][nt][2], x[mt][nt][3]));
         }
-    if (!nans)
-        add_values<D, NT, false>(tile, fac, lane, p, R);
-    else
-        add_values<D, NT, true>(tile, fac, lane, p, R);
+    add_values<D, NT>(tile, fac, lane, p, R);
+    if (nans) add_nans<D, NT>(tile, j0, lane, R);
     __syncwarp();  // before the factors of the next tile
 }
 

@@ -80,3 +80,27 @@ def test_every_one_of_more_than_2_30_tokens(cuda_lib, kernel):
     assert not (off > 0).any(), off.max().item()
     assert not ((lse.double() - l - torch.log(torch.tensor(float(rounds), dtype=torch.float64))).abs() > 2.0 ** -6).any()
     assert status.item() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("m", [1, 4, 90])
+@pytest.mark.parametrize("n", [150, 5000])
+def test_nan_values_of_no_weight(cuda_lib, m, n, d):
+    """A token whose V block is NaN and whose score lies so far below the others that its probability is 0 in any format:
+    0 * NaN is NaN, on both kernels. Rows that do not see it are as without it."""
+    c = Case(cuda_lib, [m, m], [n, 40 + m], 8, 2, d, 16, seed=n + m)
+    bad = n - 1 - m // 2  # some of the queries come before it
+    c.q[:, :, 0] = 32.0
+    k, v = ref.get(c.mem, c.slots[0][bad:bad + 1], 16, 2, d)
+    k[:, :, 0] = -2048.0  # a score of -65536 / sqrt(d)
+    v[0, 1, 40] = float("nan")
+    ref.put(c.mem, c.slots[0][bad:bad + 1], k.bfloat16(), v.bfloat16(), 16)
+    out, lse = c.run()
+    kv = c.kv()
+    o, a, l = ref.attend(c.q, c.ms, c.lens, kv, c.scale)
+    hit = torch.isnan(o)
+    assert hit[m - 1 - m // 2:m, 4:, 32:64].all() and hit.sum() == (m // 2 + 1) * 4 * 32
+    assert torch.equal(torch.isnan(out), hit) and not torch.isnan(lse).any()
+    # scores within 2^10 for the tokens that count: their fp32 sums are off by 2^-13 at most, which moves a probability by less
+    # than 2^-11 (its share in A)
+    compare(out, lse, o, a, l, floor(kv))
