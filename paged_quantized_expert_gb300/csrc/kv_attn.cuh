@@ -39,11 +39,12 @@ __device__ __forceinline__ void sequence_of(const AttnArgs &a, int b, int &first
 }
 
 // tokens [lo, hi) that query i of m sees (pos is below zero where there are more queries than tokens, and the window may be as
-// wide as an int: their difference is taken only where it is not)
+// wide as an int: their difference is not taken there. Comparing them instead took the prompt kernel five spilled words more:
+// 204.5 us against 199 for two chunks of 2048)
 __device__ __forceinline__ void visible(const AttnArgs &a, int i, int m, int len, int &lo, int &hi) {
     const int pos = len - m + i;
     hi = a.causal ? min(pos + 1, len) : len;
-    lo = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
+    lo = a.window > 0 ? max(max(pos, 0) - a.window + 1, 0) : 0;
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
