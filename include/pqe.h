@@ -671,8 +671,9 @@ PQE_API int kv_cache_read(const pqe_kv_cache *cache, const int64_t *slots, int n
  * whatever it holds. Statistics and sums are fp32; q and the probabilities
  * enter the tensor cores in f16, q scaled per row by a power of two (exact
  * down to 2^-22 of the row's largest value) and the probabilities scaled by
- * one too: those under 2^-33 of the row's largest count as zero, as do V
- * blocks whose scale is below 2^-21 of the largest they are summed with.
+ * one too: those under 2^-32 of the row's largest may count as zero, as may V
+ * blocks whose scale is below 2^-13 of the largest, in any channel, that the
+ * query sees of that head (2^-21 where the queries see the same tokens).
  * Where there are many query rows, K blocks whose scale is below 2^-21 of the
  * largest that a tile of them reads give scores of zero; where there are few,
  * K blocks of scale byte 0 (values under 2^-124) do.

@@ -11,7 +11,8 @@
 //   O[d, r] += code[j, d] * (p * 2^(vs[j, G] - top + 7)), top the largest V scale
 //              of the tiles so far: p and the factor stay inside f16, O in fp32
 // and O is scaled when a maximum or top has grown, which is rare after the
-// first tiles.
+// first tiles. (top is common to the rows of a set. Where some of them see a V
+// far above what the others see, the set's rows are summed one by one in fp32.)
 // P^T's fragments come from S^T's by movmatrix, with no trip through memory.
 //
 // The cache is read once. Work is (sequence, KV head, 8 * NT rows, tile); all of
@@ -33,7 +34,7 @@
 // to 16 warps an SM.
 #include <math.h>
 
-#include "kv_attn.cuh"
+#include "kv_attn_plain.cuh"
 #include "tc_ptx.cuh"
 
 namespace pqe {
@@ -221,7 +222,8 @@ struct Rows {
     int lo[NT][2], hi[NT][2];   // and the tokens they see
     int min_lo, max_lo, min_hi, max_hi;
     float m[NT][2], l[NT][2];   // m: of S; l: this lane's tokens only
-    uint32_t top;               // the E8M0 byte that o is in units of (2^-15 more)
+    uint32_t top;               // the E8M0 byte that o is in units of (2^-15 more): the largest that some row sees
+    uint32_t all, least;        // the largest among tokens that all rows see; the smallest token's that only some see
     float o[D / 32][2][NT][4];  // O^T: block G, channels 4g + {0, 1} and 4g + {2, 3}
 };
 
@@ -229,7 +231,8 @@ template <int D, int NT>
 __device__ __forceinline__ void begin_rows(const AttnArgs &a, const Cursor &c, int group, int lane, Rows<D, NT> &R) {
     const int g = lane >> 2, t = lane & 3;
     const int head = c.head, r0 = c.chunk * 8 * NT, n = c.s.m * group;
-    R.top = 0;
+    R.top = R.all = 0;
+    R.least = 255;
     R.min_lo = R.min_hi = INT32_MAX;
     R.max_lo = R.max_hi = 0;
 #pragma unroll
@@ -355,12 +358,25 @@ __device__ __forceinline__ void add_tile(uint8_t *tile, Factors<D> &fac, int j0,
     const bool part = have != ALL || j0 + TILE > R.min_hi || j0 < R.max_lo;  // some row does not see all of it
     if (part) {
         // V of tokens that no row sees may hold anything: scale bytes of zero
+        uint32_t all = 0, least = 255;
+#pragma unroll 1
         for (int i = lane; i < TILE; i += 32) {
             const int j = j0 + i;
-            if (!(have >> (i >> 4) & 1) || j >= R.max_hi || j < R.min_lo)
+            const bool seen = have >> (i >> 4) & 1 && j < R.max_hi && j >= R.min_lo;
+            uint32_t most = 0;
 #pragma unroll
-                for (int G = 0; G < D / 32; ++G) tile[(i >> 4) * block_bytes(D) + v_scale<D>(i & 15, G)] = 0;
+            for (int G = 0; G < D / 32; ++G) {
+                uint8_t &x = tile[(i >> 4) * block_bytes(D) + v_scale<D>(i & 15, G)];
+                if (!seen) x = 0;
+                most = max(most, x == 255 ? 0u : (uint32_t)x);
+            }
+            if (j >= R.max_lo && j < R.min_hi)
+                all = max(all, most);
+            else if (most)
+                least = min(least, most);
         }
+        R.all = max(R.all, __reduce_max_sync(0xffffffffu, all));
+        R.least = min(R.least, __reduce_min_sync(0xffffffffu, least));
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next copy into this stage
         __syncwarp();
     }
@@ -408,6 +424,7 @@ __device__ __forceinline__ void add_tile(uint8_t *tile, Factors<D> &fac, int j0,
             }
             top = __reduce_max_sync(0xffffffffu, top);
         }
+        if (!part) R.all = max(R.all, top);
         top = max(top, R.top);
         // f16 pairs of 2^(scale - top + 7): 0 from 22 below top on
         const uint32_t least = (uint32_t)max((int)top - 22, 0) * 0x10001u, off = (uint32_t)((int)top - 22) * (1024u * 0x10001u);
@@ -573,6 +590,49 @@ __device__ __forceinline__ void end_rows(const AttnArgs &a, const Cursor &c, int
         }
 }
 
+// V scales further apart than this, between what some row of a set sees and what another does, are left to plain_rows() (five
+// rows over a window of 1024: 23.0 us with the test for it, 22.4 without; single tokens: no difference). The
+// products of p and V's factors then hold 2^-32 of a row's largest p, and V blocks 13 below the largest that the row sees.
+constexpr uint32_t APART = 8;
+// Whether every row of the piece over tokens [from, to) sees a V scale near the largest of all: each sees the tokens that all see,
+// if there are any, else one of the others at least.
+template <int D, int NT>
+__device__ __forceinline__ bool alike(const Rows<D, NT> &R, int from, int to) {
+    if (R.min_lo == R.max_lo && R.min_hi == R.max_hi) return true;  // they see the same tokens
+    return R.top <= (max(R.max_lo, from) < min(R.min_hi, to) ? R.all : R.least) + APART;
+}
+
+// end_rows() for rows that are not: each by itself, from the cache
+template <int D, int NT>
+__device__ __noinline__ void plain_rows(const AttnArgs a, const Cursor c, int from, int to, bool whole, float *part) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31, group = a.n_q / a.c.n_kv, r0 = c.chunk * 8 * NT;
+    for (int r = 0; r < 8 * NT && r0 + r < c.s.m * group; ++r) {
+        int lo, hi;
+        visible(a, (r0 + r) / group, c.s.m, c.s.len, lo, hi);
+        const int head = c.head * group + (r0 + r) % group;
+        const PlainRow<D> x = plain_row<D>(a.c, a.block_table + (size_t)c.b * a.max_pages, c.head,
+                                           a.q + (int64_t)(c.s.first + (r0 + r) / group) * a.q_stride + head * D, a.scale,
+                                           max(lo, from), min(hi, to));
+        const int64_t row = whole ? row_index(a, c.s, c.head, group, r0 + r) : 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            if (whole)
+                a.out[row * D + lane * E + e] = f32_to_bf16_rn(x.l == 0.f ? 0.f : x.o[e] / x.l);
+            else
+                part[r * D + lane * E + e] = x.o[e];
+        }
+        if (lane == 0) {  // l in units of 2^-8, as the rows' own
+            if (!whole) {
+                part[8 * NT * D + r] = x.m;
+                part[8 * NT * D + 8 * NT + r] = x.l * 256.f;
+            } else if (a.lse) {
+                a.lse[row] = x.l == 0.f ? -INFINITY : (x.m + log2f(x.l)) * 0.693147180559945309f;
+            }
+        }
+    }
+}
+
 // Workspace: prefix [B + 1] of the sequences' units, then two partials per warp
 __host__ __device__ inline size_t prefix_bytes(int B) { return round_up(((size_t)B + 1) * 8, 256); }
 
@@ -688,12 +748,12 @@ __global__ void __launch_bounds__(WARPS * 32, ctas(D, NT)) attn_split_kernel(con
         uint32_t it = 0;
         while (left > 0 && ok) {
             // the tiles of one (sequence, head, rows)
-            int j0, j_end, tiles;
+            int j0, j_end, j_start, tiles;
             {
                 const Cursor c = sm.at[warp];
                 begin_rows<D, NT>(a, c, group, lane, R);
                 tiles = min(c.s.T - c.tile, left);
-                j0 = (c.s.t0 + c.tile) * TILE;
+                j0 = j_start = (c.s.t0 + c.tile) * TILE;
                 j_end = j0 + tiles * TILE;
             }
             for (; j0 < j_end; j0 += TILE, ++it) {
@@ -719,7 +779,12 @@ __global__ void __launch_bounds__(WARPS * 32, ctas(D, NT)) attn_split_kernel(con
             if (ended) left -= OPEN;
             // the share's first piece in the first partial, one that begins inside it in the second
             float *part = parts + ((size_t)2 * (blockIdx.x * WARPS + warp) + (seg_start > u0 ? 1 : 0)) * PART;
-            if (ok) end_rows<D, NT>(a, c, group, lane, R, whole, part);
+            if (ok) {
+                if (alike(R, j_start, j_end))
+                    end_rows<D, NT>(a, c, group, lane, R, whole, part);
+                else
+                    plain_rows<D, NT>(a, c, j_start, j_end, whole, part);
+            }
             if (left > 0) {
                 next_rows<NT>(a, c, group);
                 __syncwarp();

@@ -104,3 +104,137 @@ def test_nan_values_of_no_weight(cuda_lib, m, n, d):
     # scores within 2^10 for the tokens that count: their fp32 sums are off by 2^-13 at most, which moves a probability by less
     # than 2^-11 (its share in A)
     compare(out, lse, o, a, l, floor(kv))
+
+
+def _unlike(c, window, hit, least=2.0 ** -32):
+    """Rows marked in `hit` see a token out of scale with the others: finite is all that is asked of them. The others are held to
+    the bound of what they see themselves: n 2^-32 of the largest |v| among their tokens, since V's factors, up to 2^8 below
+    the largest of the tile's rows, meet probabilities in f16."""
+    out, lse = c.run(window=window)
+    assert c.status.item() == 0
+    kv = c.kv()
+    o, a, l = ref.attend(c.q, c.ms, c.lens, kv, c.scale, True, window)
+    rest, start = torch.zeros(c.total, dtype=torch.float64, device=DEV), 0
+    for m, n, (k, v) in zip(c.ms, c.lens, kv):
+        for i in range(m):
+            pos = n - m + i
+            seen = v[max(pos - window + 1, 0) if window else 0:max(pos + 1, 0)]
+            rest[start + i] = len(seen) * least * seen.abs().max() if len(seen) else 0.0
+        start += m
+    keep = ~hit
+    assert torch.isfinite(out[hit]).all() and torch.isfinite(lse[hit]).all()
+    off = (out.double() - o).abs() - (U * (1 + U) * o.abs() + 2.0 ** -9 * a + rest[:, None, None])
+    assert not (off[keep] > 0).any(), off[keep].max().item()
+    assert torch.equal(lse[keep] == float("-inf"), l[keep] == float("-inf"))
+    both = keep[:, None] & (l != float("-inf"))
+    assert not ((lse.double() - l).abs() > 2.0 ** -11 * (1 + l.abs()))[both].any()
+
+
+def _grow(c, b, token, power, k=False, v=False, block=None):
+    """Token `token` of sequence b 2^power times as large: its K, its V, or one 32-channel block of them."""
+    at = c.slots[b][token:token + 1]
+    rows = list(ref.get(c.mem, at, c.page, c.n_kv, c.d))
+    part = slice(None) if block is None else slice(32 * block, 32 * block + 32)
+    for x, use in zip(rows, (k, v)):
+        if use:
+            x[..., part] *= 2.0 ** power
+    ref.put(c.mem, at, *(x.bfloat16() for x in rows), c.page)
+
+
+def _sees(c, b, token, window):
+    """Which rows see the token."""
+    hit = torch.zeros(c.total, dtype=torch.bool, device=DEV)
+    start = sum(c.ms[:b])
+    for i in range(c.ms[b]):
+        pos = c.lens[b] - c.ms[b] + i
+        hit[start + i] = token <= pos and (not window or token > pos - window)
+    return hit
+
+
+POWERS = [4, 7, 8, 9, 11, 13, 14, 24, 40, 90]
+
+
+@pytest.mark.parametrize("kernel", ["few"], indirect=True)
+@pytest.mark.parametrize("power", POWERS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("m", [2, 5, 100])
+def test_large_values_that_a_query_does_not_see(cuda_lib, m, d, power):
+    """A token that comes after some of the queries, with V far above all others: nothing of it reaches those. One sequence of many
+    cached tokens, one of none but the queries' own; all channels, and one block of them."""
+    for lens, block in (([300, m], None), ([5000, 70 + m], 1)):
+        c = Case(cuda_lib, [m, m], lens, 8, 2, d, 16, seed=m)
+        hit = torch.zeros(c.total, dtype=torch.bool, device=DEV)
+        for b, token in ((0, lens[0] - 1), (1, lens[1] - 1 - m // 3)):
+            _grow(c, b, token, power, v=True, block=block)
+            hit |= _sees(c, b, token, 0)
+        assert hit.any() and not hit.all()
+        _unlike(c, 0, hit)
+
+
+@pytest.mark.parametrize("kernel", ["few"], indirect=True)
+@pytest.mark.parametrize("power", POWERS)
+@pytest.mark.parametrize("d,page", [(64, 32), (128, 16)])
+@pytest.mark.parametrize("m,window", [(2, 30), (5, 17), (100, 40), (100, 3), (3, 3000)])
+def test_large_values_before_the_window(cuda_lib, m, window, d, page, power):
+    """Tokens that some queries' windows no longer hold, and one that none does, with V (and K, of the last) far above all others."""
+    n = 700 if window < 700 else 5000
+    c = Case(cuda_lib, [m, m], [n, m + 20], 8, 2, d, page, seed=window)
+    first = n - m - window + 1  # the first query's first token
+    _grow(c, 0, first, power, v=True)  # that only the first query sees
+    _grow(c, 0, first - 1, power, k=True, v=True)  # that none does
+    _grow(c, 1, 4, power, v=True)
+    hit = _sees(c, 0, first, window) | _sees(c, 1, 4, window)
+    assert hit.any() and not hit.all()
+    _unlike(c, window, hit)
+
+
+@pytest.mark.parametrize("kernel", ["few"], indirect=True)
+@pytest.mark.parametrize("m", [4, 40])
+def test_queries_that_see_only_small_values(cuda_lib, m):
+    """First tokens with V of zero and of almost nothing, and heads whose values differ by 2^60."""
+    c = Case(cuda_lib, [m, m], [m, 30 + m], 8, 2, 128, 16, seed=9)
+    for b in (0, 1):
+        for token, power in ((0, None), (1, -40), (2, -20)):
+            at = c.slots[b][token:token + 1]
+            k, v = ref.get(c.mem, at, 16, 2, 128)
+            v = v * (0.0 if power is None else 2.0 ** power)
+            v[:, 1] *= 2.0 ** -60
+            ref.put(c.mem, at, k.bfloat16(), v.bfloat16(), 16)
+    _unlike(c, 0, torch.zeros(c.total, dtype=torch.bool, device=DEV))
+
+
+@pytest.mark.parametrize("kernel", ["few"], indirect=True)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("m", [2, 60])
+def test_rows_out_of_scale_keep_the_other_rules(cuda_lib, m, d):
+    """Beside a token that only the last query sees and that is 2^40 larger: a bad table entry, NaN in K and V blocks, a query that
+    is not finite, strided queries; equal bits every time."""
+    n = 300
+    c = Case(cuda_lib, [m, m], [n, n], 8, 2, d, 16, seed=m + d)
+    for b in (0, 1):
+        _grow(c, b, n - 1, 40, v=True)
+    c.q[m, 3, 5] = float("nan")
+    at = c.slots[1][[7, n - 1 - m // 2]]
+    k, v = ref.get(c.mem, at, 16, 2, d)
+    v[0, 0, 33] = float("nan")  # all queries see it
+    k[1, 1, 0] = float("inf")  # some of them
+    ref.put(c.mem, at, k.bfloat16(), v.bfloat16(), 16)
+    kv = c.kv()
+    c.table[0, 3] = c.n_pages  # 16 tokens of the first sequence are gone
+    here = torch.ones(n, dtype=torch.bool, device=DEV)
+    here[48:64] = False
+    kv[0] = tuple(x[here] for x in kv[0])
+    fused = torch.zeros((2 * m, 12, d), dtype=torch.bfloat16, device=DEV)
+    fused[:, 2:10] = c.q
+    out, lse = c.run(q=fused[:, 2:10])
+    assert c.status.item() == cuda_lib.PQE_STATUS_BAD_PAGE
+    o, a, l = ref.attend(c.q, c.ms, [n - 16, n], kv, c.scale)
+    o[m, 3] = l[m, 3] = float("nan")  # (the statement's own 0 * NaN leaves nothing else of that row)
+    keep = torch.ones(2 * m, dtype=torch.bool, device=DEV)
+    keep[[m - 1, 2 * m - 1]] = False
+    least = n * 2.0 ** -32 * max(torch.nan_to_num(v[:-1]).abs().max().item() for _, v in kv)
+    compare(out[keep], lse[keep], o[keep], a[keep], l[keep], least)
+    for _ in range(3):
+        again, lse2 = c.run()
+        assert torch.equal(torch.nan_to_num(again, nan=7.0), torch.nan_to_num(out, nan=7.0))
+        assert torch.equal(torch.nan_to_num(lse2, nan=7.0), torch.nan_to_num(lse, nan=7.0))
