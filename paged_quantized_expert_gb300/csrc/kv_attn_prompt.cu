@@ -326,15 +326,15 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
 #pragma unroll
                 for (int x = 0; x < 4; ++x) two = __vmaxu2(two, __vmaxu2(w[x] & 0x00FF00FFu, (w[x] >> 8) & 0x00FF00FFu));
                 int top = (int)max(two & 0xFFFFu, two >> 16);
-                if (top == 255 || j + BLOCK > k_end) {
-                    // byte by byte: some are NaN, or of tokens that are not there
+                if (top == 255 || j + BLOCK > k_end || j < lo) {
+                    // byte by byte: some are NaN, or of tokens that are not there or that no row sees
                     top = 0;
                     for (int x = 0; x < 16; ++x) {
                         // the token that the byte belongs to: K [token][G], V [t][G][j]
                         const int at = (piece % (PIECES / 2)) * 16 + x;
                         const int tok = is_v ? 2 * (at / (D / 8)) + (x & 1) + 8 * (x >> 1 & 1) : at / (D / 32);
                         const uint32_t word = x < 4 ? w[0] : x < 8 ? w[1] : x < 12 ? w[2] : w[3];
-                        const int s = j + tok < k_end ? (int)(word >> (8 * (x & 3)) & 255u) : 0;
+                        const int s = j + tok < k_end && j + tok >= lo ? (int)(word >> (8 * (x & 3)) & 255u) : 0;
                         if (s == 255)
                             nan |= is_v ? 1 : 2;
                         else
@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
                 const bool in = pages[i] >= 0 && pages[i] < a.c.n_pages;
                 if (in) have |= 1u << i;
                 const uint8_t *blk = block_of<D>(a.c, in ? pages[i] : 0, in ? j & page_mask : 0, head);
-                const int left = k_end - j;  // tokens of the block that count
+                const int left = k_end - j, skip = lo - j;  // tokens of the block that count: from skip on, below left
                 if constexpr (D == 128) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -656,19 +656,20 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
                     vs[q2][i][0] = s.x;
                     vs[q2][i][1] = s.y;
                 }
-                if (!in || left < BLOCK) {
-                    // tokens that are not there: K of scale byte 0, V of zero (bytes of scale 0, codes 0)
+                if (!in || left < BLOCK || skip > 0) {
+                    // tokens that are not there, or that no row sees (their scales may be above the largest): K of scale
+                    // byte 0, V of zero (bytes of scale 0, codes 0)
                     if constexpr (D == 128) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            if (!in || tok8 + 8 * h >= left) ks[2 * i + h] = 0;
+                            if (!in || tok8 + 8 * h >= left || tok8 + 8 * h < skip) ks[2 * i + h] = 0;
                     } else {
-                        if (!in || tok16 >= left) ks[i] = 0;
+                        if (!in || tok16 >= left || tok16 < skip) ks[i] = 0;
                     }
                     const uint32_t tk[4] = {2u * t, 2u * t + 1, 2u * t + 8, 2u * t + 9};
                     uint32_t keep = 0;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) keep |= (in && (int)tk[x] < left ? 0xFFu : 0u) << (8 * x);
+                    for (int x = 0; x < 4; ++x) keep |= (in && (int)tk[x] < left && (int)tk[x] >= skip ? 0xFFu : 0u) << (8 * x);
 #pragma unroll
                     for (int q2 = 0; q2 < NV; ++q2) {
                         vs[q2][i][0] &= keep;

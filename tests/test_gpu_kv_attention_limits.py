@@ -238,3 +238,18 @@ def test_rows_out_of_scale_keep_the_other_rules(cuda_lib, m, d):
         again, lse2 = c.run()
         assert torch.equal(torch.nan_to_num(again, nan=7.0), torch.nan_to_num(out, nan=7.0))
         assert torch.equal(torch.nan_to_num(lse2, nan=7.0), torch.nan_to_num(lse, nan=7.0))
+
+
+@pytest.mark.parametrize("power", [24, 40, 90])
+@pytest.mark.parametrize("d,page", [(64, 32), (128, 16)])
+@pytest.mark.parametrize("m,window", [(1, 30), (5, 18), (100, 40), (3, 3000), (300, 129)])
+def test_large_values_that_no_query_sees(cuda_lib, m, window, d, page, power):
+    """The tokens just before the first query's window, in the same block of 16 as tokens that it sees (of one sequence at least), with K
+    and V far above all others: every row is as without them."""
+    n = 700 if window < 700 else 5000
+    c = Case(cuda_lib, [m, m], [n, n + 5], 8, 2, d, page, seed=window)
+    for b in (0, 1):
+        first = c.lens[b] - m - window + 1
+        for token in range(first // 16 * 16, first):
+            _grow(c, b, token, power, k=True, v=True)
+    _unlike(c, window, torch.zeros(c.total, dtype=torch.bool, device=DEV))
