@@ -56,6 +56,9 @@ constexpr int LAUNCH_REGS = 128, SOFT_REGS = 168, CONV_REGS = 112, MMA_REGS = 64
 static_assert((2 * SOFT_REGS + CONV_REGS + MMA_REGS) * 128 <= LAUNCH_REGS * THREADS, "above the launch's total");
 constexpr int CHUNK = 128 * 128;  // bytes of 128 rows of 64 f16
 constexpr float LAZY = 7.f;       // growth of a maximum that its reference does not follow
+// Exponents of two (a score and its reference) above which c s - c ref is not taken as one fma: the product of the reference, once
+// rounded, would be off by a part of its own size, which is all of p's exponent from 2^27 or so on.
+constexpr float FAR = 1 << 20;
 
 // TMEM columns
 __device__ __forceinline__ constexpr uint32_t s_col(int tile) { return 128 * tile; }
@@ -416,7 +419,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
         fence_async();
         q_barrier();  // Q is there
         if (tile < tiles) {
-            float ref = -INFINITY, l = 0.f;  // exponents of two; l: 2^8 times the sum
+            float ref = -INFINITY, l = 0.f;  // ref: of S, c times it an exponent of two; l: 2^8 times the sum
             bool ok = true;
             for (int it = 0; it < steps; ++it) {
                 if (!mbar_wait(smem_u32(&sm.s_full[tile]), it & 1, a.wait_limit)) ok = false;
@@ -428,11 +431,12 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
                 const uint32_t have = *reinterpret_cast<const volatile uint32_t *>(sm.have[it & 3]);
                 const bool all = __all_sync(0xffffffffu, !valid || (k0 + BK <= my_hi && k0 >= my_lo)) && have == 0x03030303u;
                 bool done = false;
-                if (all && __all_sync(0xffffffffu, ref != -INFINITY)) {
+                if (all && __all_sync(0xffffffffu, fabsf(ref * c) < FAR)) {
                     // Every token is seen, and the reference will most likely stand: one pass, the probabilities held
                     // back until the maximum is known.
                     uint32_t p[BK / 2], s[2][32];
-                    const uint64_t c2 = pair(c, c), base2 = pair(8.f - ref, 8.f - ref);
+                    const float base = fmaf(-ref, c, 8.f);
+                    const uint64_t c2 = pair(c, c), base2 = pair(base, base);
                     uint64_t sum2[2] = {0, 0};
                     float top0 = -INFINITY, top1 = -INFINITY;
                     tmem_ld32(s_at, s[0]);
@@ -464,7 +468,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
                             p[16 * ch + x] = pack_f16(e[j], e[j + 1]);
                         }
                     }
-                    if (!__any_sync(0xffffffffu, fmaxf(top0, top1) * c > ref + LAZY)) {
+                    if (!__any_sync(0xffffffffu, (fmaxf(top0, top1) - ref) * c > LAZY)) {
                         tmem_st32(p_at, *reinterpret_cast<const uint32_t(*)[32]>(p));
                         tmem_st32(p_at + 32, *reinterpret_cast<const uint32_t(*)[32]>(p + 32));
                         float x, y;
@@ -491,12 +495,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
                                 if (sees >> i & 1) top = fmaxf(top, __uint_as_float(s[i]));
                         }
                     }
-                    const float e = top == -INFINITY ? -INFINITY : top * c;
                     // the reference follows a maximum that has outgrown it; O and the sum with it
-                    const bool grow = e > ref + LAZY || (ref == -INFINITY && e > ref);
+                    const bool grow = (top - ref) * c > LAZY;  // (nothing seen yet: NaN, or infinity)
                     if (__any_sync(0xffffffffu, grow)) {
-                        const float keep = grow ? exp2_approx(ref - e) : 1.f;
-                        if (grow) ref = e;
+                        const float keep = grow ? exp2_approx((ref - top) * c) : 1.f;
+                        if (grow) ref = top;
                         l *= keep;
                         if (it > 0) {
 #pragma unroll 1
@@ -512,7 +515,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
                         }
                     }
                     // pass 2: the probabilities
-                    const float base = ref == -INFINITY ? 0.f : 8.f - ref;
+                    const float base = ref == -INFINITY ? 0.f : ref;
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
                     for (int ch = 0; ch < BK / 32; ++ch) {
@@ -521,7 +524,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
                         tmem_ld_wait();
                         float p[32];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) p[i] = exp2_approx(fmaf(__uint_as_float(s[i]), c, base));
+                        for (int i = 0; i < 32; ++i) p[i] = exp2_approx(fmaf(__uint_as_float(s[i]) - base, c, 8.f));
                         if (!all) {
                             const uint32_t sees = seen(k0 + 32 * ch, my_lo, my_hi, have >> (8 * ch));
 #pragma unroll
@@ -602,10 +605,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
                 }
                 if constexpr (SPLIT) {
                     float *ml = parts + (size_t)blockIdx.x * part_floats(D) + ROWS * D + tile * BM + r;
-                    ml[0] = ref;
+                    ml[0] = ref * c;
                     ml[ROWS] = l;
                 } else if (valid && a.lse) {
-                    a.lse[out_row] = l == 0.f ? -INFINITY : (ref + log2f(l) - 8.f) * 0.693147180559945309f;
+                    a.lse[out_row] = l == 0.f ? -INFINITY : (ref * c + log2f(l) - 8.f) * 0.693147180559945309f;
                 }
             }
         }

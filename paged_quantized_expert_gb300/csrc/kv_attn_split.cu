@@ -96,11 +96,16 @@ __device__ __forceinline__ void next_rows(const AttnArgs &a, Cursor &c, int grou
     }
 }
 
+// Exponents of two (c m of a row) above which p's, c S - c m, is not right as one fma: c m, rounded, is off by a part of its own
+// size, which from 2^27 or so on is all of p's exponent. A set of rows with such scores is left to plain_rows().
+constexpr float FAR = 1 << 20;
+
 // what a tile's scale bytes become for the MMAs' lanes
 template <int D>
-struct Factors {
+struct alignas(16) Factors {
     float k[TILE][D / 32];        // [token][block]: 2^(scale - 127)
     uint32_t v[TB][4][D / 32][2];  // [16 tokens][t][block]: f16 pairs for tokens 2t, 2t+1 and 2t+8, 2t+9
+    uint32_t far;                  // not 0: some row's maximum was above FAR
 };
 
 template <int D, int NT>
@@ -113,6 +118,8 @@ struct Smem {
     int64_t share[WARPS + 1];  // units at which the warps' shares begin
     int64_t first[WARPS];      // unit at which the sequence begins that a share begins in
 };
+
+static_assert(sizeof(Factors<64>) % 16 == 0 && sizeof(Factors<128>) % 16 == 0, "a warp's factors are read 16 bytes at a time");
 
 // shares that `total` units are cut into: at least one unit each
 __host__ __device__ __forceinline__ int64_t shares(int64_t total, int ctas) {
@@ -532,6 +539,12 @@ __device__ __forceinline__ void add_tile(uint8_t *tile, Factors<D> &fac, int j0,
 #pragma unroll
                     for (int i = 0; i < 4; ++i) R.o[G][e][nt][i] *= keep[nt][i & 1];
         R.top = top;
+        bool far = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) far |= R.m[nt][i] != -INFINITY && fabsf(R.m[nt][i] * R.c[nt][i]) > FAR;
+        if (far) fac.far = 1;
     }
     uint32_t p[TB][NT][2];
 #pragma unroll
@@ -752,6 +765,8 @@ __global__ void __launch_bounds__(WARPS * 32, ctas(D, NT)) attn_split_kernel(con
             {
                 const Cursor c = sm.at[warp];
                 begin_rows<D, NT>(a, c, group, lane, R);
+                if (lane == 0) sm.fac[warp].far = 0;
+                __syncwarp();
                 tiles = min(c.s.T - c.tile, left);
                 j0 = j_start = (c.s.t0 + c.tile) * TILE;
                 j_end = j0 + tiles * TILE;
@@ -780,7 +795,7 @@ __global__ void __launch_bounds__(WARPS * 32, ctas(D, NT)) attn_split_kernel(con
             // the share's first piece in the first partial, one that begins inside it in the second
             float *part = parts + ((size_t)2 * (blockIdx.x * WARPS + warp) + (seg_start > u0 ? 1 : 0)) * PART;
             if (ok) {
-                if (alike(R, j_start, j_end))
+                if (alike(R, j_start, j_end) && !sm.fac[warp].far)
                     end_rows<D, NT>(a, c, group, lane, R, whole, part);
                 else
                     plain_rows<D, NT>(a, c, j_start, j_end, whole, part);

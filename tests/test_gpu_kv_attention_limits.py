@@ -253,3 +253,36 @@ def test_large_values_that_no_query_sees(cuda_lib, m, window, d, page, power):
         for token in range(first // 16 * 16, first):
             _grow(c, b, token, power, k=True, v=True)
     _unlike(c, window, torch.zeros(c.total, dtype=torch.bool, device=DEV))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("m", [1, 5, 100])
+@pytest.mark.parametrize("power", [16, 20, 24, 28, 40, 80])
+def test_scores_of_any_size(cuda_lib, m, d, power):
+    """Scores of 2^power times a few units, of either sign: a row is its largest score's token alone. The scores' fp32 sums (of d
+    products, and of d / 32 scaled blocks) are off by (d + 4) 2^-24 sum |q k| scale at most: rows whose two largest are nearer than
+    twice that and 2^6 more are not asked for. (Those left have p below 2^-64 for every other token.)"""
+    for sign in (1, -1):
+        c = Case(cuda_lib, [m, m], [400, 100 + m], 8, 2, d, 16, seed=power)
+        if sign < 0:  # all scores below zero
+            c.q = c.q.abs()
+            for s in c.slots:
+                k, v = ref.get(c.mem, s, 16, 2, d)
+                ref.put(c.mem, s, -k.abs().bfloat16(), v.bfloat16(), 16)
+        c.scale = 2.0 ** power
+        out, lse = c.run()
+        assert c.status.item() == 0 and torch.isfinite(out).all() and torch.isfinite(lse).all()
+        kv = c.kv()
+        o, a, l = ref.attend(c.q, c.ms, c.lens, kv, c.scale)
+        assert not ((lse.double() - l).abs() > 2.0 ** -11 * (1 + l.abs())).any()
+        clear, start = torch.zeros((c.total, 8), dtype=torch.bool, device=DEV), 0
+        for n, (k, v) in zip(c.lens, kv):
+            q = c.q[start:start + m].double().view(m, 2, 4, d)
+            see = torch.arange(n, device=DEV)[None] <= n - m + torch.arange(m, device=DEV)[:, None]
+            z = torch.einsum("mhgd,jhd->mhgj", q, k).masked_fill(~see[:, None, None], float("-inf")) * c.scale
+            size = torch.einsum("mhgd,jhd->mhgj", q.abs(), k.abs()).masked_fill(~see[:, None, None], 0.0).amax(-1) * c.scale
+            top = z.topk(2, -1).values
+            clear[start:start + m] = (top[..., 0] - top[..., 1] > 2 * (d + 4) * 2.0 ** -24 * size + 64).view(m, 8)
+            start += m
+        assert clear.float().mean() > 0.9
+        assert not ((out.double() - o).abs() > U * (1 + U) * o.abs() + 2.0 ** -9 * a + floor(kv))[clear].any()
