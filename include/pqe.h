@@ -674,9 +674,10 @@ PQE_API int kv_cache_read(const pqe_kv_cache *cache, const int64_t *slots, int n
  * one too: those under 2^-32 of the row's largest may count as zero, as may V
  * blocks whose scale is below 2^-13 of the largest, in any channel, that the
  * query sees of that head (2^-21 where the queries see the same tokens).
- * Where there are many query rows, K blocks whose scale is below 2^-21 of the
- * largest that a tile of them reads give scores of zero; where there are few,
- * K blocks of scale byte 0 (values under 2^-124) do.
+ * Where there are many query rows, K blocks whose scale is below 2^-15 of the
+ * largest that the query sees may give scores of zero; where there are few,
+ * K blocks of scale byte 0 (values under 2^-124) do. K and V from 2^100 on may
+ * overflow on the way.
  * q        device bf16, token rows q_stride elements apart, [n_q][d] each;
  *          16-byte aligned, q_stride a multiple of 8 and at least n_q * d
  * q_offsets device int32 [B + 1], ascending from 0 or more, at most total_q

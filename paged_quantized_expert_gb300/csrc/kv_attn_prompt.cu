@@ -16,26 +16,27 @@
 // Four warps turn codes into f16 in shared memory (128-byte swizzle, K-major
 // both): K as it lies, V transposed on the way, its tokens in the order in which
 // the cache's bytes hold them, which is the order P is written in. Codes are
-// multiplied by 2^(scale - top + 7) with top the largest scale that the CTA's
-// tokens have: exact while a scale is within 21 of it. Both tiles use what is
-// converted once.
+// multiplied by 2^(scale - top + 13) with top the largest scale that the CTA's
+// tokens have: exact while a scale is within 27 of it. Both tiles use what is
+// converted once. Where some row sees scales far above what another row sees, the
+// CTA's rows are summed one by one in fp32 instead.
 //
 // Where the tiles are fewer than SMs, each is cut along the cache into equal
 // parts for several CTAs, which leave theirs in the workspace for a second kernel
 // to join.
 //
-// Two chunks of 2048 tokens over 5000 to 8192 (16 heads, 4 KV heads of 128): 198.7
-// us, 907 TFLOP/s of counted work. A step of both tiles takes some 3650 clocks an
+// Two chunks of 2048 tokens over 5000 to 8192 (16 heads, 4 KV heads of 128): 194.2
+// us, 929 TFLOP/s of counted work. A step of both tiles takes some 3650 clocks an
 // SM: 32 MMAs take 2050 at their peak and about 2600 here, beside the shared
 // memory's own 2050 clocks for their operands and the converted tiles; a tile's
 // chain is 1400 of softmax, two products and the waits between them; the four
 // converting warps need about 3000. None of them is idle for long, and what runs on
 // the issue slots of one runs against the others. Prompts of 17 to 701 tokens
-// (heads of 64): 37.3 us, where a CTA's begin and end (tiles found, scales scanned,
+// (heads of 64): 37.5 us, where a CTA's begin and end (tiles found, scales scanned,
 // Q, the first conversion, the rows out) are 7 of its 12 us.
 #include <math.h>
 
-#include "kv_attn.cuh"
+#include "kv_attn_plain.cuh"
 #include "tc_ptx.cuh"
 
 namespace pqe {
@@ -83,7 +84,8 @@ struct Smem {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], drained;
     uint32_t tmem;
     Find<THREADS> find;
-    int k_top, v_top, k_nan, v_nan;
+    alignas(16) uint2 tops[THREADS / 32];  // what each warp found of the scales: K's in the low halves, V's in the high ones
+    int k_nan, v_nan;
     // of a step's 16-token blocks, two bits from each converting warp: those that are there. Four steps' worth: a
     // step's is rewritten only once the softmax of the step three before has ended.
     alignas(4) uint8_t have[4][CONV_WARPS];
@@ -182,18 +184,22 @@ __device__ __forceinline__ uint32_t seen(int j, int lo, int hi, uint32_t have) {
     return below & ~before & ((have & 1u ? 0x0000FFFFu : 0u) | (have & 2u ? 0xFFFF0000u : 0u));
 }
 
-// f16 pair of 2^(x - top + 7) for the E8M0 bytes x <= top in the halves of `two`; zero from 22 below top on
+// f16 pair of 2^(x - top + 13) for the E8M0 bytes x <= top in the halves of `two` (times a code, 6 at most, still inside f16);
+// zero from 28 below top on
 struct Weights {
     uint32_t least, add;
     __device__ __forceinline__ explicit Weights(int top)
-        : least((uint32_t)max(top - 22, 0) * 0x10001u), add((uint32_t)(22 - top) * (1024u * 0x10001u)) {}
+        : least((uint32_t)max(top - 28, 0) * 0x10001u), add((uint32_t)(28 - top) * (1024u * 0x10001u)) {}
     __device__ __forceinline__ uint32_t operator()(uint32_t two) const { return __vmaxu2(two, least) * 1024u + add; }
 };
 
-// 2^(top - 134): what a product with a weighted value lacks to the value's own
+// 2^(top - 140): what a product with a weighted value lacks to the value's own
 __device__ __forceinline__ float unweight(int top) {
-    return __uint_as_float(top > 7 ? (uint32_t)(top - 7) << 23 : 1u << (top + 15));
+    return __uint_as_float(top > 13 ? (uint32_t)(top - 13) << 23 : 1u << (top + 9));
 }
+// Scales further apart than this, between the largest that some row of a CTA sees and what another row sees, leave the CTA's rows
+// to plain_rows(). What is 15 below the largest that a row sees then still has its weight.
+constexpr int APART = 12;
 
 // The sequence and tile pair of place `at` in the line of all sequences' tile pairs, counted from its end (the last of a
 // sequence see the most tokens, and go first); .x < 0 past its beginning. For all N threads of a block.
@@ -242,6 +248,35 @@ __device__ __forceinline__ int2 find_tiles(const AttnArgs &a, int at, Find<N> &s
 constexpr int ROWS = BM * TILES;
 __host__ __device__ constexpr int part_floats(int d) { return ROWS * (d + 2); }
 
+// A CTA's rows one by one from the cache, over tokens [from, to): a warp each
+template <int D, bool SPLIT>
+__device__ __noinline__ void plain_rows(const AttnArgs a, int b, int kv_head, int first, int m, int len, int row0, int from, int to,
+                                        float *parts) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31, group = a.n_q / a.c.n_kv;
+    for (int r = threadIdx.x >> 5; r < ROWS && row0 + r < m * group; r += THREADS / 32) {
+        const int i = (row0 + r) / group, head = kv_head * group + (row0 + r) % group;
+        int lo, hi;
+        visible(a, i, m, len, lo, hi);
+        const PlainRow<D> x = plain_row<D>(a.c, a.block_table + (size_t)b * a.max_pages, kv_head,
+                                           a.q + (int64_t)(first + i) * a.q_stride + head * D, a.scale, max(lo, from), min(hi, to));
+        const int64_t row = (int64_t)(first + i) * a.n_q + head;
+        if constexpr (SPLIT) {  // in units of 2^-8, as the others' parts
+            float *part = parts + (size_t)blockIdx.x * part_floats(D);
+#pragma unroll
+            for (int e = 0; e < E; ++e) part[((lane * E + e) / 4 * ROWS + r) * 4 + (lane * E + e) % 4] = 256.f * x.o[e];
+            if (lane == 0) {
+                part[ROWS * D + r] = x.m;
+                part[ROWS * D + ROWS + r] = 256.f * x.l;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) a.out[row * D + lane * E + e] = f32_to_bf16_rn(x.l == 0.f ? 0.f : x.o[e] / x.l);
+            if (lane == 0 && a.lse) a.lse[row] = x.l == 0.f ? -INFINITY : (x.m + log2f(x.l)) * 0.693147180559945309f;
+        }
+    }
+}
+
 // SPLIT: of `splits` CTAs of a tile pair each leaves a part (a kernel of its own, so that the other has its registers).
 template <int D, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs a, int n_splits, float *parts) {
@@ -264,7 +299,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
             mbar_init(smem_u32(&sm.o_full[i]), 1);
         }
         mbar_init(smem_u32(&sm.drained), 1);
-        sm.k_top = sm.v_top = sm.k_nan = sm.v_nan = 0;
+        sm.k_nan = sm.v_nan = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
@@ -280,7 +315,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
     const int row0 = found.y * (BM * TILES), n_rows = m * group;
     const int tiles = row0 + BM < n_rows ? 2 : 1;
     // the tokens that some row of the CTA sees
-    int lo, hi, lo_last, hi_last;
+    int lo, hi, lo_last, hi_last;  // of the first row, and of the last
     visible(a, row0 / group, m, len, lo, hi);
     visible(a, (min(row0 + BM * TILES, n_rows) - 1) / group, m, len, lo_last, hi_last);
     int k_first = lo / BK * BK, k_end = max(hi_last, 0);
@@ -295,9 +330,14 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
     const int32_t *table = a.block_table + (size_t)b * a.max_pages;
     const int page_mask = (1 << a.c.page_shift) - 1;
 
-    // ---- the largest K and V scales among those tokens ----
+    // ---- the largest K and V scales among those tokens, and whether every row sees some near them ----
+    // Each row sees the tokens that all see, of which there may be whole blocks: then their largest counts. Else it sees one of
+    // the tokens at least: then the token counts whose largest block is the smallest (as 255 less, so that it is a maximum too).
+    const bool same = lo == lo_last && hi == hi_last;  // all rows see the same
+    const int all_lo = max(lo_last, k_first), all_hi = min(hi, k_end);
+    const bool common = (all_lo + BLOCK - 1) / BLOCK * BLOCK + BLOCK <= all_hi;
     {
-        int kt = 0, vt = 0, nan = 0;
+        int kt = 0, vt = 0, ka = 0, va = 0, nan = 0;
         constexpr int PIECES = D / 16;  // 16-byte pieces of a block's scales: K's, then V's
         const int n_pieces = (k_end - k_first + BLOCK - 1) / BLOCK * PIECES;
         constexpr int AHEAD = 4;  // loads in flight: table entries, then scales
@@ -322,40 +362,62 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
             }
 #pragma unroll
             for (int y = 0; y < AHEAD; ++y) {
+                if (page[y] == -2) continue;
                 const int i = i0 + y * THREADS, j = k_first + i / PIECES * BLOCK, piece = i % PIECES;
-                const uint32_t w[4] = {u[y].x, u[y].y, u[y].z, u[y].w};
+                uint32_t w[4] = {u[y].x, u[y].y, u[y].z, u[y].w};
                 const bool is_v = piece >= PIECES / 2;
-                uint32_t two = 0;
+                const int at = piece % (PIECES / 2), left = k_end - j, skip = lo - j;
+                auto largest = [&] {
+                    uint32_t two = 0;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) two = __vmaxu2(two, __vmaxu2(w[x] & 0x00FF00FFu, (w[x] >> 8) & 0x00FF00FFu));
-                int top = (int)max(two & 0xFFFFu, two >> 16);
-                if (top == 255 || j + BLOCK > k_end || j < lo) {
-                    // byte by byte: some are NaN, or of tokens that are not there or that no row sees
-                    top = 0;
-                    for (int x = 0; x < 16; ++x) {
-                        // the token that the byte belongs to: K [token][G], V [t][G][j]
-                        const int at = (piece % (PIECES / 2)) * 16 + x;
-                        const int tok = is_v ? 2 * (at / (D / 8)) + (x & 1) + 8 * (x >> 1 & 1) : at / (D / 32);
-                        const uint32_t word = x < 4 ? w[0] : x < 8 ? w[1] : x < 12 ? w[2] : w[3];
-                        const int s = j + tok < k_end && j + tok >= lo ? (int)(word >> (8 * (x & 3)) & 255u) : 0;
-                        if (s == 255)
-                            nan |= is_v ? 1 : 2;
-                        else
-                            top = max(top, s);
+                    for (int x = 0; x < 4; ++x) two = __vmaxu2(two, __vmaxu2(w[x] & 0x00FF00FFu, (w[x] >> 8) & 0x00FF00FFu));
+                    return (int)max(two & 0xFFFFu, two >> 16);
+                };
+                int top = largest(), all = j >= all_lo && j + BLOCK <= all_hi ? top : 0;
+                if (top == 255 || left < BLOCK || skip > 0 || !(common || same)) {
+                    // some blocks are NaN, or of tokens that are not there or that no row sees: K [token][G], V [t][G][j]
+                    int near = 0;
+                    uint32_t m = 0;  // V: the largest byte of each of four tokens
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t keep = 0;
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const int tok = is_v ? 2 * (D == 128 ? at : 2 * at + (x >> 1)) + (z & 1) + 8 * (z >> 1)
+                                                 : at * (512 / D) + (4 * x + z) / (D / 32);
+                            keep |= tok >= skip && tok < left ? 0xFFu << (8 * z) : 0u;
+                        }
+                        const uint32_t bad = __vcmpeq4(w[x], 0xFFFFFFFFu) & keep;
+                        if (bad) nan |= is_v ? 1 : 2;
+                        w[x] &= keep & ~bad;
+                        if (!is_v) {
+                            m = __vmaxu4(w[x], w[x] >> 8);
+                            if (D == 128) m = __vmaxu4(m, m >> 16);
+                            m &= D == 128 ? 0xFFu : 0x00FF00FFu;
+                        } else {
+                            m = x % (D / 32) == 0 ? w[x] : __vmaxu4(m, w[x]);
+                        }
+                        if (!is_v || x % (D / 32) == D / 32 - 1) {
+                            const uint32_t n = ~m & ~__vcmpeq4(m, 0);  // 255 less each that is not zero
+                            near = max(near, (int)max(max(n & 0xFFu, n >> 8 & 0xFFu), max(n >> 16 & 0xFFu, n >> 24)));
+                        }
                     }
+                    top = largest();
+                    all = !common ? near : all ? top : 0;
                 }
                 if (is_v)
-                    vt = max(vt, top);
+                    vt = max(vt, top), va = max(va, all);
                 else
-                    kt = max(kt, top);
+                    kt = max(kt, top), ka = max(ka, all);
             }
         }
         kt = __reduce_max_sync(0xffffffffu, kt);
         vt = __reduce_max_sync(0xffffffffu, vt);
+        ka = __reduce_max_sync(0xffffffffu, ka);
+        va = __reduce_max_sync(0xffffffffu, va);
         nan = __reduce_or_sync(0xffffffffu, nan);
         if (lane == 0) {
-            atomicMax(&sm.k_top, kt);
-            atomicMax(&sm.v_top, vt);
+            sm.tops[warp] = make_uint2((uint32_t)(kt | vt << 16), (uint32_t)(ka | va << 16));
             if (nan & 1) atomicOr(&sm.v_nan, 1);
             if (nan & 2) atomicOr(&sm.k_nan, 1);
         }
@@ -369,9 +431,19 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const AttnArgs 
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    const int k_top = sm.k_top, v_top = sm.v_top;
+    uint32_t tops = 0, alls = 0;
+#pragma unroll
+    for (int x = 0; x < THREADS / 32; ++x) {
+        const uint2 u = sm.tops[x];
+        tops = __vmaxu2(tops, u.x);
+        alls = __vmaxu2(alls, u.y);
+    }
+    if (!common) alls = 0x00FF00FFu - alls;
+    const int k_top = (int)(tops & 0xFFFFu), v_top = (int)(tops >> 16);
 
-    if (warp < SOFT_WARPS) {
+    if (!same && max(k_top - (int)(alls & 0xFFFFu), v_top - (int)(alls >> 16)) > APART) {
+        plain_rows<D, SPLIT>(a, b, head, first, m, len, row0, k_first, k_end, parts);
+    } else if (warp < SOFT_WARPS) {
         more_registers<SOFT_REGS>();
         // ================= softmax: a row per thread =================
         const int tile = warp >> 2, r = tid & (BM - 1), row = row0 + tile * BM + r;

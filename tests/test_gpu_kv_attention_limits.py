@@ -154,7 +154,6 @@ def _sees(c, b, token, window):
 POWERS = [4, 7, 8, 9, 11, 13, 14, 24, 40, 90]
 
 
-@pytest.mark.parametrize("kernel", ["few"], indirect=True)
 @pytest.mark.parametrize("power", POWERS)
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("m", [2, 5, 100])
@@ -171,7 +170,6 @@ def test_large_values_that_a_query_does_not_see(cuda_lib, m, d, power):
         _unlike(c, 0, hit)
 
 
-@pytest.mark.parametrize("kernel", ["few"], indirect=True)
 @pytest.mark.parametrize("power", POWERS)
 @pytest.mark.parametrize("d,page", [(64, 32), (128, 16)])
 @pytest.mark.parametrize("m,window", [(2, 30), (5, 17), (100, 40), (100, 3), (3, 3000)])
@@ -188,7 +186,6 @@ def test_large_values_before_the_window(cuda_lib, m, window, d, page, power):
     _unlike(c, window, hit)
 
 
-@pytest.mark.parametrize("kernel", ["few"], indirect=True)
 @pytest.mark.parametrize("m", [4, 40])
 def test_queries_that_see_only_small_values(cuda_lib, m):
     """First tokens with V of zero and of almost nothing, and heads whose values differ by 2^60."""
@@ -203,7 +200,6 @@ def test_queries_that_see_only_small_values(cuda_lib, m):
     _unlike(c, 0, torch.zeros(c.total, dtype=torch.bool, device=DEV))
 
 
-@pytest.mark.parametrize("kernel", ["few"], indirect=True)
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("m", [2, 60])
 def test_rows_out_of_scale_keep_the_other_rules(cuda_lib, m, d):
@@ -238,6 +234,21 @@ def test_rows_out_of_scale_keep_the_other_rules(cuda_lib, m, d):
         again, lse2 = c.run()
         assert torch.equal(torch.nan_to_num(again, nan=7.0), torch.nan_to_num(out, nan=7.0))
         assert torch.equal(torch.nan_to_num(lse2, nan=7.0), torch.nan_to_num(lse, nan=7.0))
+
+
+@pytest.mark.parametrize("power", POWERS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("m", [2, 5, 100, 300])
+def test_large_keys_that_a_query_does_not_see(cuda_lib, m, d, power):
+    """As the values: scores of the queries before the token keep their own K blocks."""
+    for lens, block in (([300 + m, m], None), ([5000, 70 + m], 1)):
+        c = Case(cuda_lib, [m, m], lens, 8, 2, d, 16, seed=m)
+        hit = torch.zeros(c.total, dtype=torch.bool, device=DEV)
+        for b, token in ((0, lens[0] - 1), (1, lens[1] - 1 - m // 3)):
+            _grow(c, b, token, power, k=True, block=block)
+            hit |= _sees(c, b, token, 0)
+        assert hit.any() and not hit.all()
+        _unlike(c, 0, hit)
 
 
 @pytest.mark.parametrize("power", [24, 40, 90])
