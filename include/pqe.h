@@ -702,6 +702,11 @@ PQE_API int kv_cache_read(const pqe_kv_cache *cache, const int64_t *slots, int n
  * default choice. Both compute the same; only rounding differs, inside the
  * stated precision. Process-wide, read at each call and workspace query.) */
 PQE_API int pqe_test_set_attention_kernel(int kind);
+/* (pqe_test_set_attention_polls: a test hook for the expiry of waits, with no
+ * GPU fault: polls of each wait of the attention kernels for data before it
+ * gives up, 0 or more; with 0 every one expires. -1, the default: as
+ * pqe_set_wait_limit says. Process-wide, read at each call.) */
+PQE_API int pqe_test_set_attention_polls(int polls);
 PQE_API size_t kv_paged_attention_workspace_size(int B, int total_q, int max_q, int n_q, int n_kv, int d);
 PQE_API int kv_paged_attention(const pqe_kv_cache *cache, const void *q, int64_t q_stride, const int32_t *q_offsets,
                                const int32_t *kv_lens, const int32_t *block_table, int max_pages, int B, int total_q,

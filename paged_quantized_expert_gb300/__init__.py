@@ -144,6 +144,7 @@ _SIGS = {
     "kv_cache_write": (I32, [C.POINTER(pqe_kv_cache), P, P, C.c_int64, C.c_int64, P, I32, P, P]),
     "kv_cache_read": (I32, [C.POINTER(pqe_kv_cache), P, I32, P, P, P, P]),
     "pqe_test_set_attention_kernel": (I32, [I32]),
+    "pqe_test_set_attention_polls": (I32, [I32]),
     "kv_paged_attention_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32]),
     "kv_paged_attention": (I32, [C.POINTER(pqe_kv_cache), P, C.c_int64, P, P, P, I32, I32, I32, I32, I32, C.c_float,
                                  I32, I32, P, P, P, SZ, P, P]),
@@ -406,6 +407,11 @@ def kv_cache_read(cache: pqe_kv_cache, slots, k, v, status, stream=None):
 def pqe_test_set_attention_kernel(kind: int):
     """Test hook: 1 the kernel for few query rows, 2 the one for many, 0 the default choice."""
     _check("pqe_test_set_attention_kernel", lib().pqe_test_set_attention_kernel(int(kind)))
+
+
+def pqe_test_set_attention_polls(polls: int):
+    """Test hook: polls of the attention kernels' waits before they give up (0: without one), -1 the ordinary limit."""
+    _check("pqe_test_set_attention_polls", lib().pqe_test_set_attention_polls(int(polls)))
 
 
 def kv_paged_attention_workspace_size(B: int, total_q: int, max_q: int, n_q: int, n_kv: int, d: int) -> int:

@@ -9,6 +9,7 @@ namespace pqe {
 namespace kv {
 
 static std::atomic<int> g_kernel{0};  // pqe_test_set_attention_kernel
+static std::atomic<int> g_polls{-1};  // pqe_test_set_attention_polls
 
 // Which kernels a call takes: the split kernel, the prompt kernel, or both, where max_q speaks of prompts but the mean does
 // not, as when a step carries single tokens beside a prompt's chunk. A sequence with more than `few_rows` query rows of a
@@ -55,6 +56,12 @@ int pqe_test_set_attention_kernel(int kind) {
     return PQE_OK;
 }
 
+int pqe_test_set_attention_polls(int polls) {
+    PQE_CHECK_ARG(polls >= -1);
+    kv::g_polls.store(polls, std::memory_order_relaxed);
+    return PQE_OK;
+}
+
 size_t kv_paged_attention_workspace_size(int B, int total_q, int max_q, int n_q, int n_kv, int d) {
     if (B < 0 || total_q < 0 || max_q < 0 || n_kv < 1 || n_q < n_kv || n_q > 1024 || n_q % n_kv || (d != 64 && d != 128))
         return 0;
@@ -90,9 +97,10 @@ int kv_paged_attention(const pqe_kv_cache *cache, const void *q, int64_t q_strid
     if (rc != PQE_OK) return rc;
     const kv::Choice use =
         kv::choose(B, total_q, max_q, n_q, cache->n_kv, cache->d, (int64_t)max_pages * cache->page_size, sms);
+    const int polls = kv::g_polls.load(std::memory_order_relaxed);
     kv::AttnArgs a{kv::cache_of(cache), static_cast<const uint16_t *>(q), q_stride, q_offsets, kv_lens, block_table, max_pages,
                    B, total_q, n_q, causal, window, scale * 1.44269504088896341f, static_cast<uint16_t *>(out), lse, status,
-                   wait_limit(), 1, INT32_MAX};
+                   polls < 0 ? wait_limit() : (uint32_t)polls, 1, INT32_MAX};
     if (use.many) {
         if (use.few) a.rows_min = use.few_rows + 1;
         const int rc2 = kv::attn_prompt(cache, a, use.splits, ws, as_stream(stream));

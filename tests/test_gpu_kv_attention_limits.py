@@ -297,3 +297,28 @@ def test_scores_of_any_size(cuda_lib, m, d, power):
             start += m
         assert clear.float().mean() > 0.9
         assert not ((out.double() - o).abs() > U * (1 + U) * o.abs() + 2.0 ** -9 * a + floor(kv))[clear].any()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("m", [1, 3, 100])
+def test_waits_that_expire(cuda_lib, m, d):
+    """Every wait for data gives up without a poll: the call comes back, says so in its status, and the next one is right. (The
+    waits for what is in flight keep their own limit, so that nothing lands in a block that has ended.)"""
+    c = Case(cuda_lib, [m, m], [2000, 3000], 8, 2, d, 16)
+    want, l = c.run()
+    for _ in range(3):
+        try:
+            cuda_lib.pqe_test_set_attention_polls(0)
+            c.run()
+            torch.cuda.synchronize()
+        finally:
+            cuda_lib.pqe_test_set_attention_polls(-1)
+        assert c.status.item() == cuda_lib.PQE_STATUS_TIMEOUT
+        c.status.zero_()
+        again, l2 = c.run()
+        assert c.status.item() == 0 and torch.equal(again, want) and torch.equal(l2, l)
+
+
+def test_polls_hook_rejects_less(cuda_lib):
+    with pytest.raises(cuda_lib.PqeError):
+        cuda_lib.pqe_test_set_attention_polls(-2)
