@@ -3,7 +3,9 @@
 // The attention kernels hold K and V (or the probabilities that meet them) in f16, relative to the largest scale that any of the
 // rows of a tile sees. Where that is far above what one of those rows sees, the row's own values would be lost under a token that
 // it does not see. Such tiles take this form instead: a warp per row, K, V and p as they are, nothing in common with other rows.
-// It is some hundred times slower, and no call of a healthy model comes here.
+// 16 rows at once on an SM take some 9 us for every 32 tokens, waiting on loads; a model whose values lie within a few orders of
+// magnitude of one another does not come here. (Two chunks of 2048 tokens over 5000 to 8192 with one token's V 2^40 above the others: 38 ms, without it 0.18; 32
+// sequences of 5 tokens over 4000: 2.3 ms, 0.045; 8 prompts of 300 tokens whose first V is 2^40 below the others: 138 us, 32.)
 #pragma once
 
 #include "kv_attn.cuh"

@@ -26,8 +26,8 @@
 //
 // Bound by the cache's bytes when there are many (4.25 bits a value), by latency
 // when there are few. 64 sequences of 1 to 8192 tokens (4 KV heads of 128, 16
-// query heads, 146 MB): 39.9 us, 3.7 TB/s; 3 of 60001 to 131071 (20 heads): 42.5 us,
-// 3.8 TB/s; one of 517: 8.2 us. Of the 42: 1.5 to set up, 5 until a warp has its
+// query heads, 146 MB): 39.8 us, 3.7 TB/s; 3 of 60001 to 131071 (20 heads): 42.6 us,
+// 3.7 TB/s; one of 517: 8.4 us. Of the 42: 1.5 to set up, 5 until a warp has its
 // first tile, 24.5 of walking them (a warp's share takes 20 to 29), 5 for the join,
 // the rest launches and tails. Within the walk no pipe is full (issue 47%, ALU 45%,
 // MMA 24%): a warp's tile is a chain of some 2 us, and registers leave room for 12
@@ -52,7 +52,7 @@ constexpr int tile_bytes() {
     return TILE / BLOCK * block_bytes(D);
 }
 // CTAs an SM: what the registers of a warp leave room for. (Heads of 64, one row tile, 4 against 3: 64 sequences of 4000: 39.4
-// us, 40.3; 16 of 1000: 8.7, 10.3. Heads of 128 spill at 4.)
+// us, 40.3; 16 of 1000: 8.7, 10.3. Heads of 128 spill 32 bytes at 3, and 160 at 4.)
 __host__ __device__ constexpr int ctas(int d, int nt) { return nt == 1 ? (d == 64 ? 4 : 3) : 2; }
 // one partial result: O [rows][D], m [rows], l [rows], all fp32
 __host__ __device__ constexpr int part_floats(int d, int rows) { return rows * (d + 2); }

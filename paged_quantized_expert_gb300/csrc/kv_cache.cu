@@ -9,9 +9,10 @@
 //
 // Bound by memory once there are many tokens, with the conversions close behind
 // (an instruction for every two values each of expanding, scaling and coding), by
-// latency below. 16384 tokens of 8 heads of 128, 85 MB: write 16.6 us (5.1 TB/s),
-// read 14.4 us (5.9 TB/s); 65537 of 4 heads: read 28.3 us (6.0 TB/s); 64 tokens of
-// 8 heads: 1.7 us each.
+// latency below. 16384 tokens of 8 heads of 128, 85 MB: write 18.1 us (4.7 TB/s),
+// read 15.7 us (5.4 TB/s), on three sets of tensors in turn (on one, partly in L2:
+// 16.6 and 14.4); 65537 of 4 heads: read 28.4 us (6.0 TB/s); 64 tokens of 8 heads:
+// 1.7 us each.
 #include "kv_layout.cuh"
 
 namespace pqe {
