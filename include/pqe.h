@@ -74,6 +74,7 @@ extern "C" {
 #define PQE_STATUS_CORRUPT_STREAM 0x2 /* a compressed row that does not decode */
 #define PQE_STATUS_BAD_PAGE 0x4       /* page table entry outside the pool, or unknown format */
 #define PQE_STATUS_TIMEOUT 0x8        /* a bounded device wait gave up */
+#define PQE_STATUS_NO_TOKEN 0x10      /* a row of sample_tokens with nothing to draw from */
 
 /* page formats (per expert page) */
 #define PQE_FMT_FP8 0   /* E4M3 weights, one fp32 scale per output row */
@@ -723,8 +724,11 @@ PQE_API int kv_paged_attention(const pqe_kv_cache *cache, const void *q, int64_t
  *               code = RNE_e4m3(y / s), as pqe_quantize_fp8_rows
  *   PQE_Q8_MX:  per 32 values X = 2^(floor(log2 max|y|) - 8) as E8M0 [T, H/32]
  *               (byte 0 as for kv_cache_write), code = RNE_e4m3(y / X)
- * saturating at 448. y is quantised unrounded. A NaN in a row (or block of 32)
- * of y gives NaN codes and a NaN scale (255).
+ *   PQE_Q8_B128: per 128 values (the last block may be shorter) s and codes as
+ *               for PQE_Q8_ROW, scales fp32 [T, ceil(H/128)]: what
+ *               fp8_block_matmul takes
+ * saturating at 448. y is quantised unrounded. A NaN in a row (or block of 32
+ * or 128) of y gives NaN codes and a NaN scale (255).
  * x, residual device bf16, rows x_stride (r_stride) elements apart; weight
  * device bf16 [H]; all 16-byte aligned, strides multiples of 8 and >= H.
  * sum_out, y_out device bf16 [T, H] or NULL; sum_out may be residual or x
@@ -733,9 +737,85 @@ PQE_API int kv_paged_attention(const pqe_kv_cache *cache, const void *q, int64_t
  * H % 32 == 0, 32 <= H <= 16384; T >= 0; eps >= 0. */
 #define PQE_Q8_ROW 0
 #define PQE_Q8_MX 1
+#define PQE_Q8_B128 2
 PQE_API int add_rms_norm(const void *x, int64_t x_stride, const void *residual, int64_t r_stride, const void *weight,
                          float eps, int T, int H, void *sum_out, void *y_out, uint8_t *q, void *q_scale, int q_fmt,
                          void *stream);
+
+/* ------------------------------------------------------------------------
+ * Block-scaled FP8 products -- what stands between a decoder layer's parts:
+ * activations as E4M3 codes with one fp32 scale for each 128 values of a row,
+ * weights as E4M3 codes with one for each tile of 128 x 128 (the last block of
+ * a row, and the last tile of a column, may be smaller).
+ * ------------------------------------------------------------------------ */
+
+/* fp8_block_quantize -- activations x [T, H] to codes and scales, per block b
+ * of 128 values: s = max|x| / 448 in fp32 (1 where that is 0), code =
+ * RNE_e4m3(x / s), saturating at 448. A NaN or an infinity in a block gives a
+ * NaN or infinite scale; codes of a NaN block are NaN. (The same out of the
+ * residual norm: add_rms_norm with PQE_Q8_B128.)
+ * x       device bf16, rows x_stride elements apart (a multiple of 8, >= H),
+ *         16-byte aligned
+ * q       device uint8 [T, H] E4M3 out, 16-byte aligned
+ * scale   device fp32 [T, ceil(H/128)] out
+ * H % 16 == 0, 16 <= H <= 32768; T >= 0. */
+PQE_API int fp8_block_quantize(const void *x, int64_t x_stride, int T, int H, uint8_t *q, float *scale, void *stream);
+
+/* pqe_quantize_fp8_blocks -- weights w fp32 [rows, cols] (device) to E4M3 codes
+ * q [rows, cols] with one fp32 scale for each 128 x 128 tile, scale
+ * [ceil(rows/128), ceil(cols/128)], by the same rule; it prepares weights and
+ * is not on the per-step path. rows, cols >= 1. */
+PQE_API int pqe_quantize_fp8_blocks(const float *w, int rows, int cols, uint8_t *q, float *scale, void *stream);
+
+/* fp8_block_matmul -- out = x W^T:
+ *   out[m, n] = sum_b x_scale[m, b] * w_scale[n / 128, b] * sum_k x[m, k] w[n, k]
+ * over the blocks b of 128 along K and the k of each. Products are exact, sums
+ * and scaling fp32 (the product of the two scales is rounded once to fp32 and
+ * should be in its range); out is rounded once. NaN codes or scales give NaN
+ * in the rows and columns that they belong to. One token to whole prompts: few
+ * rows are a stream of the weights, many run at the tensor cores' rate.
+ * x       device E4M3 [M, K], rows x_stride bytes apart (a multiple of 16,
+ *         >= K), 16-byte aligned
+ * x_scale device fp32 [M, ceil(K/128)]
+ * w       device E4M3 [N, K], 16-byte aligned
+ * w_scale device fp32 [ceil(N/128), ceil(K/128)]
+ * out     device [M, N], rows out_stride elements apart (>= N): bf16, or fp32
+ *         where out_fp32 is not 0; aligned to its element. It overlaps no input.
+ * status  device int32: PQE_STATUS_TIMEOUT as elsewhere
+ * K % 16 == 0, 16 <= K <= 32768; 1 <= N <= 2^22; M >= 0 (0: a no-op). */
+PQE_API int fp8_block_matmul(const uint8_t *x, int64_t x_stride, const float *x_scale, const uint8_t *w,
+                             const float *w_scale, int M, int N, int K, void *out, int64_t out_stride, int out_fp32,
+                             int32_t *status, void *stream);
+
+/* ------------------------------------------------------------------------
+ * sample_tokens -- the next token of each of B rows of V logits, from one given
+ * uniform number a row. In a row with temperature t, w_j = exp((l_j - max l) / t):
+ *   order:  logits descending, the lower index first among equal ones
+ *   kept:   the first top_k of the order (all where top_k <= 0), of those the
+ *           ones with w_j >= min_p (1 where it is more), of those the shortest
+ *           beginning of the order that holds at least top_p of their sum of w
+ *           (all where top_p >= 1; always the first)
+ *   token = the first j, in index order, with sum_{i <= j, kept} w_i > u * sum_kept w
+ *   logprob = ln(w_token / sum_kept w), what the token was drawn with
+ * t == 0 takes the largest logit, the lower index among equal ones (logprob 0).
+ * A logit of -infinity is never kept. Weights enter the sums with 2^-30 of
+ * their own size and 2^-43 of the largest, the sums are whole numbers: the same
+ * in every run and for every row's place in the batch.
+ * A row with a NaN or a +infinity among its logits, nothing above -infinity, or
+ * a setting out of range (t negative or not finite, top_p or min_p NaN, u
+ * outside [0, 1)) gives token -1, logprob NaN and PQE_STATUS_NO_TOKEN; the other
+ * rows are not touched by it.
+ * logits      device [B, V], rows stride elements apart (>= V): bf16, or fp32
+ *             where fp32 is not 0; aligned to its element
+ * temperature, top_p, min_p device fp32 [B], top_k device int32 [B]; each may
+ *             be NULL: 1, 1, 0, 0 for every row
+ * u           device fp32 [B]
+ * tokens      device int32 [B] out; logprobs device fp32 [B] out or NULL
+ * status      device int32
+ * 1 <= V <= 393216; B >= 0 (0: a no-op). */
+PQE_API int sample_tokens(const void *logits, int fp32, int64_t stride, int B, int V, const float *temperature,
+                          const int32_t *top_k, const float *top_p, const float *min_p, const float *u,
+                          int32_t *tokens, float *logprobs, int32_t *status, void *stream);
 
 /* ------------------------------------------------------------------------
  * Layer runtime -- one MoE layer over its own slot pool, one call per step.

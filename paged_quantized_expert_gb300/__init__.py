@@ -32,11 +32,13 @@ PQE_STATUS_BAD_EXPERT_ID = 0x1
 PQE_STATUS_CORRUPT_STREAM = 0x2
 PQE_STATUS_BAD_PAGE = 0x4
 PQE_STATUS_TIMEOUT = 0x8
+PQE_STATUS_NO_TOKEN = 0x10
 
 PQE_FMT_FP8 = 0
 PQE_FMT_MXFP4 = 1
 PQE_Q8_ROW = 0
 PQE_Q8_MX = 1
+PQE_Q8_B128 = 2
 PQE_HUFF_LUT_BYTES = 16384
 
 LIB_PATH = _build.LIB
@@ -149,6 +151,10 @@ _SIGS = {
     "kv_paged_attention": (I32, [C.POINTER(pqe_kv_cache), P, C.c_int64, P, P, P, I32, I32, I32, I32, I32, C.c_float,
                                  I32, I32, P, P, P, SZ, P, P]),
     "add_rms_norm": (I32, [P, C.c_int64, P, C.c_int64, P, C.c_float, I32, I32, P, P, P, P, I32, P]),
+    "fp8_block_quantize": (I32, [P, C.c_int64, I32, I32, P, P, P]),
+    "pqe_quantize_fp8_blocks": (I32, [P, I32, I32, P, P, P]),
+    "fp8_block_matmul": (I32, [P, C.c_int64, P, P, P, I32, I32, I32, P, C.c_int64, I32, P, P]),
+    "sample_tokens": (I32, [P, I32, C.c_int64, I32, I32, P, P, P, P, P, P, P, P, P]),
     "pqe_layer_scratch_bytes": (SZ, [P]),
     "pqe_layer_create": (P, [P, C.POINTER(pqe_pool), P, P, P, P, P, SZ]),
     "pqe_layer_destroy": (None, [P]),
@@ -441,8 +447,9 @@ def kv_paged_attention(cache: pqe_kv_cache, q, q_offsets, kv_lens, block_table, 
 
 
 def add_rms_norm(x, residual, weight, eps: float, sum_out, y, q=None, q_scale=None, q_fmt: int = PQE_Q8_ROW, stream=None):
-    """h = x + residual, y = RMSnorm(h) * weight; sum_out, y bf16 [T, H] and q E4M3 [T, H] with q_scale (fp32 [T], or
-    E8M0 bytes [T, H/32] with PQE_Q8_MX), each optional. x, residual: bf16 [T, H], rows may lie apart."""
+    """h = x + residual, y = RMSnorm(h) * weight; sum_out, y bf16 [T, H] and q E4M3 [T, H] with q_scale (fp32 [T], E8M0
+    bytes [T, H/32] with PQE_Q8_MX, or fp32 [T, ceil(H/128)] with PQE_Q8_B128), each optional. x, residual: bf16 [T, H],
+    rows may lie apart."""
     T, H = x.shape
     if T == 0:
         return
@@ -455,11 +462,102 @@ def add_rms_norm(x, residual, weight, eps: float, sum_out, y, q=None, q_scale=No
     if q is not None:
         if q.element_size() != 1 or q.numel() < n:
             raise ValueError("q must hold T * H bytes")
-        if q_scale is None or _nbytes(q_scale) < (4 * T if q_fmt == PQE_Q8_ROW else n // 32):
+        if q_scale is None or _nbytes(q_scale) < (4 * T if q_fmt == PQE_Q8_ROW else 4 * T * _blocks(H) if q_fmt == PQE_Q8_B128
+                                                  else n // 32):
             raise ValueError("q_scale is missing or too small")
         qp, cp = _ptr(q), _ptr(q_scale)
     _check("add_rms_norm", lib().add_rms_norm(xp, xs, rp, rs, _typed(weight, torch.bfloat16, "weight", H), eps, T, H, sp, yp,
                                               qp, cp, q_fmt, _stream(stream)))
+
+
+# ---- block-scaled FP8 products, sampling ------------------------------------------
+
+def _blocks(n: int) -> int:
+    """Blocks of 128 in a row of n."""
+    return -(-n // 128)
+
+
+def _on_device(*tensors):
+    """Every tensor lies on the current CUDA device, whose streams the call uses."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != dev):
+            raise ValueError(f"expected tensors on the current CUDA device, got one on {t.device}")
+
+
+def _matrix(t: torch.Tensor, name: str) -> tuple[int, int]:
+    """Pointer and row stride (elements) of a matrix whose rows, each contiguous, may lie apart."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected a matrix of contiguous rows, got {tuple(t.shape)} with strides {t.stride()}")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _codes(t: torch.Tensor, name: str):
+    if t.dtype is not torch.uint8 and t.dtype is not torch.float8_e4m3fn:
+        raise ValueError(f"{name}: expected E4M3 codes (float8_e4m3fn or uint8), got {t.dtype}")
+
+
+def fp8_block_quantize(x, q, scale, stream=None):
+    """x bf16 [T, H] (rows may lie apart) to E4M3 codes q [T, H] and fp32 scales [T, ceil(H/128)]."""
+    T, H = x.shape
+    if T == 0:
+        return
+    _codes(q, "q")
+    xp, xs = _rows(x, T, (H,))
+    args = (xp, xs, T, H, _typed(q, q.dtype, "q", T * H), _typed(scale, torch.float32, "scale", T * _blocks(H)))
+    _on_device(x, q, scale)
+    _check("fp8_block_quantize", lib().fp8_block_quantize(*args, _stream(stream)))
+
+
+def pqe_quantize_fp8_blocks(w, q, scale, stream=None):
+    """Weights w fp32 [rows, cols] to E4M3 codes q [rows, cols] and one fp32 scale for each 128 x 128 tile."""
+    rows, cols = w.shape
+    _codes(q, "q")
+    args = (_typed(w, torch.float32, "w", 0), rows, cols, _typed(q, q.dtype, "q", rows * cols),
+            _typed(scale, torch.float32, "scale", _blocks(rows) * _blocks(cols)))
+    _on_device(w, q, scale)
+    _check("pqe_quantize_fp8_blocks", lib().pqe_quantize_fp8_blocks(*args, _stream(stream)))
+
+
+def fp8_block_matmul(x, x_scale, w, w_scale, out, status, stream=None):
+    """out [M, N] (bf16 or fp32; rows may lie apart) = x W^T of E4M3 codes x [M, K] (rows may lie apart) with fp32 scales
+    [M, ceil(K/128)] and w [N, K] with [ceil(N/128), ceil(K/128)]."""
+    M, K = x.shape
+    N = w.shape[0]
+    if w.dim() != 2 or w.shape[1] != K or out.shape != (M, N):
+        raise ValueError(f"shapes do not fit: x {tuple(x.shape)}, w {tuple(w.shape)}, out {tuple(out.shape)}")
+    if out.dtype is not torch.bfloat16 and out.dtype is not torch.float32:
+        raise ValueError(f"out: expected bf16 or fp32, got {out.dtype}")
+    if M == 0:
+        return
+    _codes(x, "x")
+    _codes(w, "w")
+    xp, xs = _matrix(x, "x")
+    op, os_ = _matrix(out, "out")
+    f32 = torch.float32
+    args = (xp, xs, _typed(x_scale, f32, "x_scale", M * _blocks(K)), _typed(w, w.dtype, "w", N * K),
+            _typed(w_scale, f32, "w_scale", _blocks(N) * _blocks(K)), M, N, K, op, os_, int(out.dtype is f32),
+            _typed(status, torch.int32, "status", 1))
+    _on_device(x, x_scale, w, w_scale, out, status)
+    _check("fp8_block_matmul", lib().fp8_block_matmul(*args, _stream(stream)))
+
+
+def sample_tokens(logits, u, tokens, status, temperature=None, top_k=None, top_p=None, min_p=None, logprobs=None, stream=None):
+    """The next token of each row of logits [B, V] (bf16 or fp32; rows may lie apart) into tokens int32 [B], from uniform
+    numbers u fp32 [B] in [0, 1); temperature, top_p, min_p fp32 [B], top_k int32 [B], logprobs fp32 [B] out."""
+    B, V = logits.shape
+    if logits.dtype is not torch.bfloat16 and logits.dtype is not torch.float32:
+        raise ValueError(f"logits: expected bf16 or fp32, got {logits.dtype}")
+    if B == 0:
+        return
+    lp, ls = _matrix(logits, "logits")
+    f32, i32 = torch.float32, torch.int32
+    opt = lambda t, dtype, name: None if t is None else _typed(t, dtype, name, B)  # noqa: E731
+    args = (lp, int(logits.dtype is f32), ls, B, V, opt(temperature, f32, "temperature"), opt(top_k, i32, "top_k"),
+            opt(top_p, f32, "top_p"), opt(min_p, f32, "min_p"), _typed(u, f32, "u", B), _typed(tokens, i32, "tokens", B),
+            opt(logprobs, f32, "logprobs"), _typed(status, i32, "status", 1))
+    _on_device(logits, u, tokens, status, temperature, top_k, top_p, min_p, logprobs)
+    _check("sample_tokens", lib().sample_tokens(*args, _stream(stream)))
 
 
 # ---- pager ---------------------------------------------------------------------

@@ -11,10 +11,12 @@
 // bound by memory then (16384 rows of 2560, bf16 sum and codes out: 49.5 us, 5.96
 // TB/s), by the latency of one load, two reductions and a store where there are
 // few (64 rows of 2048: 2.4 us).
+#include "fp8_codes.cuh"
 #include "pqe_common.cuh"
 
 namespace pqe {
 namespace norm {
+using namespace fp8;
 
 struct Args {
     const uint16_t *x, *r, *w;
@@ -32,18 +34,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-
-__device__ __forceinline__ void unpack8(const uint4 &u, float (&f)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-}
-
-// bits of |f|: they order as the values do, with NaN above infinity
-__device__ __forceinline__ uint32_t abs_bits(float f) { return __float_as_uint(f) & 0x7FFFFFFFu; }
 
 // What a thread (of a warp or a CTA that shares a row) does with its V vectors of eight values, vector j at index
 // first + j * step of the row.
@@ -134,22 +124,37 @@ struct Part {
         return top;
     }
 
+    // the codes with a scale for each 128 values: sixteen neighbouring lanes (the last block may end early). As for
+    // scale(), all 32 lanes are here.
+    __device__ __forceinline__ void block_codes(const Args &a, int row, int first, int step) {
+        const int nv = a.H / 8;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int i = first + j * step;
+            uint32_t t = 0;
+            if (i < nv) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t = max(t, abs_bits(h[j][e]));
+            }
+#pragma unroll
+            for (int o = 1; o < 16; o *= 2) t = max(t, __shfl_xor_sync(0xffffffffu, t, o));
+            if (i >= nv) continue;
+            const float s = scale_of(t);
+            reinterpret_cast<uint2 *>(a.q + (size_t)row * a.H)[i] = codes8(h[j], s);
+            if (i % 16 == 0) static_cast<float *>(a.q_scale)[(size_t)row * ((a.H + 127) / 128) + i / 16] = s;
+        }
+    }
+
     // the codes with one scale for the row
     __device__ __forceinline__ void codes(const Args &a, int row, int first, int step, uint32_t top) {
         const int nv = a.H / 8;
-        float s = top > 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float(top) / 448.f;
-        if (s == 0.f) s = 1.f;  // a row of zeros, or one so small that fp32 does not hold its scale
+        const float s = scale_of(top);
         if (first == 0) static_cast<float *>(a.q_scale)[row] = s;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int i = first + j * step;
             if (i >= nv) break;
-            uint32_t o[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                o[e] = (uint32_t)f32x2_to_e4m3x2(h[j][4 * e] / s, h[j][4 * e + 1] / s) |
-                       (uint32_t)f32x2_to_e4m3x2(h[j][4 * e + 2] / s, h[j][4 * e + 3] / s) << 16;
-            reinterpret_cast<uint2 *>(a.q + (size_t)row * a.H)[i] = make_uint2(o[0], o[1]);
+            reinterpret_cast<uint2 *>(a.q + (size_t)row * a.H)[i] = codes8(h[j], s);
         }
     }
 };
@@ -168,6 +173,7 @@ __global__ void __launch_bounds__(512) norm_cta_kernel(const Args a) {
     ss = 0.f;
     for (int i = 0; i < nw; ++i) ss += part_sum[i];
     uint32_t top = p.scale(a, row, threadIdx.x, blockDim.x, rsqrtf(fmaf(ss, a.mean, a.eps)));
+    if (a.q && a.fmt == PQE_Q8_B128) p.block_codes(a, row, threadIdx.x, blockDim.x);
     if (!a.q || a.fmt != PQE_Q8_ROW) return;
     top = __reduce_max_sync(0xffffffffu, top);
     if (lane == 0) part_max[warp] = top;
@@ -188,6 +194,7 @@ __global__ void __launch_bounds__(32 * ROW_WARPS) norm_warp_kernel(const Args a,
     const float ss = warp_sum(p.load(a, row, lane, 32));
     const uint32_t top = p.scale(a, row, lane, 32, rsqrtf(fmaf(ss, a.mean, a.eps)));
     if (a.q && a.fmt == PQE_Q8_ROW) p.codes(a, row, lane, 32, __reduce_max_sync(0xffffffffu, top));
+    if (a.q && a.fmt == PQE_Q8_B128) p.block_codes(a, row, lane, 32);
 }
 
 }  // namespace norm
@@ -206,7 +213,7 @@ int add_rms_norm(const void *x, int64_t x_stride, const void *residual, int64_t 
     PQE_CHECK_ARG(!residual || (r_stride >= H && r_stride % 8 == 0));
     PQE_CHECK_ARG(aligned(x, 16) && aligned(residual, 16) && aligned(weight, 16) && aligned(sum_out, 16) &&
                   aligned(y_out, 16) && aligned(q, 8));
-    PQE_CHECK_ARG(!q || (q_scale && (q_fmt == PQE_Q8_MX || (q_fmt == PQE_Q8_ROW && aligned(q_scale, 4)))));
+    PQE_CHECK_ARG(!q || (q_scale && (q_fmt == PQE_Q8_MX || ((q_fmt == PQE_Q8_ROW || q_fmt == PQE_Q8_B128) && aligned(q_scale, 4)))));
     float c = 1.f;
     while (c * c * (float)H > 1.f) c *= 0.5f;
     const norm::Args a{static_cast<const uint16_t *>(x), static_cast<const uint16_t *>(residual),

@@ -1,0 +1,281 @@
+"""Block-scaled FP8 products: the quantisers bit for bit, the product against 64 bits.
+
+The product's bound: within a block of 128 the tensor cores sum 32 products and the sum so far at a time, each aligned to the
+largest and cut to 24 bits or more, so a block is off by at most 4 * 33 * 2^-24 of its sum of |x w|; the scaled blocks are
+added with one rounding each (kb of them), and the two scales' product is rounded once: (132 + kb + 2) * 2^-24 of
+A = sum |xs ws x w| in all. bf16 results add half a step, 2^-8 of the value."""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def tiles(x, rows):
+    """fp32 [n, k] -> codes and scales of rows x 128 tiles, on the CPU in fp32."""
+    n, k = x.shape
+    x = x.float().cpu()
+    pad = torch.nn.functional.pad(x, (0, -k % 128, 0, -n % rows))
+    t = pad.unflatten(0, (-1, rows)).unflatten(2, (-1, 128))
+    amax = t.abs().amax((1, 3))
+    s = amax / 448
+    s = torch.where(s == 0, 1.0, s)
+    q = (t / s[:, None, :, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+    return q.flatten(2).flatten(0, 1)[:n, :k].contiguous(), s
+
+
+def exact(xq, xs, wq, ws):
+    """The product and the sum of its terms' absolute values, in 64 bits."""
+    N, K = wq.shape
+    x = xq.to(DEV).double() * xs.to(DEV).double().repeat_interleave(128, 1)[:, :K]
+    w = wq.to(DEV).double() * ws.to(DEV).double().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+    return x @ w.T, x.abs() @ w.abs().T
+
+
+def inputs(M, N, K, seed=0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn((M, K), generator=g, device=DEV) * (1 + 30 * (torch.rand(K, generator=g, device=DEV) < 0.02))
+    w = torch.randn((N, K), generator=g, device=DEV) * torch.rand((N, 1), generator=g, device=DEV)
+    # blocks of very different sizes, so that a scale taken from a neighbour shows
+    x *= 2.0 ** torch.randint(-6, 7, (M, -(-K // 128)), generator=g, device=DEV).repeat_interleave(128, 1)[:, :K]
+    w *= 2.0 ** torch.randint(-6, 7, (-(-N // 128), -(-K // 128)), generator=g, device=DEV).repeat_interleave(128, 1)[:, :K].repeat_interleave(128, 0)[:N]
+    xq, xs = tiles(x, 1)
+    wq, ws = tiles(w, 128)
+    return xq.to(DEV), xs.to(DEV), wq.to(DEV), ws.to(DEV)
+
+
+def check(out, xq, xs, wq, ws):
+    want, A = exact(xq, xs, wq, ws)
+    bound = (132 + xs.shape[1] + 2) * 2.0 ** -24 * A
+    if out.dtype is torch.bfloat16:
+        bound = bound * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs()
+    off = (out.double() - want).abs()
+    assert torch.isfinite(out).all() and not (off > bound).any(), f"worst {(off / bound.clamp(min=1e-300)).max().item():.3g} of the bound"
+
+
+# ---- quantisers ----
+
+
+@pytest.mark.parametrize("T,H", [(1, 16), (1, 128), (3, 144), (64, 2560), (5, 112), (7, 2064), (1000, 1040), (3, 32768), (5000, 256)])
+def test_quantize_rows(cuda_lib, T, H):
+    g = torch.Generator(device=DEV).manual_seed(T + H)
+    x = (torch.randn((T, H), generator=g, device=DEV) * 2.0 ** torch.randint(-20, 20, (T, 1), generator=g, device=DEV)).bfloat16()
+    x[0, :16] = 0
+    if H > 128:
+        x[0, :128] = 0
+    q = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=DEV)
+    s = torch.empty((T, -(-H // 128)), device=DEV)
+    cuda_lib.fp8_block_quantize(x, q, s)
+    wq, ws = tiles(x, 1)
+    assert torch.equal(s.cpu(), ws) and torch.equal(q.cpu().view(torch.uint8), wq.view(torch.uint8))
+
+
+def test_quantize_rows_of_a_wider_tensor_and_special_values(cuda_lib):
+    T, H = 6, 272
+    wide = torch.randn((T, 400), device=DEV).bfloat16()
+    x = wide[:, 64:64 + H]
+    x[1, 3] = float("nan")
+    x[2, 200] = float("inf")
+    x[3] = 2.0 ** -133
+    x[4] = 3e38
+    q = torch.full((T + 1, H), 0x55, dtype=torch.uint8, device=DEV)
+    s = torch.full((T + 1, 3), 7.0, device=DEV)
+    cuda_lib.fp8_block_quantize(x, q, s)
+    wq, ws = tiles(x, 1)
+    rows = [0, 3, 4, 5]
+    assert torch.equal(s.cpu()[rows], ws[rows]) and torch.equal(q.cpu()[rows], wq.view(torch.uint8)[rows])
+    f = q.view(torch.float8_e4m3fn).float()
+    assert torch.isnan(s[1, 0]) and torch.isnan(f[1, :128]).all() and torch.isfinite(f[1, 128:]).all() and torch.isfinite(s[1, 1:]).all()
+    assert torch.isinf(s[2, 1]) and torch.isnan(f[2, 200]) and (f[2, 128:200] == 0).all() and torch.isfinite(s[2, [0, 2]]).all()
+    assert (q[T] == 0x55).all() and (s[T] == 7).all()  # rows behind the last one stay as they were
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (128, 128), (129, 300), (1000, 2048), (257, 1040)])
+def test_quantize_tiles(cuda_lib, rows, cols):
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    w = torch.randn((rows, cols), generator=g, device=DEV)
+    w[:, : min(cols, 128)] *= 1e-3
+    w[: min(rows, 128), : min(cols, 128)] = 0
+    q = torch.empty((rows, cols), dtype=torch.uint8, device=DEV)
+    s = torch.empty((-(-rows // 128), -(-cols // 128)), device=DEV)
+    cuda_lib.pqe_quantize_fp8_blocks(w, q, s)
+    wq, ws = tiles(w, 128)
+    assert torch.equal(s.cpu(), ws) and torch.equal(q.cpu(), wq.view(torch.uint8))
+
+
+@pytest.mark.parametrize("T,H", [(1, 32), (3, 160), (64, 2048), (5, 2560), (1300, 2560), (2000, 96), (1, 16384), (2, 8224)])
+def test_norm_with_block_scales(cuda_lib, T, H):
+    """The bounds of the norm's other formats (fp32 work under 2^-16 relative, a code within 2^-4 of y or half its smallest step)."""
+    import attention_ref as ref
+    g = torch.Generator(device=DEV).manual_seed(T + H)
+    x = torch.randn((T, H), generator=g, device=DEV).bfloat16()
+    r = (4 * torch.randn((T, H), generator=g, device=DEV) * (1 + 20 * (torch.rand(H, generator=g, device=DEV) < 0.02))).bfloat16()
+    w = (1 + 0.3 * torch.randn(H, generator=g, device=DEV)).bfloat16()
+    x[0, : min(H, 128)] = 0
+    r[0, : min(H, 128)] = 0
+    res, y = (torch.empty((T, H), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    q = torch.empty((T, H), dtype=torch.uint8, device=DEV)
+    s = torch.empty((T, -(-H // 128)), device=DEV)
+    cuda_lib.add_rms_norm(x, r, w, 1e-6, res, y, q, s, cuda_lib.PQE_Q8_B128)
+    h64, y64 = ref.norm(x, r, w, 1e-6)
+    U = 2.0 ** -8
+    assert ((res.double() - h64).abs() <= U * (1 + U) * h64.abs()).all() and ((y.double() - y64).abs() <= U * (1 + U) * y64.abs()).all()
+    amax = torch.stack([b.abs().amax(1) for b in y64.split(128, 1)], 1)
+    want = torch.where(amax == 0, 1.0, amax / 448)
+    assert ((s.double() - want).abs() <= 2.0 ** -16 * want).all()
+    scale = s.double().repeat_interleave(128, 1)[:, :H]
+    got = q.view(torch.float8_e4m3fn).double() * scale
+    assert ((got - y64).abs() <= (1 + U) * (2.0 ** -4 * y64.abs() + 2.0 ** -10 * scale)).all()
+
+
+# ---- the product ----
+
+SHAPES = [(1, 1, 16), (1, 128, 128), (1, 3584, 2048), (2, 130, 144), (3, 1000, 272), (7, 64, 4096), (8, 2048, 2560), (15, 257, 1024),
+          (16, 4096, 512), (17, 384, 1040), (31, 1003, 656), (33, 5000, 128), (48, 2048, 2048), (64, 2048, 2560), (65, 512, 8192),
+          (96, 1152, 384), (127, 129, 2048), (128, 128, 128), (129, 2560, 1040), (200, 640, 16384), (255, 1024, 2048), (256, 384, 640),
+          (257, 3584, 512), (333, 1003, 1040), (511, 768, 2560), (777, 2048, 256), (1024, 2560, 2048), (1025, 131, 1168), (2050, 1280, 384),
+          (4099, 3584, 2048), (300, 20000, 512), (5, 40000, 256), (40, 33000, 784)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_product(cuda_lib, M, N, K, dtype):
+    a = inputs(M, N, K, M + N + K)
+    out = torch.full((M, N), float("nan"), dtype=dtype, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    cuda_lib.fp8_block_matmul(*a, out, status)
+    check(out, *a)
+    assert status.item() == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 200, 528), (64, 1003, 256), (300, 328, 400), (1100, 1290, 272)])
+@pytest.mark.parametrize("dtype,shift", [(torch.bfloat16, 0), (torch.bfloat16, 1), (torch.bfloat16, 8), (torch.float32, 0), (torch.float32, 3)])
+def test_rows_that_lie_apart(cuda_lib, M, N, K, dtype, shift):
+    """x and out as parts of wider tensors, out at any element; what lies around it stays."""
+    a = list(inputs(M, N, K, 5))
+    wide = torch.zeros((M, K + 48), dtype=torch.uint8, device=DEV)
+    wide[:, 16:16 + K] = a[0].view(torch.uint8)
+    a[0] = wide[:, 16:16 + K].view(torch.float8_e4m3fn)
+    buf = torch.full((M + 2, N + 16), 123.0, dtype=dtype, device=DEV)
+    out = buf[1:M + 1, shift:shift + N]
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    cuda_lib.fp8_block_matmul(*a, out, status)
+    check(out, *a)
+    mask = torch.ones_like(buf, dtype=torch.bool)
+    mask[1:M + 1, shift:shift + N] = False
+    assert (buf[mask] == 123).all() and status.item() == 0
+
+
+@pytest.mark.parametrize("M", [1, 20, 64, 200, 600])
+def test_same_result_every_time_and_for_every_row(cuda_lib, M):
+    """A row's result does not change from run to run."""
+    a = inputs(M, 1000, 2064, 9)
+    outs = [torch.empty((M, 1000), device=DEV) for _ in range(3)]
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for o in outs:
+        cuda_lib.fp8_block_matmul(*a, o, status)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@pytest.mark.parametrize("M", [4, 70, 500])
+def test_nan_stays_in_its_rows_and_columns(cuda_lib, M):
+    N, K = 500, 400
+    xq, xs, wq, ws = inputs(M, N, K, 2)
+    xq.view(torch.uint8)[1, 5] = 0x7F
+    xs[2, 3] = float("nan")
+    wq.view(torch.uint8)[7, 399] = 0xFF
+    ws[2, 1] = float("nan")
+    out = torch.empty((M, N), device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    cuda_lib.fp8_block_matmul(xq, xs, wq, ws, out, status)
+    bad = torch.zeros((M, N), dtype=torch.bool, device=DEV)
+    bad[1] = bad[2] = True
+    bad[:, 7] = True
+    bad[:, 256:384] = True
+    assert torch.equal(torch.isnan(out), bad)
+
+
+def test_largest_values_and_zeros(cuda_lib):
+    """Every code at its largest: sums of 448 * 448 * 128; and rows of zeros."""
+    M, N, K = 130, 260, 1024
+    xq = torch.full((M, K), 448.0, device=DEV).to(torch.float8_e4m3fn)
+    wq = torch.full((N, K), -448.0, device=DEV).to(torch.float8_e4m3fn)
+    xq.view(torch.uint8)[3] = 0x80  # -0
+    xs, ws = torch.full((M, 8), 2.0 ** 40, device=DEV), torch.full((3, 8), 2.0 ** -30, device=DEV)
+    out = torch.empty((M, N), device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    cuda_lib.fp8_block_matmul(xq, xs, wq, ws, out, status)
+    want = torch.full((M, N), -448.0 * 448 * 1024 * 2 ** 10, device=DEV)
+    want[3] = 0
+    assert torch.equal(out, want)
+
+
+def test_no_rows(cuda_lib):
+    _, _, wq, ws = inputs(1, 10, 16)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    n = cuda_lib.lib().pqe_kernel_launches()
+    cuda_lib.fp8_block_matmul(wq[:0], ws[:0], wq, ws, torch.empty((0, 10), device=DEV), status)
+    cuda_lib.fp8_block_quantize(torch.empty((0, 16), dtype=torch.bfloat16, device=DEV), wq[:0], ws[:0])
+    assert cuda_lib.lib().pqe_kernel_launches() == n
+
+
+@pytest.mark.parametrize("M", [1, 64, 300, 2048])
+def test_in_a_graph_and_on_another_stream(cuda_lib, M):
+    """Two captured calls on two streams, replayed together with new inputs in place."""
+    N, K = 1100, 640
+    a, b = inputs(M, N, K, 1), inputs(M, N, K, 2)
+    outs = [torch.empty((M, N), device=DEV) for _ in range(2)]
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    graphs = []
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for o, s in zip(outs, streams):
+        g = torch.cuda.CUDAGraph()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(g, stream=s):
+            cuda_lib.fp8_block_matmul(*(a if o is outs[0] else b), o, status)
+        graphs.append(g)
+    c = inputs(M, N, K, 3)
+    for dst, src in zip(a, c):
+        dst.copy_(src)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    check(outs[0], *c)
+    check(outs[1], *b)
+    assert status.item() == 0
+
+
+def test_chain_of_norm_product_quantise_product(cuda_lib):
+    """As a layer runs them: norm with codes, product, codes of its rows, product."""
+    T, H, n = 70, 512, 640
+    g = torch.Generator(device=DEV).manual_seed(4)
+    x, r = (torch.randn((T, H), generator=g, device=DEV).bfloat16() for _ in range(2))
+    w = torch.ones(H, dtype=torch.bfloat16, device=DEV)
+    ws = [torch.randn(s, generator=g, device=DEV) * s[1] ** -0.5 for s in ((n, H), (H, n))]
+    packed = []
+    for m in ws:
+        q, s = torch.empty(m.shape, dtype=torch.float8_e4m3fn, device=DEV), torch.empty((-(-m.shape[0] // 128), m.shape[1] // 128), device=DEV)
+        cuda_lib.pqe_quantize_fp8_blocks(m, q, s)
+        packed.append((q, s))
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    q1, s1 = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=DEV), torch.empty((T, H // 128), device=DEV)
+    cuda_lib.add_rms_norm(x, r, w, 1e-6, None, None, q1, s1, cuda_lib.PQE_Q8_B128)
+    mid = torch.empty((T, n), dtype=torch.bfloat16, device=DEV)
+    cuda_lib.fp8_block_matmul(q1, s1, *packed[0], mid, status)
+    q2, s2 = torch.empty((T, n), dtype=torch.float8_e4m3fn, device=DEV), torch.empty((T, n // 128), device=DEV)
+    cuda_lib.fp8_block_quantize(mid, q2, s2)
+    out = torch.empty((T, H), device=DEV)
+    cuda_lib.fp8_block_matmul(q2, s2, *packed[1], out, status)
+    check(mid, q1, s1, *packed[0])
+    check(out, q2, s2, *packed[1])
+    h = (x.double() + r.double())
+    y = h / (h.square().mean(1, keepdim=True) + 1e-6).sqrt()
+    full = (y @ ws[0].double().T) @ ws[1].double().T
+    # four codings on the way, each off by 2^-4 / sqrt(3) of a power of two at most, values spread over [1, 2) of it: 0.026 of
+    # a value each, 0.052 together by chance; half as much again is allowed
+    assert ((out.double() - full).norm() / full.norm()).item() < 0.078 and math.isfinite(out.sum().item())
