@@ -782,7 +782,15 @@ PQE_API int pqe_quantize_fp8_blocks(const float *w, int rows, int cols, uint8_t 
  * out     device [M, N], rows out_stride elements apart (>= N): bf16, or fp32
  *         where out_fp32 is not 0; aligned to its element. It overlaps no input.
  * status  device int32: PQE_STATUS_TIMEOUT as elsewhere
- * K % 16 == 0, 16 <= K <= 32768; 1 <= N <= 2^22; M >= 0 (0: a no-op). */
+ * K % 16 == 0, 16 <= K <= 32768; 1 <= N <= 2^22; 0 <= M <= 2^28 (0: a no-op). */
+/* (pqe_test_set_matmul_kernel: a test hook, which kernel the call takes whatever
+ * its sizes. tile 16 or 32: the one for few rows, that many tokens a tile, the
+ * blocks of K shared by 2^split CTAs (up to 4; 8 with 32 tokens; fewer where K
+ * has fewer blocks). tile 128 or 256: the one for many rows, that many a tile,
+ * by split columns (128; 128 or 256). 0, 0: the default choice. Only roundings
+ * differ. PQE_ERR_INVALID_ARG for anything else. Process-wide, read at each
+ * call.) */
+PQE_API int pqe_test_set_matmul_kernel(int tile, int split);
 PQE_API int fp8_block_matmul(const uint8_t *x, int64_t x_stride, const float *x_scale, const uint8_t *w,
                              const float *w_scale, int M, int N, int K, void *out, int64_t out_stride, int out_fp32,
                              int32_t *status, void *stream);

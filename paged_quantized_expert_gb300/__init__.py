@@ -153,6 +153,7 @@ _SIGS = {
     "add_rms_norm": (I32, [P, C.c_int64, P, C.c_int64, P, C.c_float, I32, I32, P, P, P, P, I32, P]),
     "fp8_block_quantize": (I32, [P, C.c_int64, I32, I32, P, P, P]),
     "pqe_quantize_fp8_blocks": (I32, [P, I32, I32, P, P, P]),
+    "pqe_test_set_matmul_kernel": (I32, [I32, I32]),
     "fp8_block_matmul": (I32, [P, C.c_int64, P, P, P, I32, I32, I32, P, C.c_int64, I32, P, P]),
     "sample_tokens": (I32, [P, I32, C.c_int64, I32, I32, P, P, P, P, P, P, P, P, P]),
     "pqe_layer_scratch_bytes": (SZ, [P]),
@@ -517,6 +518,12 @@ def pqe_quantize_fp8_blocks(w, q, scale, stream=None):
             _typed(scale, torch.float32, "scale", _blocks(rows) * _blocks(cols)))
     _on_device(w, q, scale)
     _check("pqe_quantize_fp8_blocks", lib().pqe_quantize_fp8_blocks(*args, _stream(stream)))
+
+
+def pqe_test_set_matmul_kernel(tile: int, split: int):
+    """Test hook: the kernel of fp8_block_matmul by its tile (16, 32: few rows; 128, 256: many) and split; 0, 0 the default
+    choice."""
+    _check("pqe_test_set_matmul_kernel", lib().pqe_test_set_matmul_kernel(int(tile), int(split)))
 
 
 def fp8_block_matmul(x, x_scale, w, w_scale, out, status, stream=None):

@@ -132,6 +132,54 @@ def test_norm_with_block_scales(cuda_lib, T, H):
 
 # ---- the product ----
 
+# every kernel: (tile, split) of pqe_test_set_matmul_kernel
+KERNELS = [(16, 0), (16, 1), (16, 2), (32, 0), (32, 1), (32, 2), (32, 3), (128, 128), (256, 128), (256, 256)]
+
+
+@pytest.fixture
+def kernel(request, cuda_lib):
+    cuda_lib.pqe_test_set_matmul_kernel(*request.param)
+    yield request.param
+    cuda_lib.pqe_test_set_matmul_kernel(0, 0)
+
+
+@pytest.mark.parametrize("kernel", KERNELS, indirect=True, ids=lambda k: f"{k[0]}-{k[1]}")
+@pytest.mark.parametrize("M,N,K", [(1, 1, 16), (3, 130, 144), (17, 257, 1024), (64, 2048, 2560), (129, 300, 4096), (300, 1003, 1040), (777, 2050, 1168),
+                                   (2050, 1280, 384), (20, 70000, 272)])
+def test_every_kernel(cuda_lib, kernel, M, N, K):
+    a = inputs(M, N, K, M + N)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for dtype in (torch.float32, torch.bfloat16):
+        out = torch.full((M, N), float("nan"), dtype=dtype, device=DEV)
+        cuda_lib.fp8_block_matmul(*a, out, status)
+        check(out, *a)
+    wide = torch.full((M + 2, N + 9), 123.0, dtype=torch.bfloat16, device=DEV)  # rows that end and begin anywhere
+    cuda_lib.fp8_block_matmul(*a, wide[1:M + 1, 3:N + 3], status)
+    check(wide[1:M + 1, 3:N + 3], *a)
+    wide[1:M + 1, 3:N + 3] = 123
+    assert (wide == 123).all() and status.item() == 0
+
+
+@pytest.mark.parametrize("kernel", KERNELS, indirect=True, ids=lambda k: f"{k[0]}-{k[1]}")
+def test_waits_that_expire(cuda_lib, kernel):
+    """With a limit of one poll a call may give up its waits: it returns, says so, and the next call is right."""
+    a = inputs(300, 700, 2048, 3)
+    out = torch.empty((300, 700), device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    cuda_lib.lib().pqe_set_wait_limit(1)
+    try:
+        for _ in range(3):
+            cuda_lib.fp8_block_matmul(*a, out, status)
+        torch.cuda.synchronize()
+    finally:
+        cuda_lib.lib().pqe_set_wait_limit(0)
+    assert status.item() in (0, cuda_lib.PQE_STATUS_TIMEOUT)
+    status.zero_()
+    cuda_lib.fp8_block_matmul(*a, out, status)
+    check(out, *a)
+    assert status.item() == 0
+
+
 SHAPES = [(1, 1, 16), (1, 128, 128), (1, 3584, 2048), (2, 130, 144), (3, 1000, 272), (7, 64, 4096), (8, 2048, 2560), (15, 257, 1024),
           (16, 4096, 512), (17, 384, 1040), (31, 1003, 656), (33, 5000, 128), (48, 2048, 2048), (64, 2048, 2560), (65, 512, 8192),
           (96, 1152, 384), (127, 129, 2048), (128, 128, 128), (129, 2560, 1040), (200, 640, 16384), (255, 1024, 2048), (256, 384, 640),

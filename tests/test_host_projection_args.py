@@ -24,7 +24,7 @@ def test_quantize_tiles_arguments(i, v):
 
 
 @pytest.mark.parametrize("i,v", [(0, None), (0, A + 8), (1, 112), (1, 136), (2, None), (2, A + 2), (3, None), (3, A + 8), (4, None), (4, A + 1), (5, -1),
-                                 (6, 0), (6, -3), (6, (1 << 22) + 1), (7, 0), (7, 8), (7, 130), (7, 32784), (8, None), (8, A + 2), (9, 63), (11, None),
+                                 (5, (1 << 28) + 1), (6, 0), (6, -3), (6, (1 << 22) + 1), (7, 0), (7, 8), (7, 130), (7, 32784), (8, None), (8, A + 2), (9, 63), (11, None),
                                  (11, A + 2)])
 def test_matmul_arguments(i, v):
     _refused(pqe.load().fp8_block_matmul, [A, 128, A, A, A, 2, 64, 128, A, 64, 1, A, None], i, v)
@@ -49,6 +49,13 @@ def test_without_work():
     assert lib.fp8_block_quantize(None, 0, 0, 128, None, None, None) == 0
     assert lib.fp8_block_matmul(None, 0, None, None, None, 0, 64, 128, None, 0, 0, None, None) == 0
     assert lib.sample_tokens(None, 0, 0, 0, 100, None, None, None, None, None, None, None, None, None) == 0
+
+
+def test_matmul_kernel_hook():
+    lib = pqe.load()
+    for tile, split in ((1, 0), (16, 3), (16, -1), (32, 4), (64, 0), (128, 256), (128, 0), (256, 0), (256, 64), (0, 1)):
+        assert lib.pqe_test_set_matmul_kernel(tile, split) == BAD
+    assert lib.pqe_test_set_matmul_kernel(0, 0) == 0
 
 
 def test_norm_takes_the_format():
