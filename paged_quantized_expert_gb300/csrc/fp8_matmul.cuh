@@ -6,6 +6,9 @@
 
 namespace pqe {
 namespace fp8mm {
+using ptx::cluster_rank;
+using ptx::cluster_sync;
+using ptx::map_rank;
 
 constexpr int BK = 128;  // values (bytes) of K in a scale block, and in a stage
 
@@ -147,31 +150,6 @@ __device__ __forceinline__ void umma_block(uint32_t leader, uint32_t d, uint32_t
     umma<CTAS, false>(leader, d, ad, bd, desc);
 #pragma unroll
     for (int k = 1; k < BK / 32; ++k) umma<CTAS, true>(leader, d, ad + 2 * k, bd + 2 * k, desc);
-}
-
-// address of the same place in the shared memory of CTA `rank` of the cluster
-__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// whether the phase is over, without waiting for it (a try_wait may hold the thread for a while)
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok)
-                 : "r"(bar), "r"(parity)
-                 : "memory");
-    return ok != 0;
 }
 
 // bounded wait for what other CTAs of the cluster wrote
