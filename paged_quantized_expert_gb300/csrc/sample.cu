@@ -74,6 +74,7 @@ struct Shared {
     u64 swap[4][MAX_PARTS][4];        // of the cluster's exchanges, four in turn
     int32_t table[OCTAVE + 1];        // TABLE
     uint32_t listed[3];               // entries of the list, of the inner one, of that once more
+    double min_drop;                  // t ln(min_p)
     Found found;
     u64 inner[INNER];
     union {
@@ -111,6 +112,15 @@ struct Scale {
         return shifted(mantissa(table, l, p, n), n);
     }
 };
+
+// the part p in [0, 1) of a sum, rounded down, and up (p as 64 bits after the point: exact from 2^-40 on)
+__device__ __forceinline__ u64 fixed(float p) { return __float2ull_rz(p * 18446744073709551616.f); }
+__device__ __forceinline__ u64 share(float p, u64 sum) { return __umul64hi(fixed(p), sum); }
+__device__ __forceinline__ u64 share_up(float p, u64 sum) {
+    if (!(p > 0.f)) return 0;
+    const u64 f = fixed(p);
+    return __umul64hi(f, sum) + (f * sum != 0);
+}
 
 template <class T>
 __device__ __forceinline__ T warp_scan(T v, int lane) {  // inclusive
@@ -195,6 +205,12 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // waited for before the first exchange
     pdl_acquire();
 
+    const float t = a.temperature ? a.temperature[row] : 1.f, top_p = a.top_p ? a.top_p[row] : 1.f;
+    const float min_p = a.min_p ? a.min_p[row] : 0.f, u = a.u[row];
+    const int top_k = a.top_k ? a.top_k[row] : 0;
+    // one thread: fp64 is slow here, and the row's loads hide it
+    if (threadIdx.x == THREADS - 1 && min_p > 0.f && min_p < 1.f && t > 0.f) sh.min_drop = (double)t * log((double)min_p);
+
     // ---- the row into shared memory, with its maximum ----
     float top = -INFINITY;
     bool bad = false;
@@ -246,9 +262,6 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
         const int tail = head + vecs * VEC + (int)threadIdx.x;
         if (tail < n) one(tail);
     }
-    const float t = a.temperature ? a.temperature[row] : 1.f, top_p = a.top_p ? a.top_p[row] : 1.f;
-    const float min_p = a.min_p ? a.min_p[row] : 0.f, u = a.u[row];
-    const int top_k = a.top_k ? a.top_k[row] : 0;
     __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // the other CTAs have begun
     bad = __any_sync(0xffffffffu, bad);
@@ -264,12 +277,16 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
         for (int r = 0; r < parts; ++r) key = max(key, (uint32_t)x[r][0]), bad |= x[r][1] != 0;
     }
     top = value_of(key);
-    auto answer = [&](int token, double sum) {
+    // (one thread) the token at a logit, whose weight is w of `sum`
+    auto answer = [&](int token, float l, u64 w, u64 sum) {
         a.tokens[row] = token;
         if (!a.logprobs) return;
-        if (t == 0.f) a.logprobs[row] = 0.f;
-        else
-            a.logprobs[row] = (float)(((double)data[token - c0] - (double)top) / (double)t - log(sum * (1.0 / (1ull << SCALE))));
+        float lp = 0.f;
+        if (t > 0.f) {
+            if (2 * w > sum) lp = log1pf(-((float)(sum - w) / (float)sum));  // near 0 by what the others weigh
+            else lp = 2.f * ((0.5f * l - 0.5f * top) / t) - logf((float)sum * (1.f / (1ull << SCALE)));
+        }
+        a.logprobs[row] = lp;
     };
     if (bad || !(top > -INFINITY) || !(t >= 0.f && t < INFINITY) || isnan(top_p) || isnan(min_p) || !(u >= 0.f && u < 1.f)) {
         if (rank == 0 && threadIdx.x == 0) {
@@ -294,21 +311,21 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
         u64(*x)[4] = exchange((u64)at, 0, 0, 0);
         bool mine = at != INT32_MAX;
         for (int r = 0; r < rank; ++r) mine &= (int)x[r][0] == INT32_MAX;
-        if (mine && threadIdx.x == 0) answer(at, 0);
+        if (mine && threadIdx.x == 0) answer(at, top, 1, 1);
         return;
     }
 
     Scale sc;
     {
-        const double c = fmin(2.0 * OCTAVE * 1.4426950408889634 / (double)t, 1e38);
+        constexpr float K_HI = 92.33248261689366f, K_LO = (float)(92.33248261689366 - (double)K_HI);  // 64 log2(e)
         sc.half_max = 0.5f * top;
-        sc.c_hi = (float)c;
-        sc.c_lo = (float)(c - (double)sc.c_hi);
+        sc.c_hi = fminf(K_HI / t, 1e38f);
+        sc.c_lo = sc.c_hi < 1e38f ? (fmaf(-sc.c_hi, t, K_HI) + K_LO) / t : 0.f;
     }
     // the lowest value that min_p leaves: w >= min_p exactly where l >= max + t ln(min_p)
     float low = -INFINITY;  // (and not equal to it)
     if (min_p >= 1.f) low = top;
-    else if (min_p > 0.f) low = __double2float_ru((double)top + (double)t * log((double)min_p));
+    else if (min_p > 0.f) low = __double2float_ru((double)top + sh.min_drop);
     auto in_min = [&](float l) { return l >= low && l > -INFINITY; };
 
     // what is kept: values above the border, and its equals up to index `last`
@@ -376,9 +393,9 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
                 total_mass += x[r][1] + x[r][3];
             }
         }
-        // the first bin with `count` elements, or `mass` of weight, up to its end; every CTA learns it
-        auto find = [&](bool counts, u64 count, double mass) {
-            auto enough = [&](u64 c, u64 m) { return counts ? c >= count : (double)m >= mass; };
+        // the first bin with `least` elements (or weight) up to its end; every CTA learns it
+        auto find = [&](bool counts, u64 least) {
+            auto enough = [&](u64 c, u64 m) { return (counts ? c : m) >= least; };
             if (threadIdx.x == 0) sh.found.bin = -1;
             __syncthreads();
             u64 c = before_count + count_to - bins_count, m = before_mass + mass_to - bins_mass;
@@ -474,8 +491,8 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
 
         const bool cut_k = by_k && total_count > (u64)top_k;
         Found f{-1, 0, 0, 0};
-        if (cut_k) f = find(true, (u64)top_k, 0);
-        else if (by_p) f = find(false, 0, (double)top_p * (double)total_mass);
+        if (cut_k) f = find(true, (u64)top_k);
+        else if (by_p) f = find(false, share_up(top_p, total_mass));
         if (f.bin >= 0 && (u64)f.count + f.in <= LIST) {
             // ---- a list of everything down to the border's bin: the first CTA does the rest ----
             gather(0, f.bin, sh.list, sh.listed[0], LIST);
@@ -487,9 +504,9 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
             bool is[EACH];
             if (by_p) {
                 const u64 sum = list_sums(sh.list, keep, by_key, sums);
-                const double want = (double)top_p * (double)(cut_k ? sum : total_mass);
+                const u64 want = share_up(top_p, cut_k ? sum : total_mass);
 #pragma unroll
-                for (int j = 0; j < EACH; ++j) is[j] = (int)threadIdx.x * EACH + j < keep && (double)sums[j] >= want;
+                for (int j = 0; j < EACH; ++j) is[j] = (int)threadIdx.x * EACH + j < keep && sums[j] >= want;
                 keep = first_where(keep - 1, is) + 1;
             }
             // the kept ones by index
@@ -499,16 +516,13 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
             sort(sh.list, size);
             auto by_index = [](u64 v) { return value_of(~(uint32_t)v); };
             const u64 sum = list_sums(sh.list, keep, by_index, sums);
-            const double want = (double)u * (double)sum;
+            const u64 want = share(u, sum);
 #pragma unroll
-            for (int j = 0; j < EACH; ++j) is[j] = (int)threadIdx.x * EACH + j < keep && (double)sums[j] > want;
+            for (int j = 0; j < EACH; ++j) is[j] = (int)threadIdx.x * EACH + j < keep && sums[j] > want;
             const int at = first_where(keep - 1, is);
             if (threadIdx.x == 0) {
-                const u64 v = sh.list[at];
-                const float l = by_index(v);
-                a.tokens[row] = (int)(v >> 32);
-                if (a.logprobs)
-                    a.logprobs[row] = (float)(((double)l - (double)top) / (double)t - log((double)sum * (1.0 / (1ull << SCALE))));
+                const float l = by_index(sh.list[at]);
+                answer((int)(sh.list[at] >> 32), l, sc.weight(sh.table, l), sum);
             }
             return;
         }
@@ -516,8 +530,9 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
         u64 equals = ~0ull;       // of the border's own equals: this many
         u64 ties = 0;             // there are so many of them
         u64 kept_mass = total_mass;
-        // border, equals, ties from the bin where it falls: `counts` elements from the row's first, or `mass` of weight
-        auto refine = [&](const Found &g, bool counts, u64 count, double mass, uint32_t &listed) -> u64 {
+        // border, equals, ties from the bin where it falls: `least` elements from the row's first (or weight); returns the weight
+        // of all that is kept
+        auto refine = [&](const Found &g, bool counts, u64 least, uint32_t &listed) -> u64 {
             if (g.in <= INNER) {
                 gather(g.bin, g.bin, sh.inner, listed, INNER);
                 u64 got[4] = {};
@@ -529,11 +544,11 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
                     if (by_p) list_sums(sh.inner, m, by_key, sums);
                     else
                         for (int j = 0; j < EACH; ++j) sums[j] = 0;
-                    int at = (int)(count - g.count) - 1;
+                    int at = (int)(least - g.count) - 1;
                     if (!counts) {
 #pragma unroll
                         for (int j = 0; j < EACH; ++j)
-                            is[j] = (int)threadIdx.x * EACH + j < m && (double)(g.mass + sums[j]) >= mass;
+                            is[j] = (int)threadIdx.x * EACH + j < m && g.mass + sums[j] >= least;
                         at = first_where(m - 1, is);
                     }
                     const uint32_t k = ~(uint32_t)(sh.inner[at] >> 32);
@@ -581,7 +596,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
             while (lo < hi) {  // the largest key that gives enough
                 const uint32_t mid = lo + (hi - lo + 1) / 2;
                 since(mid, c, m);
-                if (counts ? c >= count : (double)m >= mass) lo = mid;
+                if ((counts ? c : m) >= least) lo = mid;
                 else hi = mid - 1;
             }
             border = lo;
@@ -590,22 +605,18 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
             since(lo + 1, c, m);  // (an infinity's key is above every other's)
             ties = c1 - c;
             const u64 w = ties ? (m1 - m) / ties : 0;
-            if (counts) equals = count - c;
-            else {
-                const double need = w ? ceil((mass - (double)m) / (double)w) : 1.0;
-                equals = need < 1.0 ? 1 : need < (double)ties ? (u64)need : ties;
-            }
+            equals = counts ? least - c : w && least > m ? (least - m + w - 1) / w : 1;
             equals = min(equals, ties);
             return m + equals * w;
         };
-        if (cut_k) kept_mass = refine(f, true, (u64)top_k, 0, sh.listed[1]);
+        if (cut_k) kept_mass = refine(f, true, (u64)top_k, sh.listed[1]);
         if (by_p) {
-            const double want = (double)top_p * (double)kept_mass;
+            const u64 want = share_up(top_p, kept_mass);
             const uint32_t k_border = border;
             const u64 k_equals = equals, k_ties = ties;
-            const Found g = cut_k ? find(false, 0, want) : f;
+            const Found g = cut_k ? find(false, want) : f;
             if (g.bin >= 0 && !(cut_k && g.bin > f.bin)) {
-                refine(g, false, 0, want, sh.listed[2]);
+                refine(g, false, want, sh.listed[2]);
                 if (cut_k && border < k_border) border = k_border, equals = k_equals, ties = k_ties;
                 else if (cut_k && border == k_border) equals = min(equals, k_equals);
             }
@@ -642,6 +653,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
         return k > border || (k == border && c0 + i <= last);
     };
     u64 mine = 0, all;
+#pragma unroll 4
     for (int i = from; i < to; ++i)
         if (kept(i)) mine += sc.weight(sh.table, data[i]);
     const u64 upto = block_scan(sh, mine, all);
@@ -653,16 +665,24 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
             sum += x[r][0];
         }
     }
-    const double want = (double)u * (double)sum;
-    u64 c = before + upto - mine;
-    if (!((double)c > want) && (double)(c + mine) > want)
-        for (int i = from; i < to; ++i) {
-            if (kept(i)) c += sc.weight(sh.table, data[i]);
-            if ((double)c > want) {
-                answer(c0 + i, (double)sum);
-                break;
-            }
+    const u64 want = share(u, sum), c = before + upto;
+    const uint32_t here = __ballot_sync(0xffffffffu, c - mine <= want && c > want);  // one thread of all
+    if (!here) return;
+    // its warp walks the stretch
+    const int who = __ffs(here) - 1;
+    u64 at = __shfl_sync(0xffffffffu, c - mine, who);
+    const int first = __shfl_sync(0xffffffffu, from, who), end = __shfl_sync(0xffffffffu, to, who);
+    for (int i0 = first; i0 < end; i0 += 32) {
+        const int i = i0 + lane;
+        const u64 w = i < end && kept(i) ? sc.weight(sh.table, data[i]) : 0;
+        const u64 to_here = at + warp_scan(w, lane);
+        const uint32_t past = __ballot_sync(0xffffffffu, to_here > want);
+        if (past) {
+            if (lane == __ffs(past) - 1) answer(c0 + i, data[i], w, sum);
+            return;
         }
+        at = __shfl_sync(0xffffffffu, to_here, 31);
+    }
 }
 
 template <bool FP32>
