@@ -71,6 +71,7 @@ struct Found {         // where a border falls
 
 struct Shared {
     u64 part[WARPS];                  // of block scans
+    uint32_t count_part[WARPS];
     u64 swap[4][MAX_PARTS][4];        // of the cluster's exchanges, four in turn
     int32_t table[OCTAVE + 1];        // TABLE
     uint32_t listed[3];               // entries of the list, of the inner one, of that once more
@@ -107,9 +108,9 @@ struct Scale {
     }
     __device__ __forceinline__ u64 weight(const int32_t *table, float l) const {
         const float p = place(l);
-        if (!(p < (float)LAST_MASS)) return 0;
-        const int n = (int)p;
-        return shifted(mantissa(table, l, p, n), n);
+        const int n = bin(p);
+        const u64 w = shifted(mantissa(table, l, p, n), n < LAST_MASS ? n : 0);
+        return n < LAST_MASS ? w : 0;
     }
 };
 
@@ -132,23 +133,44 @@ __device__ __forceinline__ T warp_scan(T v, int lane) {  // inclusive
     return v;
 }
 
-// inclusive scan over the CTA, and the total
-__device__ __forceinline__ u64 block_scan(Shared &sh, u64 v, u64 &total) {
+// inclusive scans over the CTA of two values, and their totals
+__device__ __forceinline__ void block_scan(Shared &sh, uint32_t &c, u64 &m, uint32_t &c_all, u64 &m_all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    c = warp_scan(c, lane);
+    m = warp_scan(m, lane);
+    __syncthreads();
+    if (lane == 31) sh.count_part[warp] = c, sh.part[warp] = m;
+    __syncthreads();
+    uint32_t c0 = 0;
+    u64 m0 = 0;
+    c_all = 0, m_all = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        if (w == warp) c0 = c_all, m0 = m_all;
+        c_all += sh.count_part[w], m_all += sh.part[w];
+    }
+    c += c0, m += m0;
+}
+template <class T>
+__device__ __forceinline__ T block_scan(Shared &sh, T v, T &all) {  // one value, 32 or 64 bits
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     v = warp_scan(v, lane);
     __syncthreads();
     if (lane == 31) sh.part[warp] = v;
     __syncthreads();
-    const u64 p = lane < WARPS ? sh.part[lane] : 0;
-    const u64 s = warp_scan(p, lane);
-    total = __shfl_sync(0xffffffffu, s, WARPS - 1);
-    const u64 before = __shfl_sync(0xffffffffu, s - p, warp);
+    T before = 0;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        if (w == warp) before = all;
+        all += (T)sh.part[w];
+    }
     return v + before;
 }
 __device__ __forceinline__ u64 block_sum(Shared &sh, u64 v) {
-    u64 total;
-    block_scan(sh, v, total);
-    return total;
+    u64 all;
+    block_scan(sh, v, all);
+    return all;
 }
 
 // ascending sort of n values (a power of two) by the whole CTA
@@ -297,8 +319,16 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
         return;
     }
 
-    // a thread's stretch of the row; an odd length keeps the threads of a warp in different banks
+    // a thread's stretch of the row, four logits at a time (behind its end: -infinity); an odd length keeps the threads of a warp in different banks
     const int len = ((chunk + THREADS - 1) / THREADS) | 1, from = min(n, (int)threadIdx.x * len), to = min(n, from + len);
+    auto each4 = [&](auto f) {
+        for (int i = from; i < to; i += 4) {
+            float l[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) l[j] = i + j < to ? data[i + j] : -INFINITY;
+            f(i, l);
+        }
+    };
     if (t == 0.f) {  // the first of the largest
         int at = INT32_MAX;
         for (int i = from; i < to && at == INT32_MAX; ++i)
@@ -338,36 +368,53 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
         const float prune = by_k || top_p <= 0.f ? INFINITY : ceilf((float)OCTAVE * log2f((float)a.V / (1.f - top_p)) + 1.f);
         uint32_t far_count = 0;
         u64 far_mass = 0;
-        for (int i = from; i < to; ++i) {
-            const float l = data[i];
-            if (!in_min(l)) continue;
-            const float p = sc.place(l);
-            const int b = Scale::bin(p);
-            if (by_p && b < LAST_MASS) {
-                const uint32_t w = sc.mantissa(sh.table, l, p, b);
-                if (!(p < prune)) {
-                    ++far_count;
-                    far_mass += Scale::shifted(w, b);
-                    continue;
+        if (by_p)
+            each4([&](int, const float(&l)[4]) {
+                int b[4];
+                uint32_t w[4];
+                bool near[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float p = sc.place(l[j]);
+                    b[j] = Scale::bin(p);
+                    near[j] = p < prune;
+                    w[j] = b[j] < LAST_MASS ? sc.mantissa(sh.table, l[j], p, b[j]) : 0;
                 }
-                // what is above the bin's lower end, less a little for roundings: 25 bits
-                const uint32_t over = w - (uint32_t)(sh.table[b % OCTAVE + 1] - SLACK);
-                atomicAdd(&sh.lo[b], over & 4095u);
-                atomicAdd(&sh.hi[b], over >> 12);
-            } else if (!(p < prune)) {
-                ++far_count;
-                continue;
-            }
-            atomicAdd(&sh.count[b], 1u);
-        }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (!in_min(l[j])) continue;
+                    if (!near[j]) {
+                        ++far_count;
+                        far_mass += Scale::shifted(w[j], min(b[j], LAST_MASS - 1));
+                        continue;
+                    }
+                    atomicAdd(&sh.count[b[j]], 1u);
+                    if (b[j] >= LAST_MASS) continue;
+                    // what is above the bin's lower end, less a little for roundings: 25 bits
+                    const uint32_t over = w[j] - (uint32_t)(sh.table[b[j] % OCTAVE + 1] - SLACK);
+                    atomicAdd(&sh.lo[b[j]], over & 4095u);
+                    atomicAdd(&sh.hi[b[j]], over >> 12);
+                }
+            });
+        else
+            each4([&](int, const float(&l)[4]) {
+                int b[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) b[j] = Scale::bin(sc.place(l[j]));
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (in_min(l[j])) atomicAdd(&sh.count[b[j]], 1u);
+            });
         __syncwarp();
         cluster_sync();
         // ---- a slice of the bins from every CTA, merged in place ----
         const int per = BINS >> parts_log, own = rank * per, width = max(1, per / THREADS);  // neighbouring bins of a thread
-        u64 bins_count = 0, bins_mass = 0;
+        uint32_t bins_count = 0;
+        u64 bins_mass = 0;
         if ((int)threadIdx.x * width < per)
             for (int b = own + threadIdx.x * width, e = b + width; b < e; ++b) {
-                u64 c = 0, s = 0;
+                uint32_t c = 0;
+                u64 s = 0;
 #pragma unroll 4
                 for (int r = 0; r < parts; ++r) {
                     c += ld_remote(map_rank(smem_u32(&sh.count[b]), r));
@@ -375,18 +422,19 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
                         s += ld_remote(map_rank(smem_u32(&sh.lo[b]), r)) + ((u64)ld_remote(map_rank(smem_u32(&sh.hi[b]), r)) << 12);
                 }
                 const u64 w = by_p && b < LAST_MASS ? Scale::shifted(s + c * (u64)(sh.table[b % OCTAVE + 1] - SLACK), b) : 0;
-                sh.count[b] = (uint32_t)c;
+                sh.count[b] = c;
                 sh.lo[b] = (uint32_t)w;
                 sh.hi[b] = (uint32_t)(w >> 32);
                 bins_count += c;
                 bins_mass += w;
             }
-        u64 slice_count, slice_mass;
-        const u64 count_to = block_scan(sh, bins_count, slice_count), mass_to = block_scan(sh, bins_mass, slice_mass);
-        const u64 far_all = block_sum(sh, far_mass), far_n = block_sum(sh, far_count);
+        uint32_t slice_count, far_all_count = 0, count_to = bins_count;
+        u64 slice_mass, far_all_mass = 0, mass_to = bins_mass;
+        block_scan(sh, count_to, mass_to, slice_count, slice_mass);
+        if (by_p) block_scan(sh, far_count, far_mass, far_all_count, far_all_mass);
         u64 total_count = 0, total_mass = 0, before_count = 0, before_mass = 0;
         {
-            u64(*x)[4] = exchange(slice_count, slice_mass, far_n, far_all);
+            u64(*x)[4] = exchange(slice_count, slice_mass, far_all_count, far_all_mass);
             for (int r = 0; r < parts; ++r) {
                 if (r < rank) before_count += x[r][0], before_mass += x[r][1];
                 total_count += x[r][0] + x[r][2];
@@ -425,28 +473,37 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
                 const int b = Scale::bin(sc.place(l));
                 return b >= b0 && b <= b1;
             };
-            uint32_t mine = 0;
-            for (int i = from; i < to; ++i) mine += in(data[i]);
-            u64 all;
-            const u64 upto = block_scan(sh, mine, all);
+            // a thread's own, as bits of the fours of its stretch
+            uint32_t mine = 0, fours = 0;
+            each4([&](int i, const float(&l)[4]) {
+                uint32_t any = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) any += in(l[j]);
+                mine += any;
+                if (any) fours |= 1u << ((i - from) >> 2);
+            });
+            uint32_t all;
+            const uint32_t upto = block_scan(sh, mine, all);
             __syncthreads();
             if (threadIdx.x == 0) {
                 uint32_t at;
                 asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;"
                              : "=r"(at)
-                             : "r"(map_rank(smem_u32(&listed), 0)), "r"((uint32_t)all)
+                             : "r"(map_rank(smem_u32(&listed), 0)), "r"(all)
                              : "memory");
                 sh.part[0] = at;
             }
             __syncthreads();
-            uint32_t at = (uint32_t)sh.part[0] + (uint32_t)upto - mine;
+            uint32_t at = (uint32_t)sh.part[0] + upto - mine;
             const uint32_t to_list = map_rank(smem_u32(list), 0);
-            if (mine)
-                for (int i = from; i < to; ++i)
+            for (; fours; fours &= fours - 1) {
+                const int i0 = from + 4 * (__ffs(fours) - 1);
+                for (int i = i0; i < min(i0 + 4, to); ++i)
                     if (in(data[i])) {
                         if (at < room) st_remote(to_list + 8 * at, (u64)~key_of(data[i]) << 32 | (uint32_t)(c0 + i));
                         ++at;
                     }
+            }
             __syncwarp();
             cluster_sync();
         };
@@ -572,11 +629,15 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
             auto inside = [&](float l) { return in_min(l) && Scale::bin(sc.place(l)) == g.bin; };
             // count and sum of the bin's elements from key k on
             auto since = [&](uint32_t k, u64 &c, u64 &m) {
-                u64 c0_ = 0, m0 = 0;
-                for (int i = from; i < to; ++i)
-                    if (inside(data[i]) && key_of(data[i]) >= k) ++c0_, m0 += sc.weight(sh.table, data[i]);
-                c0_ = block_sum(sh, c0_), m0 = block_sum(sh, m0);
-                u64(*x)[4] = exchange(c0_, m0, 0, 0);
+                uint32_t nc = 0, nc_all;
+                u64 nm = 0, nm_all;
+                each4([&](int, const float(&l)[4]) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (inside(l[j]) && key_of(l[j]) >= k) ++nc, nm += sc.weight(sh.table, l[j]);
+                });
+                block_scan(sh, nc, nm, nc_all, nm_all);
+                u64(*x)[4] = exchange(nc_all, nm_all, 0, 0);
                 c = g.count, m = g.mass;
                 for (int r = 0; r < parts; ++r) c += x[r][0], m += x[r][1];
             };
@@ -648,14 +709,19 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
     }
 
     // ---- the kept weights' sums in index order, and where u falls ----
-    auto kept = [&](int i) {
-        const uint32_t k = key_of(data[i]);
+    auto kept = [&](float l, int i) {
+        const uint32_t k = key_of(l);
         return k > border || (k == border && c0 + i <= last);
     };
     u64 mine = 0, all;
-#pragma unroll 4
-    for (int i = from; i < to; ++i)
-        if (kept(i)) mine += sc.weight(sh.table, data[i]);
+    each4([&](int i, const float(&l)[4]) {
+        u64 w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = sc.weight(sh.table, l[j]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (kept(l[j], i + j)) mine += w[j];
+    });
     const u64 upto = block_scan(sh, mine, all);
     u64 before = 0, sum = 0;
     {
@@ -674,7 +740,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
     const int first = __shfl_sync(0xffffffffu, from, who), end = __shfl_sync(0xffffffffu, to, who);
     for (int i0 = first; i0 < end; i0 += 32) {
         const int i = i0 + lane;
-        const u64 w = i < end && kept(i) ? sc.weight(sh.table, data[i]) : 0;
+        const u64 w = i < end && kept(data[i], i) ? sc.weight(sh.table, data[i]) : 0;
         const u64 to_here = at + warp_scan(w, lane);
         const uint32_t past = __ballot_sync(0xffffffffu, to_here > want);
         if (past) {
