@@ -13,10 +13,10 @@
 //                                  gives the border's value and how many of its equals are kept, and the row is walked as above.
 //   more than that in one bin      (thousands of equal logits, or nearly) bisection on the values' bits.
 //
-// Weights: with P = 32 log2(e) (max - l) / t, its whole part n and rest f, w = 2^(-n / 32) 2^(-f / 32): the first factor from a
-// table of 32 and a shift, the second from five terms of its series. P is held in two floats: 2^-29 of a weight, against which
-// a sum of thousands of them is more exact still. u of 24 bits falls so near a border of two tokens that it matters about once
-// in a million rows of 10^5 nearly equal tokens.
+// Weights: with P = 32 log2(e) (max - l) / t, n a whole number near it and below, f the rest, w = 2^(-n / 32) 2^(-f / 32): the
+// first factor from a table of all n, the second from five terms of its series. P is held in two floats: w is within 2^-29 of
+// itself (and 2^-44 of the largest), sums of thousands of them within far less. u of 24 bits falls so near a border of two tokens
+// that it matters about once in a million rows of 10^5 nearly equal tokens.
 #include <math.h>
 
 #include <atomic>
@@ -40,20 +40,23 @@ struct Args {
 };
 
 constexpr int THREADS = 512, WARPS = THREADS / 32;
-constexpr int BINS = 2048, OCTAVE = 32;      // bins in all, and for a factor of two
-constexpr int LAST_MASS = 44 * OCTAVE;       // bins from here on weigh less than 2^-44 each: nothing
-constexpr int LIST = 2048, INNER = 1024;     // candidates that one CTA sorts: all of a row's, or a bin's
+constexpr int OCTAVE = 32;                   // bins for a factor of two
+constexpr int FAR = 44 * OCTAVE + 1;         // what falls into this bin weighs less than 2^-44: nothing
+constexpr int BINS = 1536;                   // FAR and a little, in slices of whole warps
+constexpr int LIST = 2048, INNER = 512;       // candidates that one CTA sorts: all of a row's, or a bin's beside the histogram
+constexpr int RANKED = 256;                  // up to so many it ranks by comparing each with each
 constexpr int MAX_PARTS = 8;
 constexpr int SCALE = 43;                    // the largest logit's weight: 2^43; 2^18.6 of them fit 63 bits
 constexpr int CHUNK_MAX = 49152;             // logits of a CTA; sums of a bin's 13-bit parts stay below 2^32
 static_assert((int64_t)CHUNK_MAX << 13 < (int64_t)1 << 32, "");
 
-// 2^30 2^(-i / 32)
-__constant__ int32_t TABLE[OCTAVE + 1] = {
-    1073741824, 1050733751, 1028218693, 1006186087, 984625594, 963527098, 942880699, 922676710, 902905651, 883558244, 864625413,
-    846098274, 827968132, 810226483, 792865000, 775875538, 759250125, 742980960, 727060411, 711481005, 696235434, 681316545,
-    666717336, 652430958, 638450708, 624770026, 611382493, 598281827, 585461881, 572916640, 560640218, 548626854, 536870912};
-constexpr int SLACK = 8192;                  // a mantissa is at most this much under its bin's end (roundings of P)
+// 2^SCALE 2^(-i / 32)
+__constant__ u64 TABLE[OCTAVE] = {
+    8796093022208ull, 8607610887057ull, 8423167535396ull, 8242676424423ull, 8066052865769ull, 7893213985764ull, 7724078686549ull, 7558567608024ull,
+    7396603090613ull, 7238109138825ull, 7083011385596ull, 6931237057393ull, 6782714940072ull, 6637375345460ull, 6495150078656ull, 6355972406040ull,
+    6219777023951ull, 6086500028053ull, 5956078883349ull, 5828452394836ull, 5703560678795ull, 5581345134690ull, 5461748417677ull, 5344714411690ull,
+    5230188203118ull, 5118116055032ull, 5008445381977ull, 4901124725294ull, 4796103728980ull, 4693333116055ull, 4592764665442ull, 4494351189345ull};
+constexpr int SLACK = 65536;                 // of 2^30: a weight is less than that under its bin's lower end (0.001 of P, and roundings)
 
 // Whole numbers that order as the values do (-0 as +0); -infinity gives KEY_NEG_INF, NaN below it or above +infinity's.
 __device__ __forceinline__ uint32_t key_of(float l) {
@@ -73,7 +76,7 @@ struct Shared {
     u64 part[WARPS];                  // of block scans
     uint32_t count_part[WARPS];
     u64 swap[4][MAX_PARTS][4];        // of the cluster's exchanges, four in turn
-    int32_t table[OCTAVE + 1];        // TABLE
+    u64 weight[FAR + 1];              // of the upper ends of the bins: bin b holds P from b - 1 on
     uint32_t listed[3];               // entries of the list, of the inner one, of that once more
     double min_drop;                  // t ln(min_p)
     Found found;
@@ -87,31 +90,81 @@ struct Shared {
     };
 };
 
+// two fp32 operations in one instruction
+__device__ __forceinline__ u64 pair(float x, float y) {
+    u64 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ u64 pair(float x) { return pair(x, x); }
+__device__ __forceinline__ float2 unpair(u64 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+    u64 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+    u64 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+    u64 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // What a row's weights go by.
+constexpr float MAGIC = 12582912.f;  // 1.5 * 2^23: a number added to it is rounded to a whole one
 struct Scale {
     float half_max, c_hi, c_lo;  // max / 2, and 64 log2(e) / t in two parts (values enter halved: their difference does not overflow)
-    __device__ __forceinline__ float place(float l) const { return (half_max - 0.5f * l) * c_hi; }  // P, of 24 bits: rises as l falls
-    __device__ __forceinline__ static int bin(float p) { return p < (float)(BINS - 1) ? (int)p : BINS - 1; }
-    // w / 2^(n / 32 rounded down) times 2^30 of a logit at p < LAST_MASS in bin n
-    __device__ __forceinline__ uint32_t mantissa(const int32_t *table, float l, float p, int n) const {
-        const float a = 0.5f * l, s = half_max - a;  // and what rounding took: s + e = half_max - a
-        const float b = s - half_max, e = (half_max - (s - b)) - (a + b);
-        const float f = (p - (float)n) + (fmaf(s, c_hi, -p) + fmaf(s, c_lo, e * c_hi));
-        const float r = f * 0.0216608493924982909f;  // ln(2) / 32
-        const float q = r * fmaf(r, fmaf(r, fmaf(r, fmaf(r, 1.f / 120, -1.f / 24), 1.f / 6), -0.5f), 1.f);  // 1 - exp(-r)
-        const int t = table[n % OCTAVE];
-        return (uint32_t)(t - (int)(((int64_t)t * __float2int_rn(q * 2147483648.f)) >> 31));
+    // MAGIC + the whole part of P of a logit, less what keeps the rest positive: rises as l falls
+    __device__ __forceinline__ float spot(float l) const {
+        return (fminf((half_max - 0.5f * l) * c_hi, (float)FAR) - 0.501f) + MAGIC;
     }
-    __device__ __forceinline__ static u64 shifted(u64 mantissas, int n) {  // sums of mantissas of a bin, as weights
-        const int by = n / OCTAVE;
-        return ((mantissas << (SCALE - 30)) + ((1ull << by) >> 1)) >> by;
+    __device__ __forceinline__ static int bin(float spot) { return __float_as_int(spot) - (0x4B400000 - 1); }
+    __device__ __forceinline__ static float spot_of(int bin) { return MAGIC + (float)(bin - 1); }
+    // the bins and weights of four logits
+    __device__ __forceinline__ void weigh(const u64 *weight, const float (&l)[4], int (&b)[4], u64 (&w)[4]) const {
+#pragma unroll
+        for (int h = 0; h < 4; h += 2) {
+            const u64 x = pair(l[h], l[h + 1]), hm = pair(half_max), c = pair(c_hi), minus = pair(-1.f);
+            const u64 a = mul2(x, pair(0.5f)), s = fma2(x, pair(-0.5f), hm);  // s + e = half_max - a: what rounding took
+            const u64 v = add2(s, pair(-half_max)), e = fma2(add2(a, v), minus, fma2(fma2(v, minus, s), minus, hm));
+            const u64 np = mul2(s, pair(-c_hi));  // -P, and what P lacks
+            const u64 lack = fma2(e, c, fma2(s, pair(c_lo), fma2(s, c, np)));
+            const float2 q = unpair(np);
+            const u64 at = add2(add2(pair(fminf(-q.x, (float)FAR), fminf(-q.y, (float)FAR)), pair(-0.501f)), pair(MAGIC));
+            const float2 spots = unpair(at);
+            b[h] = bin(spots.x), b[h + 1] = bin(spots.y);
+            const u64 f = fma2(add2(np, add2(at, pair(-MAGIC))), minus, lack);
+            const u64 r = mul2(f, pair(0.0216608493924982909f));  // ln(2) / 32
+            u64 y = fma2(r, pair(1.f / 120), pair(-1.f / 24));
+            y = fma2(r, y, pair(1.f / 6));
+            y = fma2(r, y, pair(-0.5f));
+            y = fma2(r, y, pair(1.f));
+            const float2 z = unpair(mul2(mul2(r, y), pair(4294967296.f)));  // (1 - exp(-r)) 2^32
+            w[h] = less(weight[b[h]], __float2uint_rn(z.x));
+            w[h + 1] = less(weight[b[h + 1]], __float2uint_rn(z.y));
+        }
     }
-    __device__ __forceinline__ u64 weight(const int32_t *table, float l) const {
-        const float p = place(l);
-        const int n = bin(p);
-        const u64 w = shifted(mantissa(table, l, p, n), n < LAST_MASS ? n : 0);
-        return n < LAST_MASS ? w : 0;
+    __device__ __forceinline__ static u64 less(u64 w, uint32_t part) {  // w (1 - part / 2^32)
+        return w - ((w >> 32) * part + __umulhi((uint32_t)w, part));
     }
+    __device__ __forceinline__ u64 weight_of(const u64 *weight, float l) const {
+        const float x[4] = {l, l, l, l};
+        int b[4];
+        u64 w[4];
+        weigh(weight, x, b, w);
+        return w[0];
+    }
+    // bins sum weights as what they have over the bin's lower end, in 30 bits of a weight's own
+    __device__ __forceinline__ static int drop(int b) { return max(SCALE - 30 - max(b - 1, 0) / OCTAVE, 0); }
+    __device__ __forceinline__ static int base(const u64 *weight, int b) { return (int)(weight[b + 1] >> drop(b)) - SLACK; }
 };
 
 // the part p in [0, 1) of a sum, rounded down, and up (p as 64 bits after the point: exact from 2^-40 on)
@@ -200,8 +253,10 @@ template <bool FP32>
 __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int parts_log, int chunk) {
     extern __shared__ __align__(128) uint8_t smem[];
     Shared &sh = *reinterpret_cast<Shared *>(smem);
-    float *data = reinterpret_cast<float *>(smem + (sizeof(Shared) + 127) / 128 * 128);
-    const int lane = threadIdx.x & 31, parts = 1 << parts_log;
+    // the CTA's logits from line[shift] on, in fours; -infinity before and behind them
+    float *line = reinterpret_cast<float *>(smem + (sizeof(Shared) + 127) / 128 * 128);
+    int shift;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, parts = 1 << parts_log;
     const int rank = (int)cluster_rank();
     const int64_t row = blockIdx.x >> parts_log;
     const int c0 = rank * chunk, n = max(0, min(chunk, a.V - c0));
@@ -221,7 +276,11 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
     };
 
     for (int i = threadIdx.x; i < BINS; i += THREADS) sh.count[i] = sh.lo[i] = sh.hi[i] = 0;
-    if (threadIdx.x <= OCTAVE) sh.table[threadIdx.x] = TABLE[threadIdx.x];
+    for (int b = threadIdx.x; b <= FAR; b += THREADS) {
+        const int n = max(b - 1, 0), by = n / OCTAVE;  // (bin 0, a hair above the largest: P - 1)
+        const u64 w = (TABLE[n % OCTAVE] + ((1ull << by) >> 1)) >> by;
+        sh.weight[b] = b == 0 ? 2 * TABLE[OCTAVE - 1] : b == FAR ? 0 : w;
+    }
     if (threadIdx.x < 3) sh.listed[threadIdx.x] = 0;
     __syncthreads();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // waited for before the first exchange
@@ -244,7 +303,8 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
         constexpr int VEC = FP32 ? 4 : 8, SIZE = FP32 ? 4 : 2;
         const uint8_t *src = static_cast<const uint8_t *>(a.logits) + (row * a.stride + c0) * SIZE;
         const int head = min(n, (int)((16 - (reinterpret_cast<uintptr_t>(src) & 15)) & 15) / SIZE);  // up to 16-byte pieces
-        data += (VEC - head) & (VEC - 1);  // pieces are aligned here too
+        shift = (VEC - head) & (VEC - 1);  // pieces are aligned here too
+        float *data = line + shift;
         auto one = [&](int i) {
             const float l = FP32 ? reinterpret_cast<const float *>(src)[i] : bf16_to_f32(reinterpret_cast<const uint16_t *>(src)[i]);
             data[i] = l;
@@ -283,6 +343,8 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
         if ((int)threadIdx.x < head) one(threadIdx.x);
         const int tail = head + vecs * VEC + (int)threadIdx.x;
         if (tail < n) one(tail);
+        if ((int)threadIdx.x < shift) line[threadIdx.x] = -INFINITY;
+        if (threadIdx.x < 4) data[n + threadIdx.x] = -INFINITY;
     }
     __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // the other CTAs have begun
@@ -319,23 +381,31 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
         return;
     }
 
-    // a thread's stretch of the row, four logits at a time (behind its end: -infinity); an odd length keeps the threads of a warp in different banks
-    const int len = ((chunk + THREADS - 1) / THREADS) | 1, from = min(n, (int)threadIdx.x * len), to = min(n, from + len);
-    auto each4 = [&](auto f) {
-        for (int i = from; i < to; i += 4) {
+    // a warp's stretch of the row: fours [four0, four1), a lane each 32nd
+    const int fours = (shift + n + 3) / 4, per_warp = (fours + THREADS - 1) / THREADS * 32;
+    const int four0 = min(fours, warp * per_warp), four1 = min(fours, four0 + per_warp);
+    auto four = [&](int g, float(&l)[4]) {
+        const float4 v = reinterpret_cast<const float4 *>(line)[g];
+        l[0] = v.x, l[1] = v.y, l[2] = v.z, l[3] = v.w;
+    };
+    auto each4 = [&](auto f) {  // f(four, logits)
+        for (int g = four0 + lane; g < four1; g += 32) {
             float l[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) l[j] = i + j < to ? data[i + j] : -INFINITY;
-            f(i, l);
+            four(g, l);
+            f(g, l);
         }
     };
+    auto index = [&](int g, int j) { return c0 - shift + 4 * g + j; };
     if (t == 0.f) {  // the first of the largest
         int at = INT32_MAX;
-        for (int i = from; i < to && at == INT32_MAX; ++i)
-            if (data[i] == top) at = c0 + i;
+        each4([&](int g, const float(&l)[4]) {
+#pragma unroll
+            for (int j = 3; j >= 0; --j)
+                if (l[j] == top) at = min(at, index(g, j));
+        });
         at = __reduce_min_sync(0xffffffffu, at);
         __syncthreads();
-        if (lane == 0) sh.part[threadIdx.x >> 5] = (u64)at;
+        if (lane == 0) sh.part[warp] = (u64)at;
         __syncthreads();
         for (int w = 0; w < WARPS; ++w) at = min(at, (int)sh.part[w]);
         u64(*x)[4] = exchange((u64)at, 0, 0, 0);
@@ -363,35 +433,26 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
     int last = INT32_MAX;
     const bool by_k = top_k > 0 && top_k < a.V, by_p = top_p < 1.f;
     if (by_k || by_p) {
-        // ---- the histogram. Below `prune` all of a row's V logits together are less than 1 - top_p of the largest's weight alone:
-        // they hold no border, and go into two sums instead ----
-        const float prune = by_k || top_p <= 0.f ? INFINITY : ceilf((float)OCTAVE * log2f((float)a.V / (1.f - top_p)) + 1.f);
+        // ---- the histogram. What weighs nothing is only counted. Without top_k so is, with its weight, what all of a row's V logits
+        // together could not lift over 1 - top_p of the largest's weight alone: it holds no border ----
+        const int limit = by_k || top_p <= 0.f ? FAR : min(FAR, (int)((float)OCTAVE * log2f((float)a.V / (1.f - top_p))) + 3);
         uint32_t far_count = 0;
         u64 far_mass = 0;
         if (by_p)
             each4([&](int, const float(&l)[4]) {
                 int b[4];
-                uint32_t w[4];
-                bool near[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float p = sc.place(l[j]);
-                    b[j] = Scale::bin(p);
-                    near[j] = p < prune;
-                    w[j] = b[j] < LAST_MASS ? sc.mantissa(sh.table, l[j], p, b[j]) : 0;
-                }
+                u64 w[4];
+                sc.weigh(sh.weight, l, b, w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (!in_min(l[j])) continue;
-                    if (!near[j]) {
+                    if (b[j] >= limit) {
                         ++far_count;
-                        far_mass += Scale::shifted(w[j], min(b[j], LAST_MASS - 1));
+                        far_mass += w[j];
                         continue;
                     }
+                    const uint32_t over = (uint32_t)((int)(w[j] >> Scale::drop(b[j])) - Scale::base(sh.weight, b[j]));  // 25 bits
                     atomicAdd(&sh.count[b[j]], 1u);
-                    if (b[j] >= LAST_MASS) continue;
-                    // what is above the bin's lower end, less a little for roundings: 25 bits
-                    const uint32_t over = w[j] - (uint32_t)(sh.table[b[j] % OCTAVE + 1] - SLACK);
                     atomicAdd(&sh.lo[b[j]], over & 4095u);
                     atomicAdd(&sh.hi[b[j]], over >> 12);
                 }
@@ -400,38 +461,41 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
             each4([&](int, const float(&l)[4]) {
                 int b[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) b[j] = Scale::bin(sc.place(l[j]));
+                for (int j = 0; j < 4; ++j) b[j] = Scale::bin(sc.spot(l[j]));
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (in_min(l[j])) atomicAdd(&sh.count[b[j]], 1u);
+                    if (in_min(l[j])) {
+                        if (b[j] >= FAR) ++far_count;
+                        else atomicAdd(&sh.count[b[j]], 1u);
+                    }
             });
         __syncwarp();
         cluster_sync();
         // ---- a slice of the bins from every CTA, merged in place ----
-        const int per = BINS >> parts_log, own = rank * per, width = max(1, per / THREADS);  // neighbouring bins of a thread
+        const int per = BINS >> parts_log, own = rank * per, width = (per + THREADS - 1) / THREADS;  // neighbouring bins of a thread
+        const int bin0 = own + min((int)threadIdx.x * width, per), bin1 = min(bin0 + width, own + per);
         uint32_t bins_count = 0;
         u64 bins_mass = 0;
-        if ((int)threadIdx.x * width < per)
-            for (int b = own + threadIdx.x * width, e = b + width; b < e; ++b) {
-                uint32_t c = 0;
-                u64 s = 0;
+        for (int b = bin0; b < bin1; ++b) {
+            uint32_t c = 0;
+            u64 s = 0;
 #pragma unroll 4
-                for (int r = 0; r < parts; ++r) {
-                    c += ld_remote(map_rank(smem_u32(&sh.count[b]), r));
-                    if (by_p)
-                        s += ld_remote(map_rank(smem_u32(&sh.lo[b]), r)) + ((u64)ld_remote(map_rank(smem_u32(&sh.hi[b]), r)) << 12);
-                }
-                const u64 w = by_p && b < LAST_MASS ? Scale::shifted(s + c * (u64)(sh.table[b % OCTAVE + 1] - SLACK), b) : 0;
-                sh.count[b] = c;
-                sh.lo[b] = (uint32_t)w;
-                sh.hi[b] = (uint32_t)(w >> 32);
-                bins_count += c;
-                bins_mass += w;
+            for (int r = 0; r < parts; ++r) {
+                c += ld_remote(map_rank(smem_u32(&sh.count[b]), r));
+                if (by_p)
+                    s += ld_remote(map_rank(smem_u32(&sh.lo[b]), r)) + ((u64)ld_remote(map_rank(smem_u32(&sh.hi[b]), r)) << 12);
             }
+            const u64 w = c && by_p ? (s + (u64)((int64_t)c * Scale::base(sh.weight, b))) << Scale::drop(b) : 0;
+            sh.count[b] = c;
+            sh.lo[b] = (uint32_t)w;
+            sh.hi[b] = (uint32_t)(w >> 32);
+            bins_count += c;
+            bins_mass += w;
+        }
         uint32_t slice_count, far_all_count = 0, count_to = bins_count;
         u64 slice_mass, far_all_mass = 0, mass_to = bins_mass;
         block_scan(sh, count_to, mass_to, slice_count, slice_mass);
-        if (by_p) block_scan(sh, far_count, far_mass, far_all_count, far_all_mass);
+        block_scan(sh, far_count, far_mass, far_all_count, far_all_mass);
         u64 total_count = 0, total_mass = 0, before_count = 0, before_mass = 0;
         {
             u64(*x)[4] = exchange(slice_count, slice_mass, far_all_count, far_all_mass);
@@ -448,15 +512,14 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
             __syncthreads();
             u64 c = before_count + count_to - bins_count, m = before_mass + mass_to - bins_mass;
             const bool had = before_count + count_to - bins_count > 0 && enough(c, m);
-            if ((int)threadIdx.x * width < per && !had && enough(c + bins_count, m + bins_mass))
-                for (int b = own + threadIdx.x * width;; ++b) {
+            if (!had && enough(c + bins_count, m + bins_mass))
+                for (int b = bin0; b < bin1; ++b) {
                     const u64 c1 = c + sh.count[b], m1 = m + ((u64)sh.hi[b] << 32 | sh.lo[b]);
                     if (c1 > c && enough(c1, m1)) {
                         sh.found = {b, (uint32_t)c, (uint32_t)(c1 - c), m};
                         break;
                     }
                     c = c1, m = m1;
-                    if (b + 1 == own + (int)threadIdx.x * width + width) break;
                 }
             __syncthreads();
             const Found f = sh.found;
@@ -468,19 +531,19 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
         };
         // the elements in bins [b0, b1], in any order, to a list of the first CTA
         auto gather = [&](int b0, int b1, u64 *list, uint32_t &listed, uint32_t room) {
+            const float s0 = Scale::spot_of(b0), s1 = Scale::spot_of(b1);
             auto in = [&](float l) {
-                if (!in_min(l)) return false;
-                const int b = Scale::bin(sc.place(l));
-                return b >= b0 && b <= b1;
+                const float at = sc.spot(l);
+                return in_min(l) && at >= s0 && at <= s1;
             };
-            // a thread's own, as bits of the fours of its stretch
-            uint32_t mine = 0, fours = 0;
-            each4([&](int i, const float(&l)[4]) {
+            // a lane's own, as bits of its fours
+            uint32_t mine = 0, has = 0;
+            each4([&](int g, const float(&l)[4]) {
                 uint32_t any = 0;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) any += in(l[j]);
                 mine += any;
-                if (any) fours |= 1u << ((i - from) >> 2);
+                if (any) has |= 1u << ((g - four0) / 32);
             });
             uint32_t all;
             const uint32_t upto = block_scan(sh, mine, all);
@@ -496,11 +559,14 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
             __syncthreads();
             uint32_t at = (uint32_t)sh.part[0] + upto - mine;
             const uint32_t to_list = map_rank(smem_u32(list), 0);
-            for (; fours; fours &= fours - 1) {
-                const int i0 = from + 4 * (__ffs(fours) - 1);
-                for (int i = i0; i < min(i0 + 4, to); ++i)
-                    if (in(data[i])) {
-                        if (at < room) st_remote(to_list + 8 * at, (u64)~key_of(data[i]) << 32 | (uint32_t)(c0 + i));
+            for (; has; has &= has - 1) {
+                const int g = four0 + 32 * (__ffs(has) - 1) + lane;
+                float l[4];
+                four(g, l);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (in(l[j])) {
+                        if (at < room) st_remote(to_list + 8 * at, (u64)~key_of(l[j]) << 32 | (uint32_t)index(g, j));
                         ++at;
                     }
             }
@@ -515,6 +581,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
             sort(list, size);
         };
         constexpr int EACH = LIST / THREADS;
+        static_assert(EACH * THREADS == LIST && INNER <= LIST, "");
         // (first CTA) sums of the first m of the list, whose values `value` gives, for the EACH elements of a thread from `sums`:
         // inclusive sums
         auto list_sums = [&](const u64 *list, int m, auto value, u64(&sums)[EACH]) {
@@ -522,7 +589,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
 #pragma unroll
             for (int j = 0; j < EACH; ++j) {
                 const int i = threadIdx.x * EACH + j;
-                if (i < m) run += sc.weight(sh.table, value(list[i]));
+                if (i < m) run += sc.weight_of(sh.weight, value(list[i]));
                 sums[j] = run;
             }
             u64 total;
@@ -546,15 +613,47 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
         };
         auto by_key = [](u64 v) { return value_of(~(uint32_t)(v >> 32)); };
 
-        const bool cut_k = by_k && total_count > (u64)top_k;
+        bool cut_k = by_k && total_count > (u64)top_k;
         Found f{-1, 0, 0, 0};
-        if (cut_k) f = find(true, (u64)top_k);
-        else if (by_p) f = find(false, share_up(top_p, total_mass));
+        if (cut_k) {
+            f = find(true, (u64)top_k);
+            cut_k = f.bin >= 0;  // (else what is cut weighs nothing)
+        }
+        if (!cut_k && by_p) f = find(false, share_up(top_p, total_mass));
         if (f.bin >= 0 && (u64)f.count + f.in <= LIST) {
             // ---- a list of everything down to the border's bin: the first CTA does the rest ----
             gather(0, f.bin, sh.list, sh.listed[0], LIST);
             if (rank != 0) return;
-            const int m = (int)(f.count + f.in);
+            const int m = (int)(f.count + f.in), i = threadIdx.x;
+            if (m <= RANKED) {  // each compares itself with each
+                const u64 v = i < m ? sh.list[i] : 0;
+                const float l = by_key(v);
+                const u64 w = i < m ? sc.weight_of(sh.weight, l) : 0;
+                if (i < m) sh.inner[i] = w;
+                __syncthreads();
+                int before = 0;
+                u64 above = 0;
+                if (i < m)
+#pragma unroll 4
+                    for (int j = 0; j < m; ++j)
+                        if (sh.list[j] < v) ++before, above += sh.inner[j];
+                bool stays = i < m && (!cut_k || before < top_k);
+                if (by_p) {
+                    const u64 sum = block_sum(sh, stays ? w : 0);
+                    stays = stays && (before == 0 || above < share_up(top_p, cut_k ? sum : total_mass));
+                }
+                __syncthreads();
+                if (i < m) sh.inner[i] = stays ? w : 0;
+                __syncthreads();
+                u64 lower = 0;
+                if (i < m)
+#pragma unroll 4
+                    for (int j = 0; j < m; ++j)
+                        if ((uint32_t)sh.list[j] < (uint32_t)v) lower += sh.inner[j];
+                const u64 sum = block_sum(sh, stays ? w : 0), want = share(u, sum);
+                if (stays && lower <= want && want < lower + w) answer((int)(uint32_t)v, l, w, sum);
+                return;
+            }
             sort_list(sh.list, m);
             int keep = cut_k ? min(m, top_k) : m;
             u64 sums[EACH];
@@ -579,7 +678,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
             const int at = first_where(keep - 1, is);
             if (threadIdx.x == 0) {
                 const float l = by_index(sh.list[at]);
-                answer((int)(sh.list[at] >> 32), l, sc.weight(sh.table, l), sum);
+                answer((int)(sh.list[at] >> 32), l, sc.weight_of(sh.weight, l), sum);
             }
             return;
         }
@@ -589,16 +688,16 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
         u64 kept_mass = total_mass;
         // border, equals, ties from the bin where it falls: `least` elements from the row's first (or weight); returns the weight
         // of all that is kept
-        auto refine = [&](const Found &g, bool counts, u64 least, uint32_t &listed) -> u64 {
-            if (g.in <= INNER) {
-                gather(g.bin, g.bin, sh.inner, listed, INNER);
+        auto refine = [&](const Found &g, bool counts, u64 least, u64 *list, uint32_t room, uint32_t &listed) -> u64 {
+            if (g.in <= room) {
+                gather(g.bin, g.bin, list, listed, room);
                 u64 got[4] = {};
                 if (rank == 0) {
                     const int m = (int)g.in;
-                    sort_list(sh.inner, m);
+                    sort_list(list, m);
                     u64 sums[EACH];
                     bool is[EACH];
-                    if (by_p) list_sums(sh.inner, m, by_key, sums);
+                    if (by_p) list_sums(list, m, by_key, sums);
                     else
                         for (int j = 0; j < EACH; ++j) sums[j] = 0;
                     int at = (int)(least - g.count) - 1;
@@ -608,12 +707,12 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
                             is[j] = (int)threadIdx.x * EACH + j < m && g.mass + sums[j] >= least;
                         at = first_where(m - 1, is);
                     }
-                    const uint32_t k = ~(uint32_t)(sh.inner[at] >> 32);
+                    const uint32_t k = ~(uint32_t)(list[at] >> 32);
                     u64 same = 0;
 #pragma unroll
                     for (int j = 0; j < EACH; ++j) {
                         const int i = threadIdx.x * EACH + j;
-                        is[j] = i < m && ~(uint32_t)(sh.inner[i] >> 32) == k;
+                        is[j] = i < m && ~(uint32_t)(list[i] >> 32) == k;
                         same += is[j];
                         if (i == at) sh.found.mass = sums[j];
                     }
@@ -626,7 +725,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
                 border = (uint32_t)x[0][0], equals = x[0][1], ties = x[0][2];
                 return x[0][3];
             }
-            auto inside = [&](float l) { return in_min(l) && Scale::bin(sc.place(l)) == g.bin; };
+            auto inside = [&](float l) { return in_min(l) && Scale::bin(sc.spot(l)) == g.bin; };
             // count and sum of the bin's elements from key k on
             auto since = [&](uint32_t k, u64 &c, u64 &m) {
                 uint32_t nc = 0, nc_all;
@@ -634,7 +733,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
                 each4([&](int, const float(&l)[4]) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        if (inside(l[j]) && key_of(l[j]) >= k) ++nc, nm += sc.weight(sh.table, l[j]);
+                        if (inside(l[j]) && key_of(l[j]) >= k) ++nc, nm += sc.weight_of(sh.weight, l[j]);
                 });
                 block_scan(sh, nc, nm, nc_all, nm_all);
                 u64(*x)[4] = exchange(nc_all, nm_all, 0, 0);
@@ -642,8 +741,11 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
                 for (int r = 0; r < parts; ++r) c += x[r][0], m += x[r][1];
             };
             uint32_t lo = UINT32_MAX, hi = 0;
-            for (int i = from; i < to; ++i)
-                if (inside(data[i])) lo = min(lo, key_of(data[i])), hi = max(hi, key_of(data[i]));
+            each4([&](int, const float(&l)[4]) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (inside(l[j])) lo = min(lo, key_of(l[j])), hi = max(hi, key_of(l[j]));
+            });
             lo = __reduce_min_sync(0xffffffffu, lo), hi = __reduce_max_sync(0xffffffffu, hi);
             __syncthreads();
             if (lane == 0) sh.part[threadIdx.x >> 5] = (u64)lo << 32 | hi;
@@ -670,37 +772,51 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
             equals = min(equals, ties);
             return m + equals * w;
         };
-        if (cut_k) kept_mass = refine(f, true, (u64)top_k, sh.listed[1]);
+        if (cut_k) kept_mass = refine(f, true, (u64)top_k, by_p ? sh.inner : sh.list, by_p ? INNER : LIST, sh.listed[1]);  // (the list takes the histogram's place)
         if (by_p) {
             const u64 want = share_up(top_p, kept_mass);
             const uint32_t k_border = border;
             const u64 k_equals = equals, k_ties = ties;
             const Found g = cut_k ? find(false, want) : f;
             if (g.bin >= 0 && !(cut_k && g.bin > f.bin)) {
-                refine(g, false, want, sh.listed[2]);
+                refine(g, false, want, sh.list, LIST, sh.listed[2]);
                 if (cut_k && border < k_border) border = k_border, equals = k_equals, ties = k_ties;
                 else if (cut_k && border == k_border) equals = min(equals, k_equals);
             }
         }
         if (equals < ties) {  // the index of the last equal that is kept
-            u64 mine = 0, all;
-            for (int i = from; i < to; ++i) mine += key_of(data[i]) == border;
-            const u64 upto = block_scan(sh, mine, all);
+            uint32_t mine = 0, all;
+            const float value = value_of(border);
+            each4([&](int, const float(&l)[4]) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mine += l[j] == value;
+            });
+            mine = __reduce_add_sync(0xffffffffu, mine);
+            const uint32_t upto = block_scan(sh, lane == 31 ? mine : 0u, all);  // (lane 31: up to the warp's end)
             u64 before = 0;
             {
                 u64(*x)[4] = exchange(all, 0, 0, 0);
                 for (int r = 0; r < rank; ++r) before += x[r][0];
             }
-            u64 c = before + upto - mine;
-            __syncthreads();
             if (threadIdx.x == 0) sh.part[0] = ~0ull;
             __syncthreads();
+            u64 c = before + __shfl_sync(0xffffffffu, upto, 31) - mine;  // before the warp
             if (c < equals && equals <= c + mine)
-                for (int i = from;; ++i)
-                    if (key_of(data[i]) == border && ++c == equals) {
-                        sh.part[0] = (u64)(c0 + i);
-                        break;
+                for (int g0 = four0; g0 < four1; g0 += 32) {
+                    float l[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    if (g0 + lane < four1) four(g0 + lane, l);
+                    uint32_t own = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) own += l[j] == value;
+                    const uint32_t to_here = warp_scan(own, lane);
+                    if (c + to_here - own < equals && equals <= c + to_here) {
+                        uint32_t at = (uint32_t)(equals - (c + to_here - own));
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (l[j] == value && --at == 0) sh.part[0] = (u64)index(g0 + lane, j);
                     }
+                    c += __shfl_sync(0xffffffffu, to_here, 31);
+                }
             __syncthreads();
             u64(*x)[4] = exchange(sh.part[0], 0, 0, 0);
             for (int r = 0; r < parts; ++r)
@@ -709,19 +825,28 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
     }
 
     // ---- the kept weights' sums in index order, and where u falls ----
-    auto kept = [&](float l, int i) {
-        const uint32_t k = key_of(l);
-        return k > border || (k == border && c0 + i <= last);
-    };
-    u64 mine = 0, all;
-    each4([&](int i, const float(&l)[4]) {
+    const float value = value_of(border);
+    auto kept = [&](float l, int i) { return l > value || (l == value && i <= last); };
+    auto weights = [&](int g, const float(&l)[4], u64 sum) {  // sum + those of a four
+        int b[4];
         u64 w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = sc.weight(sh.table, l[j]);
+        sc.weigh(sh.weight, l, b, w);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (kept(l[j], i + j)) mine += w[j];
-    });
+            if (kept(l[j], index(g, j))) sum += w[j];
+        return sum;
+    };
+    u64 mine = 0, all;
+    if (last == INT32_MAX)
+        each4([&](int, const float(&l)[4]) {
+            int b[4];
+            u64 w[4];
+            sc.weigh(sh.weight, l, b, w);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (l[j] >= value) mine += w[j];
+        });
+    else each4([&](int g, const float(&l)[4]) { mine = weights(g, l, mine); });
     const u64 upto = block_scan(sh, mine, all);
     u64 before = 0, sum = 0;
     {
@@ -731,20 +856,25 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
             sum += x[r][0];
         }
     }
-    const u64 want = share(u, sum), c = before + upto;
-    const uint32_t here = __ballot_sync(0xffffffffu, c - mine <= want && c > want);  // one thread of all
-    if (!here) return;
-    // its warp walks the stretch
-    const int who = __ffs(here) - 1;
-    u64 at = __shfl_sync(0xffffffffu, c - mine, who);
-    const int first = __shfl_sync(0xffffffffu, from, who), end = __shfl_sync(0xffffffffu, to, who);
-    for (int i0 = first; i0 < end; i0 += 32) {
-        const int i = i0 + lane;
-        const u64 w = i < end && kept(data[i], i) ? sc.weight(sh.table, data[i]) : 0;
-        const u64 to_here = at + warp_scan(w, lane);
+    const u64 want = share(u, sum), warp_end = before + __shfl_sync(0xffffffffu, upto, 31);
+    u64 at = before + __shfl_sync(0xffffffffu, upto - mine, 0);
+    if (at > want || warp_end <= want) return;
+    // one warp of all: it walks its stretch
+    for (int g0 = four0; g0 < four1; g0 += 32) {
+        float l[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (g0 + lane < four1) four(g0 + lane, l);
+        const u64 own = weights(g0 + lane, l, 0), to_here = at + warp_scan(own, lane);
         const uint32_t past = __ballot_sync(0xffffffffu, to_here > want);
         if (past) {
-            if (lane == __ffs(past) - 1) answer(c0 + i, data[i], w, sum);
+            if (lane == __ffs(past) - 1) {
+                u64 c = to_here - own;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const u64 w = kept(l[j], index(g0 + lane, j)) ? sc.weight_of(sh.weight, l[j]) : 0;
+                    if (c <= want && c + w > want) answer(index(g0 + lane, j), l[j], w, sum);
+                    c += w;
+                }
+            }
             return;
         }
         at = __shfl_sync(0xffffffffu, to_here, 31);
@@ -758,13 +888,14 @@ static int launch(const Args &a, int B, cudaStream_t s) {
     const int rc = device_info(dev, sms);
     if (rc != PQE_OK) return rc;
     constexpr size_t HEAD = (sizeof(Shared) + 127) / 128 * 128 + 64;  // + room to align the pieces
+    static_assert(HEAD + CHUNK_MAX * sizeof(float) <= 227 * 1024, "shared memory of one CTA");
     if (!attr_set[dev].load(std::memory_order_relaxed)) {
         PQE_CUDA_TRY(cudaFuncSetAttribute(sample_kernel<FP32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           (int)(HEAD + CHUNK_MAX * sizeof(float))));
         attr_set[dev].store(1, std::memory_order_relaxed);
     }
     // as few CTAs a row as leave room for two on an SM; more where SMs would stay idle
-    constexpr int CHUNK_TWO = 20224;
+    constexpr int CHUNK_TWO = 19968;
     int log = 0;
     while (log < 3 && (a.V + (1 << log) - 1) >> log > CHUNK_TWO) ++log;
     while (log < 3 && ((int64_t)B << (log + 1)) <= sms && a.V >> (log + 1) >= 2048) ++log;
