@@ -51,7 +51,7 @@ constexpr int CHUNK_MAX = 49152;             // logits of a CTA; sums of a bin's
 static_assert((int64_t)CHUNK_MAX << 13 < (int64_t)1 << 32, "");
 
 // 2^SCALE 2^(-i / 32)
-__constant__ u64 TABLE[OCTAVE] = {
+__device__ const u64 TABLE[OCTAVE] = {
     8796093022208ull, 8607610887057ull, 8423167535396ull, 8242676424423ull, 8066052865769ull, 7893213985764ull, 7724078686549ull, 7558567608024ull,
     7396603090613ull, 7238109138825ull, 7083011385596ull, 6931237057393ull, 6782714940072ull, 6637375345460ull, 6495150078656ull, 6355972406040ull,
     6219777023951ull, 6086500028053ull, 5956078883349ull, 5828452394836ull, 5703560678795ull, 5581345134690ull, 5461748417677ull, 5344714411690ull,
@@ -75,12 +75,19 @@ struct Found {         // where a border falls
 struct Shared {
     u64 part[WARPS];                  // of block scans
     uint32_t count_part[WARPS];
+    struct {
+        u64 mass, far_mass;
+        uint32_t count, far_count;
+    } parts[WARPS];
     u64 swap[4][MAX_PARTS][4];        // of the cluster's exchanges, four in turn
     u64 weight[FAR + 1];              // of the upper ends of the bins: bin b holds P from b - 1 on
     uint32_t listed[3];               // entries of the list, of the inner one, of that once more
     double min_drop;                  // t ln(min_p)
     Found found;
-    u64 inner[INNER];
+    union {
+        u64 tops[MAX_PARTS * WARPS];  // at first: each warp's largest logit, and whether one was not a number
+        u64 inner[INNER];
+    };
     union {
         struct {
             uint32_t count[BINS];     // merged in place: counts, and sums of weights as (low, high) words
@@ -350,16 +357,17 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // the other CTAs have begun
     bad = __any_sync(0xffffffffu, bad);
     uint32_t key = __reduce_max_sync(0xffffffffu, key_of(top));
-    if (lane == 0) sh.part[threadIdx.x >> 5] = (u64)bad << 32 | key;
-    __syncthreads();
-    for (int w = 0; w < WARPS; ++w) {
-        bad |= (sh.part[w] >> 32) != 0;
-        key = max(key, (uint32_t)sh.part[w]);
+    if (lane < parts) st_remote(map_rank(smem_u32(&sh.tops[rank * WARPS + warp]), lane), (u64)bad << 32 | key);
+    __syncwarp();
+    cluster_sync();
+    bad = false, key = 0;
+    for (int i = lane; i < parts * WARPS; i += 32) {
+        const u64 x = sh.tops[i];
+        bad |= (x >> 32) != 0;
+        key = max(key, (uint32_t)x);
     }
-    {
-        u64(*x)[4] = exchange(key, bad, 0, 0);
-        for (int r = 0; r < parts; ++r) key = max(key, (uint32_t)x[r][0]), bad |= x[r][1] != 0;
-    }
+    bad = __any_sync(0xffffffffu, bad);
+    key = __reduce_max_sync(0xffffffffu, key);
     top = value_of(key);
     // (one thread) the token at a logit, whose weight is w of `sum`
     auto answer = [&](int token, float l, u64 w, u64 sum) {
@@ -492,10 +500,26 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
             bins_count += c;
             bins_mass += w;
         }
-        uint32_t slice_count, far_all_count = 0, count_to = bins_count;
-        u64 slice_mass, far_all_mass = 0, mass_to = bins_mass;
-        block_scan(sh, count_to, mass_to, slice_count, slice_mass);
-        block_scan(sh, far_count, far_mass, far_all_count, far_all_mass);
+        uint32_t slice_count = 0, far_all_count = 0, count_to = warp_scan(bins_count, lane);
+        u64 slice_mass = 0, far_all_mass = 0, mass_to = by_p ? warp_scan(bins_mass, lane) : 0;
+        far_count = __reduce_add_sync(0xffffffffu, far_count);
+        if (by_p)
+#pragma unroll
+            for (int o = 16; o; o /= 2) far_mass += __shfl_xor_sync(0xffffffffu, far_mass, o);
+        __syncthreads();
+        if (lane == 31) sh.parts[warp] = {mass_to, far_mass, count_to, far_count};
+        __syncthreads();
+        {
+            uint32_t c0_ = 0;
+            u64 m0 = 0;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) {
+                if (w == warp) c0_ = slice_count, m0 = slice_mass;
+                slice_count += sh.parts[w].count, slice_mass += sh.parts[w].mass;
+                far_all_count += sh.parts[w].far_count, far_all_mass += sh.parts[w].far_mass;
+            }
+            count_to += c0_, mass_to += m0;
+        }
         u64 total_count = 0, total_mass = 0, before_count = 0, before_mass = 0;
         {
             u64(*x)[4] = exchange(slice_count, slice_mass, far_all_count, far_all_mass);
@@ -545,19 +569,15 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
                 mine += any;
                 if (any) has |= 1u << ((g - four0) / 32);
             });
-            uint32_t all;
-            const uint32_t upto = block_scan(sh, mine, all);
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                uint32_t at;
+            // a warp takes its places, if it needs any
+            const uint32_t upto = warp_scan(mine, lane);
+            uint32_t at = 0;
+            if (lane == 31 && upto)
                 asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;"
                              : "=r"(at)
-                             : "r"(map_rank(smem_u32(&listed), 0)), "r"(all)
+                             : "r"(map_rank(smem_u32(&listed), 0)), "r"(upto)
                              : "memory");
-                sh.part[0] = at;
-            }
-            __syncthreads();
-            uint32_t at = (uint32_t)sh.part[0] + upto - mine;
+            at = __shfl_sync(0xffffffffu, at, 31) + upto - mine;
             const uint32_t to_list = map_rank(smem_u32(list), 0);
             for (; has; has &= has - 1) {
                 const int g = four0 + 32 * (__ffs(has) - 1) + lane;
