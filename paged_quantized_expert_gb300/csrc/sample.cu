@@ -44,6 +44,7 @@ constexpr int OCTAVE = 32;                   // bins for a factor of two
 constexpr int FAR = 44 * OCTAVE + 1;         // what falls into this bin weighs less than 2^-44: nothing
 constexpr int BINS = 1536;                   // FAR and a little, in slices of whole warps
 constexpr int LIST = 2048, INNER = 512;       // candidates that one CTA sorts: all of a row's, or a bin's beside the histogram
+constexpr int GROUPS = 128, FEW_K = 100;     // groups of lanes whose largest logits are compared; up to this top_k by them alone
 constexpr int RANKED = 256;                  // up to so many it ranks by comparing each with each
 constexpr int MAX_PARTS = 8;
 constexpr int SCALE = 43;                    // the largest logit's weight: 2^43; 2^18.6 of them fit 63 bits
@@ -58,7 +59,8 @@ __device__ const u64 TABLE[OCTAVE] = {
     5230188203118ull, 5118116055032ull, 5008445381977ull, 4901124725294ull, 4796103728980ull, 4693333116055ull, 4592764665442ull, 4494351189345ull};
 constexpr int SLACK = 65536;                 // of 2^30: a weight is less than that under its bin's lower end (0.001 of P, and roundings)
 
-// Whole numbers that order as the values do (-0 as +0); -infinity gives KEY_NEG_INF, NaN below it or above +infinity's.
+// Whole numbers that order as the values do (-0 as +0), NaN below -infinity's or above +infinity's.
+constexpr uint32_t KEY_NEG_INF = 0x007FFFFFu, KEY_INF = 0xFF800000u;
 __device__ __forceinline__ uint32_t key_of(float l) {
     const uint32_t b = __float_as_uint(l + 0.f);
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
@@ -73,21 +75,24 @@ struct Found {         // where a border falls
 };
 
 struct Shared {
-    u64 part[WARPS];                  // of block scans
-    uint32_t count_part[WARPS];
-    struct {
-        u64 mass, far_mass;
-        uint32_t count, far_count;
-    } parts[WARPS];
-    u64 swap[4][MAX_PARTS][4];        // of the cluster's exchanges, four in turn
+    union {                           // of block scans
+        struct {
+            u64 part[WARPS];
+            uint32_t count_part[WARPS];
+        };
+        struct {
+            u64 mass, far_mass;
+            uint32_t count, far_count;
+        } parts[WARPS];
+    };
+    u64 swap[3][MAX_PARTS][4];        // of the cluster's exchanges, three in turn
     u64 weight[FAR + 1];              // of the upper ends of the bins: bin b holds P from b - 1 on
-    uint32_t listed[3];               // entries of the list, of the inner one, of that once more
+    uint32_t listed[4];               // entries of each list gathered
     double min_drop;                  // t ln(min_p)
     Found found;
-    union {
-        u64 tops[MAX_PARTS * WARPS];  // at first: each warp's largest logit, and whether one was not a number
-        u64 inner[INNER];
-    };
+    uint32_t tops[GROUPS];            // the groups' largest logits
+    float floor;                      // no smaller logit is among the first top_k
+    u64 inner[INNER];
     union {
         struct {
             uint32_t count[BINS];     // merged in place: counts, and sums of weights as (low, high) words
@@ -271,7 +276,8 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
 
     // every CTA's four values to every CTA
     auto exchange = [&](u64 v0, u64 v1, u64 v2, u64 v3) -> u64(*)[4] {
-        u64(*slot)[4] = sh.swap[swaps++ & 3];
+        u64(*slot)[4] = sh.swap[swaps];
+        swaps = swaps == 2 ? 0 : swaps + 1;
         __syncthreads();
         if ((int)threadIdx.x < 4 * parts) {
             const int j = threadIdx.x & 3;
@@ -288,7 +294,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
         const u64 w = (TABLE[n % OCTAVE] + ((1ull << by) >> 1)) >> by;
         sh.weight[b] = b == 0 ? 2 * TABLE[OCTAVE - 1] : b == FAR ? 0 : w;
     }
-    if (threadIdx.x < 3) sh.listed[threadIdx.x] = 0;
+    if (threadIdx.x < 4) sh.listed[threadIdx.x] = 0;
     __syncthreads();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // waited for before the first exchange
     pdl_acquire();
@@ -355,19 +361,20 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
     }
     __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // the other CTAs have begun
-    bad = __any_sync(0xffffffffu, bad);
-    uint32_t key = __reduce_max_sync(0xffffffffu, key_of(top));
-    if (lane < parts) st_remote(map_rank(smem_u32(&sh.tops[rank * WARPS + warp]), lane), (u64)bad << 32 | key);
+    uint32_t key = bad ? UINT32_MAX : key_of(top);
+    {  // the largest of each group of 4 * parts lanes: GROUPS of them in the cluster
+        const int size = 4 * parts;
+        for (int o = size / 2; o; o /= 2) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
+        const int group = (rank * THREADS + (int)threadIdx.x) / size;
+        for (int r = lane % size; r < parts; r += size)
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(smem_u32(&sh.tops[group]), r)), "r"(key) : "memory");
+    }
     __syncwarp();
     cluster_sync();
-    bad = false, key = 0;
-    for (int i = lane; i < parts * WARPS; i += 32) {
-        const u64 x = sh.tops[i];
-        bad |= (x >> 32) != 0;
-        key = max(key, (uint32_t)x);
-    }
-    bad = __any_sync(0xffffffffu, bad);
+    key = 0;
+    for (int i = lane; i < GROUPS; i += 32) key = max(key, sh.tops[i]);
     key = __reduce_max_sync(0xffffffffu, key);
+    bad = key >= KEY_INF;
     top = value_of(key);
     // (one thread) the token at a logit, whose weight is w of `sum`
     auto answer = [&](int token, float l, u64 w, u64 sum) {
@@ -441,6 +448,171 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
     int last = INT32_MAX;
     const bool by_k = top_k > 0 && top_k < a.V, by_p = top_p < 1.f;
     if (by_k || by_p) {
+        // the elements whose spots lie in [s0, s1], in any order, to a list of the first CTA
+        auto gather = [&](float s0, float s1, u64 *list, uint32_t &listed, uint32_t room) {
+            auto in = [&](float l) {
+                const float at = sc.spot(l);
+                return in_min(l) && at >= s0 && at <= s1;
+            };
+            // a lane's own, as bits of its fours
+            uint32_t mine = 0, has = 0;
+            each4([&](int g, const float(&l)[4]) {
+                uint32_t any = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) any += in(l[j]);
+                mine += any;
+                if (any) has |= 1u << ((g - four0) / 32);
+            });
+            // a warp takes its places, if it needs any
+            const uint32_t upto = warp_scan(mine, lane);
+            uint32_t at = 0;
+            if (lane == 31 && upto)
+                asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;"
+                             : "=r"(at)
+                             : "r"(map_rank(smem_u32(&listed), 0)), "r"(upto)
+                             : "memory");
+            at = __shfl_sync(0xffffffffu, at, 31) + upto - mine;
+            const uint32_t to_list = map_rank(smem_u32(list), 0);
+            for (; has; has &= has - 1) {
+                const int g = four0 + 32 * (__ffs(has) - 1) + lane;
+                float l[4];
+                four(g, l);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (in(l[j])) {
+                        if (at < room) st_remote(to_list + 8 * at, (u64)~key_of(l[j]) << 32 | (uint32_t)index(g, j));
+                        ++at;
+                    }
+            }
+            __syncwarp();
+            cluster_sync();
+        };
+        // (first CTA) a list in order, padded to a power of two
+        auto sort_list = [&](u64 *list, int m) {
+            int size = 2;
+            while (size < m) size *= 2;
+            for (int i = m + threadIdx.x; i < size; i += THREADS) list[i] = ~0ull;
+            sort(list, size);
+        };
+        constexpr int EACH = LIST / THREADS;
+        static_assert(EACH * THREADS == LIST && INNER <= LIST, "");
+        // (first CTA) sums of the first m of the list, whose values `value` gives, for the EACH elements of a thread from `sums`:
+        // inclusive sums
+        auto list_sums = [&](const u64 *list, int m, auto value, u64(&sums)[EACH]) {
+            u64 run = 0;
+#pragma unroll
+            for (int j = 0; j < EACH; ++j) {
+                const int i = threadIdx.x * EACH + j;
+                if (i < m) run += sc.weight_of(sh.weight, value(list[i]));
+                sums[j] = run;
+            }
+            u64 total;
+            const u64 upto = block_scan(sh, run, total);
+#pragma unroll
+            for (int j = 0; j < EACH; ++j) sums[j] += upto - run;
+            return total;
+        };
+        auto first_where = [&](int none, const bool(&is)[EACH]) {  // the lowest index of the list where `is`, or none
+            int at = INT32_MAX;
+#pragma unroll
+            for (int j = EACH - 1; j >= 0; --j)
+                if (is[j]) at = threadIdx.x * EACH + j;
+            at = __reduce_min_sync(0xffffffffu, at);
+            __syncthreads();
+            if (lane == 0) sh.part[threadIdx.x >> 5] = (u64)at;
+            __syncthreads();
+            for (int w = 0; w < WARPS; ++w) at = min(at, (int)sh.part[w]);
+            __syncthreads();
+            return at == INT32_MAX ? none : at;
+        };
+        auto by_key = [](u64 v) { return value_of(~(uint32_t)(v >> 32)); };
+
+        // (first CTA) the rest, from a list of m that holds all that top_k or top_p may leave: `total` is the weight of the row
+        auto finish = [&](u64 *list, u64 *spare, int m, bool cut_k, u64 total) {
+            const int i = threadIdx.x;
+            if (m <= RANKED) {  // each compares itself with each
+                const u64 v = i < m ? list[i] : 0;
+                const float l = by_key(v);
+                const u64 w = i < m ? sc.weight_of(sh.weight, l) : 0;
+                if (i < m) spare[i] = w;
+                __syncthreads();
+                int before = 0;
+                u64 above = 0;
+                if (i < m)
+#pragma unroll 4
+                    for (int j = 0; j < m; ++j)
+                        if (list[j] < v) ++before, above += spare[j];
+                bool stays = i < m && (!cut_k || before < top_k);
+                if (by_p) {
+                    const u64 sum = block_sum(sh, stays ? w : 0);
+                    stays = stays && (before == 0 || above < share_up(top_p, cut_k ? sum : total));
+                }
+                __syncthreads();
+                if (i < m) spare[i] = stays ? w : 0;
+                __syncthreads();
+                u64 lower = 0;
+                if (i < m)
+#pragma unroll 4
+                    for (int j = 0; j < m; ++j)
+                        if ((uint32_t)list[j] < (uint32_t)v) lower += spare[j];
+                const u64 sum = block_sum(sh, stays ? w : 0), want = share(u, sum);
+                if (stays && lower <= want && want < lower + w) answer((int)(uint32_t)v, l, w, sum);
+                return;
+            }
+            sort_list(list, m);
+            int keep = cut_k ? min(m, top_k) : m;
+            u64 sums[EACH];
+            bool is[EACH];
+            if (by_p) {
+                const u64 sum = list_sums(list, keep, by_key, sums);
+                const u64 want = share_up(top_p, cut_k ? sum : total);
+#pragma unroll
+                for (int j = 0; j < EACH; ++j) is[j] = (int)threadIdx.x * EACH + j < keep && sums[j] >= want;
+                keep = first_where(keep - 1, is) + 1;
+            }
+            // the kept ones by index
+            int size = 2;
+            while (size < keep) size *= 2;
+            for (int i = threadIdx.x; i < size; i += THREADS) list[i] = i < keep ? list[i] << 32 | list[i] >> 32 : ~0ull;
+            sort(list, size);
+            auto by_index = [](u64 v) { return value_of(~(uint32_t)v); };
+            const u64 sum = list_sums(list, keep, by_index, sums);
+            const u64 want = share(u, sum);
+#pragma unroll
+            for (int j = 0; j < EACH; ++j) is[j] = (int)threadIdx.x * EACH + j < keep && sums[j] > want;
+            const int at = first_where(keep - 1, is);
+            if (threadIdx.x == 0) {
+                const float l = by_index(list[at]);
+                answer((int)(list[at] >> 32), l, sc.weight_of(sh.weight, l), sum);
+            }
+            return;
+        };
+        // ---- a small top_k: at least that many logits are not below the top_k-th of the groups' largest, and hardly more ----
+        if (by_k && top_k <= FEW_K) {
+            if ((int)threadIdx.x < GROUPS) {
+                const uint32_t mine = sh.tops[threadIdx.x];
+                int before = 0;
+#pragma unroll 8
+                for (int i = 0; i < GROUPS; ++i) {
+                    const uint32_t x = sh.tops[i];
+                    before += x > mine || (x == mine && i < (int)threadIdx.x);
+                }
+                if (before == top_k - 1) sh.floor = mine > KEY_NEG_INF ? value_of(mine) : -INFINITY;
+            }
+            __syncthreads();
+            // (spots rise as logits fall: all of the floor's spot come along)
+            gather(Scale::spot_of(0), sc.spot(sh.floor), sh.inner, sh.listed[0], INNER);
+            const uint32_t m = ld_remote(map_rank(smem_u32(&sh.listed[0]), 0));
+            if (m <= INNER) {
+                __syncwarp();
+                asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+                if (rank != 0) return;
+                finish(sh.inner, sh.list, (int)m, true, 0);
+                __syncwarp();
+                asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all have read the count here
+                return;
+            }
+        }
         // ---- the histogram. What weighs nothing is only counted. Without top_k so is, with its weight, what all of a row's V logits
         // together could not lift over 1 - top_p of the largest's weight alone: it holds no border ----
         const int limit = by_k || top_p <= 0.f ? FAR : min(FAR, (int)((float)OCTAVE * log2f((float)a.V / (1.f - top_p))) + 3);
@@ -553,86 +725,6 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
                 got = {(int)(uint32_t)(x[r][0] >> 32), (uint32_t)x[r][0], (uint32_t)x[r][1], x[r][2]};
             return got;
         };
-        // the elements in bins [b0, b1], in any order, to a list of the first CTA
-        auto gather = [&](int b0, int b1, u64 *list, uint32_t &listed, uint32_t room) {
-            const float s0 = Scale::spot_of(b0), s1 = Scale::spot_of(b1);
-            auto in = [&](float l) {
-                const float at = sc.spot(l);
-                return in_min(l) && at >= s0 && at <= s1;
-            };
-            // a lane's own, as bits of its fours
-            uint32_t mine = 0, has = 0;
-            each4([&](int g, const float(&l)[4]) {
-                uint32_t any = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) any += in(l[j]);
-                mine += any;
-                if (any) has |= 1u << ((g - four0) / 32);
-            });
-            // a warp takes its places, if it needs any
-            const uint32_t upto = warp_scan(mine, lane);
-            uint32_t at = 0;
-            if (lane == 31 && upto)
-                asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;"
-                             : "=r"(at)
-                             : "r"(map_rank(smem_u32(&listed), 0)), "r"(upto)
-                             : "memory");
-            at = __shfl_sync(0xffffffffu, at, 31) + upto - mine;
-            const uint32_t to_list = map_rank(smem_u32(list), 0);
-            for (; has; has &= has - 1) {
-                const int g = four0 + 32 * (__ffs(has) - 1) + lane;
-                float l[4];
-                four(g, l);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (in(l[j])) {
-                        if (at < room) st_remote(to_list + 8 * at, (u64)~key_of(l[j]) << 32 | (uint32_t)index(g, j));
-                        ++at;
-                    }
-            }
-            __syncwarp();
-            cluster_sync();
-        };
-        // (first CTA) a list in order, padded to a power of two
-        auto sort_list = [&](u64 *list, int m) {
-            int size = 2;
-            while (size < m) size *= 2;
-            for (int i = m + threadIdx.x; i < size; i += THREADS) list[i] = ~0ull;
-            sort(list, size);
-        };
-        constexpr int EACH = LIST / THREADS;
-        static_assert(EACH * THREADS == LIST && INNER <= LIST, "");
-        // (first CTA) sums of the first m of the list, whose values `value` gives, for the EACH elements of a thread from `sums`:
-        // inclusive sums
-        auto list_sums = [&](const u64 *list, int m, auto value, u64(&sums)[EACH]) {
-            u64 run = 0;
-#pragma unroll
-            for (int j = 0; j < EACH; ++j) {
-                const int i = threadIdx.x * EACH + j;
-                if (i < m) run += sc.weight_of(sh.weight, value(list[i]));
-                sums[j] = run;
-            }
-            u64 total;
-            const u64 upto = block_scan(sh, run, total);
-#pragma unroll
-            for (int j = 0; j < EACH; ++j) sums[j] += upto - run;
-            return total;
-        };
-        auto first_where = [&](int none, const bool(&is)[EACH]) {  // the lowest index of the list where `is`, or none
-            int at = INT32_MAX;
-#pragma unroll
-            for (int j = EACH - 1; j >= 0; --j)
-                if (is[j]) at = threadIdx.x * EACH + j;
-            at = __reduce_min_sync(0xffffffffu, at);
-            __syncthreads();
-            if (lane == 0) sh.part[threadIdx.x >> 5] = (u64)at;
-            __syncthreads();
-            for (int w = 0; w < WARPS; ++w) at = min(at, (int)sh.part[w]);
-            __syncthreads();
-            return at == INT32_MAX ? none : at;
-        };
-        auto by_key = [](u64 v) { return value_of(~(uint32_t)(v >> 32)); };
-
         bool cut_k = by_k && total_count > (u64)top_k;
         Found f{-1, 0, 0, 0};
         if (cut_k) {
@@ -642,64 +734,8 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
         if (!cut_k && by_p) f = find(false, share_up(top_p, total_mass));
         if (f.bin >= 0 && (u64)f.count + f.in <= LIST) {
             // ---- a list of everything down to the border's bin: the first CTA does the rest ----
-            gather(0, f.bin, sh.list, sh.listed[0], LIST);
-            if (rank != 0) return;
-            const int m = (int)(f.count + f.in), i = threadIdx.x;
-            if (m <= RANKED) {  // each compares itself with each
-                const u64 v = i < m ? sh.list[i] : 0;
-                const float l = by_key(v);
-                const u64 w = i < m ? sc.weight_of(sh.weight, l) : 0;
-                if (i < m) sh.inner[i] = w;
-                __syncthreads();
-                int before = 0;
-                u64 above = 0;
-                if (i < m)
-#pragma unroll 4
-                    for (int j = 0; j < m; ++j)
-                        if (sh.list[j] < v) ++before, above += sh.inner[j];
-                bool stays = i < m && (!cut_k || before < top_k);
-                if (by_p) {
-                    const u64 sum = block_sum(sh, stays ? w : 0);
-                    stays = stays && (before == 0 || above < share_up(top_p, cut_k ? sum : total_mass));
-                }
-                __syncthreads();
-                if (i < m) sh.inner[i] = stays ? w : 0;
-                __syncthreads();
-                u64 lower = 0;
-                if (i < m)
-#pragma unroll 4
-                    for (int j = 0; j < m; ++j)
-                        if ((uint32_t)sh.list[j] < (uint32_t)v) lower += sh.inner[j];
-                const u64 sum = block_sum(sh, stays ? w : 0), want = share(u, sum);
-                if (stays && lower <= want && want < lower + w) answer((int)(uint32_t)v, l, w, sum);
-                return;
-            }
-            sort_list(sh.list, m);
-            int keep = cut_k ? min(m, top_k) : m;
-            u64 sums[EACH];
-            bool is[EACH];
-            if (by_p) {
-                const u64 sum = list_sums(sh.list, keep, by_key, sums);
-                const u64 want = share_up(top_p, cut_k ? sum : total_mass);
-#pragma unroll
-                for (int j = 0; j < EACH; ++j) is[j] = (int)threadIdx.x * EACH + j < keep && sums[j] >= want;
-                keep = first_where(keep - 1, is) + 1;
-            }
-            // the kept ones by index
-            int size = 2;
-            while (size < keep) size *= 2;
-            for (int i = threadIdx.x; i < size; i += THREADS) sh.list[i] = i < keep ? sh.list[i] << 32 | sh.list[i] >> 32 : ~0ull;
-            sort(sh.list, size);
-            auto by_index = [](u64 v) { return value_of(~(uint32_t)v); };
-            const u64 sum = list_sums(sh.list, keep, by_index, sums);
-            const u64 want = share(u, sum);
-#pragma unroll
-            for (int j = 0; j < EACH; ++j) is[j] = (int)threadIdx.x * EACH + j < keep && sums[j] > want;
-            const int at = first_where(keep - 1, is);
-            if (threadIdx.x == 0) {
-                const float l = by_index(sh.list[at]);
-                answer((int)(sh.list[at] >> 32), l, sc.weight_of(sh.weight, l), sum);
-            }
+            gather(Scale::spot_of(0), Scale::spot_of(f.bin), sh.list, sh.listed[3], LIST);
+            if (rank == 0) finish(sh.list, sh.inner, (int)(f.count + f.in), cut_k, total_mass);
             return;
         }
         // ---- the border's value alone ----
@@ -710,7 +746,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
         // of all that is kept
         auto refine = [&](const Found &g, bool counts, u64 least, u64 *list, uint32_t room, uint32_t &listed) -> u64 {
             if (g.in <= room) {
-                gather(g.bin, g.bin, list, listed, room);
+                gather(Scale::spot_of(g.bin), Scale::spot_of(g.bin), list, listed, room);
                 u64 got[4] = {};
                 if (rank == 0) {
                     const int m = (int)g.in;
