@@ -820,7 +820,7 @@ PQE_API int fp8_block_matmul(const uint8_t *x, int64_t x_stride, const float *x_
  * u           device fp32 [B]
  * tokens      device int32 [B] out; logprobs device fp32 [B] out or NULL
  * status      device int32
- * 1 <= V <= 393216; B >= 0 (0: a no-op). */
+ * 1 <= V <= 368640; B >= 0 (0: a no-op). */
 PQE_API int sample_tokens(const void *logits, int fp32, int64_t stride, int B, int V, const float *temperature,
                           const int32_t *top_k, const float *top_p, const float *min_p, const float *u,
                           int32_t *tokens, float *logprobs, int32_t *status, void *stream);

@@ -20,6 +20,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "pqe_common.cuh"
 #include "tc_ptx.cuh"
@@ -43,12 +44,12 @@ constexpr int THREADS = 512, WARPS = THREADS / 32;
 constexpr int OCTAVE = 32;                   // bins for a factor of two
 constexpr int FAR = 44 * OCTAVE + 1;         // what falls into this bin weighs less than 2^-44: nothing
 constexpr int BINS = 1536;                   // FAR and a little, in slices of whole warps
-constexpr int LIST = 2048, INNER = 512;       // candidates that one CTA sorts: all of a row's, or a bin's beside the histogram
+constexpr int LIST = 2 * THREADS;            // elements of a bin that one CTA sorts, two a thread
 constexpr int GROUPS = 128, FEW_K = 100;     // groups of lanes whose largest logits are compared; up to this top_k by them alone
-constexpr int RANKED = 256;                  // up to so many it ranks by comparing each with each
+constexpr int RANKED = 256;                  // candidates of a row that it ranks by comparing each with each
 constexpr int MAX_PARTS = 8;
 constexpr int SCALE = 43;                    // the largest logit's weight: 2^43; 2^18.6 of them fit 63 bits
-constexpr int CHUNK_MAX = 49152;             // logits of a CTA; sums of a bin's 13-bit parts stay below 2^32
+constexpr int CHUNK_MAX = 46080;             // logits of a CTA; sums of a bin's 13-bit parts stay below 2^32
 static_assert((int64_t)CHUNK_MAX << 13 < (int64_t)1 << 32, "");
 
 // 2^SCALE 2^(-i / 32)
@@ -92,13 +93,13 @@ struct Shared {
     Found found;
     uint32_t tops[GROUPS];            // the groups' largest logits
     float floor;                      // no smaller logit is among the first top_k
-    u64 inner[INNER];
+    u64 list[LIST];
     union {
         struct {
             uint32_t count[BINS];     // merged in place: counts, and sums of weights as (low, high) words
             uint32_t lo[BINS], hi[BINS];
         };
-        u64 list[LIST];
+        u64 spare[RANKED];            // at the end
     };
 };
 
@@ -238,18 +239,36 @@ __device__ __forceinline__ u64 block_sum(Shared &sh, u64 v) {
     return all;
 }
 
-// ascending sort of n values (a power of two) by the whole CTA
-__device__ __forceinline__ void sort(u64 *v, int n) {
-    for (int k = 2; k <= n; k *= 2)
+// ascending sort of `size` values (a power of two, at most H * THREADS), a thread's at threadIdx.x and (H = 2) THREADS further on;
+// steps inside a warp by shuffles, the others through v
+template <int H>
+__device__ __forceinline__ void sort(u64 *v, u64 (&x)[H], int size) {
+    const int i = threadIdx.x;
+#pragma unroll 1
+    for (int k = 2; k <= size; k *= 2)
+#pragma unroll 1
         for (int j = k / 2; j > 0; j /= 2) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < n / 2; i += THREADS) {
-                const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
-                const u64 a = v[lo], b = v[hi];
-                if ((a > b) == ((lo & k) == 0)) v[lo] = b, v[hi] = a;
+            u64 y[H];
+            if (H == 2 && j == THREADS) {
+                y[0] = x[H - 1], y[H - 1] = x[0];
+            } else if (j >= 32) {
+                __syncthreads();
+#pragma unroll
+                for (int h = 0; h < H; ++h) v[i + h * THREADS] = x[h];
+                __syncthreads();
+#pragma unroll
+                for (int h = 0; h < H; ++h) y[h] = v[(i ^ j) + h * THREADS];
+            } else {
+#pragma unroll
+                for (int h = 0; h < H; ++h) y[h] = __shfl_xor_sync(0xffffffffu, x[h], j);
+            }
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const int at = i + h * THREADS;
+                const bool low = ((at & j) == 0) == ((at & k) == 0);  // keeps the smaller
+                x[h] = (x[h] < y[h]) == low ? x[h] : y[h];
             }
         }
-    __syncthreads();
 }
 
 __device__ __forceinline__ void st_remote(uint32_t addr, u64 v) {
@@ -448,8 +467,8 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
     int last = INT32_MAX;
     const bool by_k = top_k > 0 && top_k < a.V, by_p = top_p < 1.f;
     if (by_k || by_p) {
-        // the elements whose spots lie in [s0, s1], in any order, to a list of the first CTA
-        auto gather = [&](float s0, float s1, u64 *list, uint32_t &listed, uint32_t room) {
+        // the elements whose spots lie in [s0, s1], in any order, to the first CTA's list
+        auto gather = [&](float s0, float s1, uint32_t &listed, uint32_t room) {
             auto in = [&](float l) {
                 const float at = sc.spot(l);
                 return in_min(l) && at >= s0 && at <= s1;
@@ -472,7 +491,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
                              : "r"(map_rank(smem_u32(&listed), 0)), "r"(upto)
                              : "memory");
             at = __shfl_sync(0xffffffffu, at, 31) + upto - mine;
-            const uint32_t to_list = map_rank(smem_u32(list), 0);
+            const uint32_t to_list = map_rank(smem_u32(sh.list), 0);
             for (; has; has &= has - 1) {
                 const int g = four0 + 32 * (__ffs(has) - 1) + lane;
                 float l[4];
@@ -487,105 +506,38 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
             __syncwarp();
             cluster_sync();
         };
-        // (first CTA) a list in order, padded to a power of two
-        auto sort_list = [&](u64 *list, int m) {
-            int size = 2;
-            while (size < m) size *= 2;
-            for (int i = m + threadIdx.x; i < size; i += THREADS) list[i] = ~0ull;
-            sort(list, size);
-        };
-        constexpr int EACH = LIST / THREADS;
-        static_assert(EACH * THREADS == LIST && INNER <= LIST, "");
-        // (first CTA) sums of the first m of the list, whose values `value` gives, for the EACH elements of a thread from `sums`:
-        // inclusive sums
-        auto list_sums = [&](const u64 *list, int m, auto value, u64(&sums)[EACH]) {
-            u64 run = 0;
-#pragma unroll
-            for (int j = 0; j < EACH; ++j) {
-                const int i = threadIdx.x * EACH + j;
-                if (i < m) run += sc.weight_of(sh.weight, value(list[i]));
-                sums[j] = run;
-            }
-            u64 total;
-            const u64 upto = block_scan(sh, run, total);
-#pragma unroll
-            for (int j = 0; j < EACH; ++j) sums[j] += upto - run;
-            return total;
-        };
-        auto first_where = [&](int none, const bool(&is)[EACH]) {  // the lowest index of the list where `is`, or none
-            int at = INT32_MAX;
-#pragma unroll
-            for (int j = EACH - 1; j >= 0; --j)
-                if (is[j]) at = threadIdx.x * EACH + j;
-            at = __reduce_min_sync(0xffffffffu, at);
-            __syncthreads();
-            if (lane == 0) sh.part[threadIdx.x >> 5] = (u64)at;
-            __syncthreads();
-            for (int w = 0; w < WARPS; ++w) at = min(at, (int)sh.part[w]);
-            __syncthreads();
-            return at == INT32_MAX ? none : at;
-        };
         auto by_key = [](u64 v) { return value_of(~(uint32_t)(v >> 32)); };
 
-        // (first CTA) the rest, from a list of m that holds all that top_k or top_p may leave: `total` is the weight of the row
-        auto finish = [&](u64 *list, u64 *spare, int m, bool cut_k, u64 total) {
+        // (first CTA) the rest, from a list of m <= RANKED that holds all that top_k or top_p may leave: each compares itself with
+        // each. `total` is the weight of the row
+        auto finish = [&](int m, bool cut_k, u64 total) {
             const int i = threadIdx.x;
-            if (m <= RANKED) {  // each compares itself with each
-                const u64 v = i < m ? list[i] : 0;
-                const float l = by_key(v);
-                const u64 w = i < m ? sc.weight_of(sh.weight, l) : 0;
-                if (i < m) spare[i] = w;
-                __syncthreads();
-                int before = 0;
-                u64 above = 0;
-                if (i < m)
+            const u64 v = i < m ? sh.list[i] : 0;
+            const float l = by_key(v);
+            const u64 w = i < m ? sc.weight_of(sh.weight, l) : 0;
+            if (i < m) sh.spare[i] = w;
+            __syncthreads();
+            int before = 0;
+            u64 above = 0;
+            if (i < m)
 #pragma unroll 4
-                    for (int j = 0; j < m; ++j)
-                        if (list[j] < v) ++before, above += spare[j];
-                bool stays = i < m && (!cut_k || before < top_k);
-                if (by_p) {
-                    const u64 sum = block_sum(sh, stays ? w : 0);
-                    stays = stays && (before == 0 || above < share_up(top_p, cut_k ? sum : total));
-                }
-                __syncthreads();
-                if (i < m) spare[i] = stays ? w : 0;
-                __syncthreads();
-                u64 lower = 0;
-                if (i < m)
-#pragma unroll 4
-                    for (int j = 0; j < m; ++j)
-                        if ((uint32_t)list[j] < (uint32_t)v) lower += spare[j];
-                const u64 sum = block_sum(sh, stays ? w : 0), want = share(u, sum);
-                if (stays && lower <= want && want < lower + w) answer((int)(uint32_t)v, l, w, sum);
-                return;
-            }
-            sort_list(list, m);
-            int keep = cut_k ? min(m, top_k) : m;
-            u64 sums[EACH];
-            bool is[EACH];
+                for (int j = 0; j < m; ++j)
+                    if (sh.list[j] < v) ++before, above += sh.spare[j];
+            bool stays = i < m && (!cut_k || before < top_k);
             if (by_p) {
-                const u64 sum = list_sums(list, keep, by_key, sums);
-                const u64 want = share_up(top_p, cut_k ? sum : total);
-#pragma unroll
-                for (int j = 0; j < EACH; ++j) is[j] = (int)threadIdx.x * EACH + j < keep && sums[j] >= want;
-                keep = first_where(keep - 1, is) + 1;
+                const u64 sum = block_sum(sh, stays ? w : 0);
+                stays = stays && (before == 0 || above < share_up(top_p, cut_k ? sum : total));
             }
-            // the kept ones by index
-            int size = 2;
-            while (size < keep) size *= 2;
-            for (int i = threadIdx.x; i < size; i += THREADS) list[i] = i < keep ? list[i] << 32 | list[i] >> 32 : ~0ull;
-            sort(list, size);
-            auto by_index = [](u64 v) { return value_of(~(uint32_t)v); };
-            const u64 sum = list_sums(list, keep, by_index, sums);
-            const u64 want = share(u, sum);
-#pragma unroll
-            for (int j = 0; j < EACH; ++j) is[j] = (int)threadIdx.x * EACH + j < keep && sums[j] > want;
-            const int at = first_where(keep - 1, is);
-            if (threadIdx.x == 0) {
-                const float l = by_index(list[at]);
-                answer((int)(list[at] >> 32), l, sc.weight_of(sh.weight, l), sum);
-            }
-            return;
+            __syncthreads();
+            if (i < m) sh.spare[i] = stays ? w : 0;
+            __syncthreads();
+            u64 lower = 0;
+            if (i < m)
+#pragma unroll 4
+                for (int j = 0; j < m; ++j)
+                    if ((uint32_t)sh.list[j] < (uint32_t)v) lower += sh.spare[j];
+            const u64 sum = block_sum(sh, stays ? w : 0), want = share(u, sum);
+            if (stays && lower <= want && want < lower + w) answer((int)(uint32_t)v, l, w, sum);
         };
         // ---- a small top_k: at least that many logits are not below the top_k-th of the groups' largest, and hardly more ----
         if (by_k && top_k <= FEW_K) {
@@ -601,13 +553,13 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
             }
             __syncthreads();
             // (spots rise as logits fall: all of the floor's spot come along)
-            gather(Scale::spot_of(0), sc.spot(sh.floor), sh.inner, sh.listed[0], INNER);
+            gather(Scale::spot_of(0), sc.spot(sh.floor), sh.listed[0], RANKED);
             const uint32_t m = ld_remote(map_rank(smem_u32(&sh.listed[0]), 0));
-            if (m <= INNER) {
+            if (m <= RANKED) {
                 __syncwarp();
                 asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
                 if (rank != 0) return;
-                finish(sh.inner, sh.list, (int)m, true, 0);
+                finish((int)m, true, 0);
                 __syncwarp();
                 asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all have read the count here
                 return;
@@ -732,50 +684,65 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
             cut_k = f.bin >= 0;  // (else what is cut weighs nothing)
         }
         if (!cut_k && by_p) f = find(false, share_up(top_p, total_mass));
-        if (f.bin >= 0 && (u64)f.count + f.in <= LIST) {
-            // ---- a list of everything down to the border's bin: the first CTA does the rest ----
-            gather(Scale::spot_of(0), Scale::spot_of(f.bin), sh.list, sh.listed[3], LIST);
-            if (rank == 0) finish(sh.list, sh.inner, (int)(f.count + f.in), cut_k, total_mass);
+        if (f.bin >= 0 && (u64)f.count + f.in <= RANKED) {
+            // ---- few candidates down to the border's bin: the first CTA does the rest ----
+            gather(Scale::spot_of(0), Scale::spot_of(f.bin), sh.listed[1], RANKED);
+            if (rank == 0) finish((int)(f.count + f.in), cut_k, total_mass);
             return;
         }
         // ---- the border's value alone ----
         u64 equals = ~0ull;       // of the border's own equals: this many
         u64 ties = 0;             // there are so many of them
         u64 kept_mass = total_mass;
+        // (first CTA) a bin's list in order, with sums up to each: the border's key, how many of its equals are kept, how many there
+        // are, and the weight of all that is kept
+        auto ordered = [&](auto halves, const Found &g, bool counts, u64 least, u64(&got)[4]) {
+            constexpr int H = decltype(halves)::value;
+            const int m = (int)g.in;
+            u64 v[H], sums[H], all, run = g.mass;
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const int i = threadIdx.x + h * THREADS;
+                v[h] = i < m ? sh.list[i] : ~0ull;
+            }
+            int size = 2;
+            while (size < m) size *= 2;
+            sort<H>(sh.list, v, size);
+            int short_of = 0;  // elements that are not enough: the next one is the border's
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const int i = threadIdx.x + h * THREADS;
+                const u64 own = i < m && by_p ? sc.weight_of(sh.weight, by_key(v[h])) : 0;
+                sums[h] = run + block_scan(sh, own, all);
+                run += all;
+                short_of += __syncthreads_count(i < m && (counts ? g.count + i + 1 < least : sums[h] < least));
+            }
+            const int at = min(short_of, m - 1);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const int i = threadIdx.x + h * THREADS;
+                if (i == at) sh.found = {0, ~(uint32_t)(v[h] >> 32), 0, sums[h]};
+            }
+            __syncthreads();
+            got[0] = sh.found.count;
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const int i = threadIdx.x + h * THREADS;
+                const bool same = i < m && ~(uint32_t)(v[h] >> 32) == (uint32_t)got[0];
+                got[1] += __syncthreads_count(same && i <= at);
+                got[2] += __syncthreads_count(same);
+            }
+            got[3] = sh.found.mass;
+        };
         // border, equals, ties from the bin where it falls: `least` elements from the row's first (or weight); returns the weight
         // of all that is kept
-        auto refine = [&](const Found &g, bool counts, u64 least, u64 *list, uint32_t room, uint32_t &listed) -> u64 {
-            if (g.in <= room) {
-                gather(Scale::spot_of(g.bin), Scale::spot_of(g.bin), list, listed, room);
+        auto refine = [&](const Found &g, bool counts, u64 least, uint32_t &listed) -> u64 {
+            if (g.in <= LIST) {
+                gather(Scale::spot_of(g.bin), Scale::spot_of(g.bin), listed, LIST);
                 u64 got[4] = {};
                 if (rank == 0) {
-                    const int m = (int)g.in;
-                    sort_list(list, m);
-                    u64 sums[EACH];
-                    bool is[EACH];
-                    if (by_p) list_sums(list, m, by_key, sums);
-                    else
-                        for (int j = 0; j < EACH; ++j) sums[j] = 0;
-                    int at = (int)(least - g.count) - 1;
-                    if (!counts) {
-#pragma unroll
-                        for (int j = 0; j < EACH; ++j)
-                            is[j] = (int)threadIdx.x * EACH + j < m && g.mass + sums[j] >= least;
-                        at = first_where(m - 1, is);
-                    }
-                    const uint32_t k = ~(uint32_t)(list[at] >> 32);
-                    u64 same = 0;
-#pragma unroll
-                    for (int j = 0; j < EACH; ++j) {
-                        const int i = threadIdx.x * EACH + j;
-                        is[j] = i < m && ~(uint32_t)(list[i] >> 32) == k;
-                        same += is[j];
-                        if (i == at) sh.found.mass = sums[j];
-                    }
-                    got[0] = k;
-                    got[1] = (u64)(at - first_where(at, is) + 1);
-                    got[2] = block_sum(sh, same);
-                    got[3] = g.mass + sh.found.mass;
+                    if (g.in <= THREADS) ordered(std::integral_constant<int, 1>(), g, counts, least, got);
+                    else ordered(std::integral_constant<int, 2>(), g, counts, least, got);
                 }
                 u64(*x)[4] = exchange(got[0], got[1], got[2], got[3]);
                 border = (uint32_t)x[0][0], equals = x[0][1], ties = x[0][2];
@@ -828,14 +795,14 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
             equals = min(equals, ties);
             return m + equals * w;
         };
-        if (cut_k) kept_mass = refine(f, true, (u64)top_k, by_p ? sh.inner : sh.list, by_p ? INNER : LIST, sh.listed[1]);  // (the list takes the histogram's place)
+        if (cut_k) kept_mass = refine(f, true, (u64)top_k, sh.listed[2]);
         if (by_p) {
             const u64 want = share_up(top_p, kept_mass);
             const uint32_t k_border = border;
             const u64 k_equals = equals, k_ties = ties;
             const Found g = cut_k ? find(false, want) : f;
             if (g.bin >= 0 && !(cut_k && g.bin > f.bin)) {
-                refine(g, false, want, sh.list, LIST, sh.listed[2]);
+                refine(g, false, want, sh.listed[3]);
                 if (cut_k && border < k_border) border = k_border, equals = k_equals, ties = k_ties;
                 else if (cut_k && border == k_border) equals = min(equals, k_equals);
             }
@@ -895,6 +862,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const Args a, int pa
     u64 mine = 0, all;
     if (last == INT32_MAX)
         each4([&](int, const float(&l)[4]) {
+            if (fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) < value) return;
             int b[4];
             u64 w[4];
             sc.weigh(sh.weight, l, b, w);

@@ -65,7 +65,7 @@ def test_mixed_settings(cuda_lib, V, dtype):
     check(cuda_lib, l, u, **settings(B, V + 1))
 
 
-@pytest.mark.parametrize("B,V", [(1, 50), (1, 131072), (2, 70001), (3, 393216), (300, 3000), (700, 999)])
+@pytest.mark.parametrize("B,V", [(1, 50), (1, 131072), (2, 70001), (3, 368640), (300, 3000), (700, 999)])
 @pytest.mark.parametrize("peak", [False, True])
 def test_batches(cuda_lib, B, V, peak):
     l, u = rows(B, V, B + V, peak=peak)

@@ -30,7 +30,7 @@ def test_matmul_arguments(i, v):
     _refused(pqe.load().fp8_block_matmul, [A, 128, A, A, A, 2, 64, 128, A, 64, 1, A, None], i, v)
 
 
-@pytest.mark.parametrize("i,v", [(0, None), (0, A + 2), (2, 99), (3, -1), (4, 0), (4, 393217), (5, A + 2), (6, A + 1), (7, A + 2), (8, A + 3), (9, None),
+@pytest.mark.parametrize("i,v", [(0, None), (0, A + 2), (2, 99), (3, -1), (4, 0), (4, 368641), (5, A + 2), (6, A + 1), (7, A + 2), (8, A + 3), (9, None),
                                  (9, A + 2), (10, None), (10, A + 1), (11, A + 2), (12, None), (12, A + 2)])
 def test_sample_arguments(i, v):
     _refused(pqe.load().sample_tokens, [A, 1, 100, 2, 100, None, None, None, None, A, A, None, A, None], i, v)
