@@ -478,12 +478,17 @@ def _blocks(n: int) -> int:
     return -(-n // 128)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _on_device(*tensors):
     """Every tensor lies on the current CUDA device, whose streams the call uses."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    dev = tensors[0].get_device()  # -1 on the CPU
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
+        if t is not None and (t.get_device() != dev or dev < 0):
             raise ValueError(f"expected tensors on the current CUDA device, got one on {t.device}")
+    if dev != _current_device():
+        raise ValueError(f"expected tensors on the current CUDA device, got them on {tensors[0].device}")
 
 
 def _matrix(t: torch.Tensor, name: str) -> tuple[int, int]:

@@ -1,16 +1,21 @@
 // fp8_matmul.cuh -- what the kernels of fp8_block_matmul share (internal).
 #pragma once
 
+#include "f32x2.cuh"
 #include "pqe_common.cuh"
 #include "tc_ptx.cuh"
 
 namespace pqe {
 namespace fp8mm {
+using namespace f32x2;
 using ptx::cluster_rank;
 using ptx::cluster_sync;
 using ptx::map_rank;
 
 constexpr int BK = 128;  // values (bytes) of K in a scale block, and in a stage
+// polls of a wait for what the CTA itself has under way before it ends (some 20 ms: copies and MMAs take microseconds). Whatever
+// limit other waits have, a CTA does not leave its shared memory and TMEM to them.
+constexpr uint32_t DRAIN = 1u << 16;
 
 struct Args {
     const float *xs, *ws;  // scales [M, kb], [ceil(N / 128), kb]
@@ -66,24 +71,6 @@ int launch_clusters(void (*kern)(KArgs...), unsigned grid, unsigned block, size_
 // instruction descriptor, kind::f8f6f4: D fp32, A and B E4M3, both K-major
 __host__ __device__ constexpr uint32_t idesc(int m, int n) {
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
-}
-
-__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-    return r;
-}
-__device__ __forceinline__ uint64_t pair(float lo, float hi) { return pair(__float_as_uint(lo), __float_as_uint(hi)); }
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-// a * b + c of two fp32 pairs
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
 }
 
 // waits for this thread's TMEM loads; the registers pass through it, so that nothing is computed from them before

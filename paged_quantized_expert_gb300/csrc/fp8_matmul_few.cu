@@ -29,7 +29,7 @@ struct Few {
     static constexpr int PART_OFF = STAGES * STAGE;            // [column / 4][128 rows][4]: what the CTAs of a tile send
     static constexpr int SCALE_OFF = PART_OFF + 128 * BN * 4;  // [2][GROUP][BN]
     static constexpr int BAR_OFF = SCALE_OFF + 2 * GROUP * BN * 4;
-    static constexpr int TMEM_OFF = BAR_OFF + 8 * (2 * STAGES + 5);
+    static constexpr int TMEM_OFF = BAR_OFF + 8 * (2 * STAGES + 6);
     static constexpr int SMEM = TMEM_OFF + 16 + 1024;          // + room to align to 1024
     static_assert(SMEM <= 113 * 1024, "shared memory of two CTAs");
 };
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
     const uint32_t bar_full = sbase + L::BAR_OFF, bar_empty = bar_full + 8 * L::STAGES;
-    const uint32_t bar_tfull = bar_empty + 8 * L::STAGES, bar_tempty = bar_tfull + 16, bar_parts = bar_tempty + 16;
+    const uint32_t bar_tfull = bar_empty + 8 * L::STAGES, bar_tempty = bar_tfull + 16, bar_parts = bar_tempty + 16, bar_done = bar_parts + 8;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::TMEM_OFF);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // a cluster of 2^parts_log CTAs an item, or (one) items one after another; items of one weight tile are neighbours
@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
             mbar_init(bar_tfull + 8 * b, 1);
             mbar_init(bar_tempty + 8 * b, FEW_EPI / 32);
         }
+        mbar_init(bar_done, 1);
         mbar_init(bar_parts, 1);
         mbar_expect_tx(bar_parts, BN * 512);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
             }
             if (!ok) atomicOr(a.status, PQE_STATUS_TIMEOUT);
             for (int j = it > L::STAGES ? it - L::STAGES : 0; j < it; ++j)  // what was issued last has landed
-                mbar_wait(bar_full + 8 * (j % L::STAGES), (uint32_t)(j / L::STAGES) & 1u, a.wait_limit);
+                mbar_wait(bar_full + 8 * (j % L::STAGES), (uint32_t)(j / L::STAGES) & 1u, DRAIN);
         }
     } else if (warp == 1) {
         const uint32_t one = elect();
@@ -133,8 +134,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
                 commit<1>(one, bar_tfull + 8 * b);
             }
         if (!ok && lane == 0) atomicOr(a.status, PQE_STATUS_TIMEOUT);
-        if (it)  // the MMAs are done before TMEM goes
-            mbar_wait(bar_tfull + 8 * ((it - 1) & 1), (uint32_t)((it - 1) >> 1) & 1u, a.wait_limit);
+        commit<1>(one, bar_done);  // the MMAs are done before TMEM goes
+        mbar_wait(bar_done, 0, DRAIN);
     } else {
         const int q = warp & 3, n_at = 32 * q + lane, et = threadIdx.x - 64;
         float *scales = reinterpret_cast<float *>(smem + L::SCALE_OFF);
@@ -215,8 +216,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
                              "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(map_rank(bar_parts, to))
                              : "memory");
             }
-            if (!mbar_wait_cluster(bar_parts, 0, limit)) {
-                limit = 1;
+            // (every CTA sends its parts, also one whose waits expired: none leaves before all have come)
+            if (!mbar_wait_cluster(bar_parts, 0, max(a.wait_limit, DRAIN))) {
+                late = true;
                 atomicOr(a.status, PQE_STATUS_TIMEOUT);
             }
             const int m1 = m0 + rank * own;
@@ -229,13 +231,12 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
                 if (n < a.N) put4(a, (int64_t)(m1 + c) * a.out_stride + n, min(4, a.M - m1 - c), v);
             }
         }
-        late = limit != a.wait_limit;
     }
     __syncwarp();
     if (parts_log && warp < 2) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     tc_fence_before();
     const bool any_late = __syncthreads_or(late);
-    if (parts_log && any_late) cluster_sync();  // what the others send may still come: wait until they are through, or gone
+    if (parts_log && any_late) cluster_sync();  // what the others send may still come: until they are through, or gone
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::TMEM_COLS) : "memory");

@@ -43,7 +43,7 @@ struct Many {
     static constexpr int SLOTS = 2 * NBUF, SLOT = 128 + 4;
     static constexpr int SCALE_OFF = OUT_OFF + EPI_WARPS * NOUT * BUF;
     static constexpr int BAR_OFF = SCALE_OFF + SLOTS * SLOT * 4;
-    static constexpr int TMEM_OFF = BAR_OFF + 8 * (2 * STAGES + 2 * NBUF);
+    static constexpr int TMEM_OFF = BAR_OFF + 8 * (2 * STAGES + 2 * NBUF + 1);
     static constexpr int SMEM = TMEM_OFF + 16;
     static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
 };
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     uint32_t sbase;  // in a register: as a constant it is put together anew for every descriptor (126 us against 122)
     asm volatile("mov.u32 %0, %1;" : "=r"(sbase) : "r"(smem_u32(smem)));
     const uint32_t bar_full = sbase + L::BAR_OFF, bar_empty = bar_full + 8 * L::STAGES;
-    const uint32_t bar_tfull = bar_empty + 8 * L::STAGES, bar_tempty = bar_tfull + 8 * L::NBUF;
+    const uint32_t bar_tfull = bar_empty + 8 * L::STAGES, bar_tempty = bar_tfull + 8 * L::NBUF, bar_done = bar_tempty + 8 * L::NBUF;
     float *scales = reinterpret_cast<float *>(smem + L::SCALE_OFF);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::TMEM_OFF);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
             mbar_init(bar_full + 8 * s, 1);   // the first CTA's: its own arrival, and the bytes of both
             mbar_init(bar_empty + 8 * s, 1);  // each CTA's: the commit of the MMAs that read the stage
         }
+        mbar_init(bar_done, 1);  // each CTA's: the last commit
         for (int b = 0; b < L::NBUF; ++b) {
             mbar_init(bar_tfull + 8 * b, 3);               // each CTA's: the commit, and its two scale warps
             mbar_init(bar_tempty + 8 * b, CTAS * EPI_WARPS);  // the first CTA's: the epilogue warps of both
@@ -132,10 +133,15 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
                     tma_load<CTAS>(at + L::A_BYTES, &tmW, kb * BK, n0, bar);
                 }
             }
-            if (!ok) atomicOr(a.status, PQE_STATUS_TIMEOUT);
-            if (rank == 0)  // what both issued last has landed
-                for (int j = it > L::STAGES ? it - L::STAGES : 0; j < it; ++j)
-                    mbar_wait(bar_full + 8 * (j % L::STAGES), (uint32_t)(j / L::STAGES) & 1u, a.wait_limit);
+            if (!ok) {
+                // no MMA may have waited for what was issued last: it lands (the pair's on the first CTA's barriers, some of it
+                // perhaps on none that is armed: hence the pause)
+                atomicOr(a.status, PQE_STATUS_TIMEOUT);
+                if (rank == 0)
+                    for (int j = it > L::STAGES ? it - L::STAGES : 0; j < it; ++j)
+                        mbar_wait(bar_full + 8 * (j % L::STAGES), (uint32_t)(j / L::STAGES) & 1u, DRAIN);
+                for (int j = 0; j < 200; ++j) __nanosleep(1000);
+            }
         }
         if (warp >= SCALE_WARP0) {
             // x's scales of 64 rows and one of W's, fetched a group of blocks ahead
@@ -195,8 +201,9 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
                     commit<CTAS>(one, bar_tfull + 8 * b);
                 }
             if (!ok && lane == 0) atomicOr(a.status, PQE_STATUS_TIMEOUT);
-            if (it)  // the MMAs are done before TMEM goes
-                mbar_wait(bar_tfull + 8 * ((it - 1) % L::NBUF), (uint32_t)((it - 1) / L::NBUF) & 1u, a.wait_limit);
+            if (!ok)  // what it did not wait for lands before the CTAs end
+                for (int j = 0; j < 200; ++j) __nanosleep(1000);
+            commit<CTAS>(one, bar_done);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
@@ -313,7 +320,9 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     __syncwarp();
     tc_fence_before();
     if (CTAS == 1) __syncthreads();
-    else cluster_sync();  // neither CTA goes while the other's MMAs, loads or arrivals may still reach it
+    else cluster_sync();  // neither CTA goes while the other's loads or arrivals may still reach it
+    if (warp == 1) mbar_wait(bar_done, 0, DRAIN);  // nor before the MMAs are done, and have said so to both
+    __syncwarp();
     if (warp == 1) {
         tc_fence_after();
         if constexpr (CTAS == 2)

@@ -20,27 +20,38 @@ struct RowArgs {
     float *scale;
 };
 
-constexpr int ROW_THREADS = 256;
+// A CTA takes 64 blocks in a row (of one row of x after the other), four of each sixteen lanes, all loads first.
+constexpr int ROW_THREADS = 256, EACH = 4, TAKEN = ROW_THREADS / 16 * EACH;
 __global__ void __launch_bounds__(ROW_THREADS) quantize_rows_kernel(const RowArgs a) {
     const int lane = threadIdx.x & 15;
-    const int64_t units = (int64_t)a.T * a.blocks, step = (int64_t)gridDim.x * (ROW_THREADS / 16);
+    const int64_t units = (int64_t)a.T * a.blocks, u0 = (int64_t)blockIdx.x * TAKEN, row0 = u0 / a.blocks;
+    const uint32_t b0 = (uint32_t)(u0 - row0 * a.blocks) + (threadIdx.x >> 4);
     pdl_acquire();
-    // both halves of a warp run as often: the shuffles need all lanes
-    for (int64_t u0 = (int64_t)blockIdx.x * (ROW_THREADS / 16) + (threadIdx.x >> 5) * 2; u0 < units; u0 += step) {
-        const int64_t u = u0 + (threadIdx.x >> 4 & 1);
-        const int64_t row = u / a.blocks;
-        const int b = (int)(u - row * a.blocks), i = b * BLOCK + lane * 8;
-        const bool on = u < units && i < a.H;
-        float f[8] = {};
-        if (on) unpack8(*reinterpret_cast<const uint4 *>(a.x + row * a.x_stride + i), f);
+    uint4 x[EACH];
+    bool on[EACH];
+#pragma unroll
+    for (int j = 0; j < EACH; ++j) {
+        const uint32_t b = b0 + j * (ROW_THREADS / 16), down = b / (uint32_t)a.blocks;
+        const int i = (int)(b - down * a.blocks) * BLOCK + lane * 8;
+        on[j] = row0 + down < a.T && i < a.H;
+        x[j] = make_uint4(0, 0, 0, 0);
+        if (on[j]) x[j] = *reinterpret_cast<const uint4 *>(a.x + (row0 + down) * a.x_stride + i);
+    }
+#pragma unroll
+    for (int j = 0; j < EACH; ++j) {
+        const int64_t u = u0 + (threadIdx.x >> 4) + j * (ROW_THREADS / 16);
+        if (u0 + (threadIdx.x >> 5) * 2 + j * (ROW_THREADS / 16) >= units) break;  // the whole warp: the shuffles need all lanes
+        float f[8];
+        unpack8(x[j], f);
         uint32_t t = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) t = max(t, abs_bits(f[e]));
 #pragma unroll
         for (int o = 1; o < 16; o *= 2) t = max(t, __shfl_xor_sync(0xffffffffu, t, o));
-        if (!on) continue;
-        const float s = scale_of(t);
-        *reinterpret_cast<uint2 *>(a.q + row * a.H + i) = codes8(f, s);
+        if (!on[j]) continue;
+        float s;
+        const uint32_t b = b0 + j * (ROW_THREADS / 16), down = b / (uint32_t)a.blocks;
+        *reinterpret_cast<uint2 *>(a.q + (row0 + down) * a.H + (b - down * a.blocks) * BLOCK + lane * 8) = codes8_block(f, t, s);
         if (lane == 0) a.scale[u] = s;
     }
 }
@@ -75,15 +86,11 @@ int fp8_block_quantize(const void *x, int64_t x_stride, int T, int H, uint8_t *q
     if (T == 0) return PQE_OK;
     PQE_CHECK_ARG(x && q && scale && x_stride >= H && x_stride % 8 == 0);
     PQE_CHECK_ARG(aligned(x, 16) && aligned(q, 16) && aligned(scale, 4));
-    int dev = 0, sms = 0;
-    const int rc = device_info(dev, sms);
-    if (rc != PQE_OK) return rc;
     const int blocks = (H + fp8::BLOCK - 1) / fp8::BLOCK;
     const fp8::RowArgs a{static_cast<const uint16_t *>(x), x_stride, T, H, blocks, q, scale};
-    const int64_t ctas = ((int64_t)T * blocks + fp8::ROW_THREADS / 16 - 1) / (fp8::ROW_THREADS / 16);
-    const int64_t most = 8 * (int64_t)sms;
-    return launch_pdl(fp8::quantize_rows_kernel, dim3((unsigned)(ctas < most ? ctas : most)), dim3(fp8::ROW_THREADS), 0,
-                      as_stream(stream), a);
+    const int64_t ctas = ((int64_t)T * blocks + fp8::TAKEN - 1) / fp8::TAKEN;
+    PQE_CHECK_ARG(ctas <= INT32_MAX);
+    return launch_pdl(fp8::quantize_rows_kernel, dim3((unsigned)ctas), dim3(fp8::ROW_THREADS), 0, as_stream(stream), a);
 }
 
 int pqe_quantize_fp8_blocks(const float *w, int rows, int cols, uint8_t *q, float *scale, void *stream) {

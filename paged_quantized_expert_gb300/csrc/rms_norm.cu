@@ -139,8 +139,8 @@ struct Part {
 #pragma unroll
             for (int o = 1; o < 16; o *= 2) t = max(t, __shfl_xor_sync(0xffffffffu, t, o));
             if (i >= nv) continue;
-            const float s = scale_of(t);
-            reinterpret_cast<uint2 *>(a.q + (size_t)row * a.H)[i] = codes8(h[j], s);
+            float s;
+            reinterpret_cast<uint2 *>(a.q + (size_t)row * a.H)[i] = codes8_block(h[j], t, s);
             if (i % 16 == 0) static_cast<float *>(a.q_scale)[(size_t)row * ((a.H + 127) / 128) + i / 16] = s;
         }
     }

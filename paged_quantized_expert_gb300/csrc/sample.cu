@@ -22,12 +22,14 @@
 #include <atomic>
 #include <type_traits>
 
+#include "f32x2.cuh"
 #include "pqe_common.cuh"
 #include "tc_ptx.cuh"
 
 namespace pqe {
 namespace sampling {
 using namespace ptx;
+using namespace f32x2;
 typedef unsigned long long u64;
 
 struct Args {
@@ -102,34 +104,6 @@ struct Shared {
         u64 spare[RANKED];            // at the end
     };
 };
-
-// two fp32 operations in one instruction
-__device__ __forceinline__ u64 pair(float x, float y) {
-    u64 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ u64 pair(float x) { return pair(x, x); }
-__device__ __forceinline__ float2 unpair(u64 v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
-    u64 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ u64 add2(u64 a, u64 b) {
-    u64 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
-    u64 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 
 // What a row's weights go by.
 constexpr float MAGIC = 12582912.f;  // 1.5 * 2^23: a number added to it is rounded to a whole one
