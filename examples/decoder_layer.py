@@ -1,16 +1,25 @@
-"""One decoder layer in a serving loop: attention over a 4-bit paged KV cache, then the paged MoE expert layer.
+"""One decoder layer in a serving loop: attention over a 4-bit paged KV cache, the paged MoE expert layer, and the next token.
 
 A step takes the tokens that are new (prompts, or one token a sequence) through
 
-    add_rms_norm        residual addition and norm, E4M3 codes with a scale a row
-    q|k|v projection    on those codes (a plain product; the library has none of its own)
+    add_rms_norm        residual addition and norm, E4M3 codes with a scale for each 128 values
+    fp8_block_matmul    the q|k|v projection on those codes
     kv_cache_write      K and V rows, quantised into the sequences' pages
     kv_paged_attention  over everything cached so far
-    output projection
+    fp8_block_quantize  its rows as codes
+    fp8_block_matmul    the output projection
     add_rms_norm        residual addition and norm, bf16 for the expert layer
     PagedMoELayer.step  route, permute, refill, expert FFN, combine
 
-    python examples/decoder_layer.py [--sequences 8] [--prompt 300] [--steps 32]
+and the sequences' last tokens through
+
+    add_rms_norm        residual addition and norm, codes
+    fp8_block_matmul    fp32 logits over the vocabulary
+    sample_tokens       the next token of each
+
+(A layer without block scales takes codes with a scale a row through a plain product.)
+
+    python examples/decoder_layer.py [--sequences 8] [--prompt 300] [--steps 32] [--vocabulary 32000]
 """
 from __future__ import annotations
 
@@ -58,11 +67,36 @@ class Sequences:
         self.tables[b], self.lens[b] = [], 0
 
 
+def blocks(n: int) -> int:
+    return -(-n // 128)
+
+
+def codes_of(shape, device) -> tuple[torch.Tensor, torch.Tensor]:
+    """Room for the E4M3 codes of rows and a scale for each 128 values."""
+    return (torch.empty(shape, dtype=torch.float8_e4m3fn, device=device),
+            torch.empty((shape[0], blocks(shape[1])), dtype=torch.float32, device=device))
+
+
+class BlockLinear:
+    """y = x W^T with W [n, k] in E4M3 with a scale for each 128 x 128 tile, x in codes with one for each 128 values."""
+
+    def __init__(self, w: torch.Tensor):
+        n, k = w.shape
+        self.q = torch.empty((n, k), dtype=torch.float8_e4m3fn, device=w.device)
+        self.scale = torch.empty((blocks(n), blocks(k)), dtype=torch.float32, device=w.device)
+        pqe.pqe_quantize_fp8_blocks(w, self.q, self.scale)
+
+    def __call__(self, codes, scale, status, dtype=torch.bfloat16):
+        y = torch.empty((codes.shape[0], self.q.shape[0]), dtype=dtype, device=codes.device)
+        pqe.fp8_block_matmul(codes, scale, self.q, self.scale, y, status)
+        return y
+
+
 class DecoderLayer:
     """Random weights of one decoder layer, its KV cache and its expert layer."""
 
     def __init__(self, H=2048, n_q=16, n_kv=4, d=128, E=16, I=512, k=4, n_pages=1024, page_size=64, max_tokens=4096, window=0,
-                 seed=0, device="cuda"):
+                 seed=0, device="cuda", block_fp8=False):
         g = torch.Generator(device=device).manual_seed(seed)
         rand = lambda *s: torch.randn(s, generator=g, device=device)  # noqa: E731
         self.H, self.n_q, self.n_kv, self.d, self.window, self.device = H, n_q, n_kv, d, window, device
@@ -74,6 +108,8 @@ class DecoderLayer:
         self.wqkv_scale = torch.empty(w.shape[0], dtype=torch.float32, device=device)
         pqe.pqe_quantize_fp8_rows(w, self.wqkv, self.wqkv_scale)
         self.wo = (rand(H, n_q * d) * (n_q * d) ** -0.5).bfloat16()
+        # with block scales: both projections on codes
+        self.qkv, self.out = (BlockLinear(w), BlockLinear(self.wo.float())) if block_fp8 else (None, None)
         self.w_router = rand(E, H) * 0.02
         stride = pqe.slot_stride(H, I)
         host = torch.zeros((E, stride), dtype=torch.uint8).pin_memory()
@@ -87,18 +123,22 @@ class DecoderLayer:
         self.ws = torch.empty(0, dtype=torch.uint8, device=device)
 
     def project(self, codes, scale):
-        """x W^T of E4M3 codes with row scales on both sides. E4M3 values are exact in bf16; a library product that takes the
-        codes and scales as they are does the same."""
+        """x W^T of E4M3 codes with row scales on both sides. E4M3 values are exact in bf16."""
         y = codes.bfloat16() @ self.wqkv.view(torch.float8_e4m3fn).bfloat16().T
         return (y.float() * scale[:, None] * self.wqkv_scale).bfloat16()
 
     def attention(self, delta, residual, step):
         """norm, projection, cache write, attention, output projection; residual += delta in place. Returns the new delta."""
         T = step["total"]
-        codes = torch.empty((T, self.H), dtype=torch.float8_e4m3fn, device=self.device)
-        scale = torch.empty(T, dtype=torch.float32, device=self.device)
-        pqe.add_rms_norm(delta, residual, self.norm1, 1e-6, residual, None, codes, scale, pqe.PQE_Q8_ROW)
-        heads = self.project(codes, scale).view(T, self.n_q + 2 * self.n_kv, self.d)
+        codes, scale = codes_of((T, self.H), self.device)
+        if self.qkv:
+            pqe.add_rms_norm(delta, residual, self.norm1, 1e-6, residual, None, codes, scale, pqe.PQE_Q8_B128)
+            heads = self.qkv(codes, scale, self.status)
+        else:
+            scale = torch.empty(T, dtype=torch.float32, device=self.device)
+            pqe.add_rms_norm(delta, residual, self.norm1, 1e-6, residual, None, codes, scale, pqe.PQE_Q8_ROW)
+            heads = self.project(codes, scale)
+        heads = heads.view(T, self.n_q + 2 * self.n_kv, self.d)
         q, k, v = heads.split([self.n_q, self.n_kv, self.n_kv], 1)  # views into the fused rows
         pqe.kv_cache_write(self.cache, k, v, step["slots"], self.status)
         need = pqe.kv_paged_attention_workspace_size(len(step["kv_lens"]), T, step["max_q"], self.n_q, self.n_kv, self.d)
@@ -107,7 +147,11 @@ class DecoderLayer:
         out = torch.empty((T, self.n_q, self.d), dtype=torch.bfloat16, device=self.device)
         pqe.kv_paged_attention(self.cache, q, step["q_offsets"], step["kv_lens"], step["block_table"], step["max_q"], self.scale,
                                out, self.ws, self.status, window=self.window)
-        return out.flatten(1) @ self.wo.T
+        if not self.out:
+            return out.flatten(1) @ self.wo.T
+        codes, scale = codes_of((T, self.n_q * self.d), self.device)
+        pqe.fp8_block_quantize(out.flatten(1), codes, scale)
+        return self.out(codes, scale, self.status)
 
     def experts(self, delta, residual):
         """norm and expert layer; residual += delta in place. Returns the new delta."""
@@ -122,35 +166,68 @@ class DecoderLayer:
         return self.experts(delta, residual)
 
 
+class Vocabulary:
+    """Random weights of what follows the last layer: the final norm, the product with the vocabulary, and sampling."""
+
+    def __init__(self, H: int, V: int, seed=0, device="cuda"):
+        g = torch.Generator(device=device).manual_seed(seed)
+        self.norm = (1 + 0.1 * torch.randn(H, generator=g, device=device)).bfloat16()
+        self.head = BlockLinear(torch.randn((V, H), generator=g, device=device) * 3 * H ** -0.5)
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def logits(self, delta, residual):
+        codes, scale = codes_of(delta.shape, delta.device)
+        pqe.add_rms_norm(delta, residual, self.norm, 1e-6, None, None, codes, scale, pqe.PQE_Q8_B128)
+        return self.head(codes, scale, self.status, torch.float32)
+
+    def __call__(self, delta, residual, u, **settings):
+        """The next token of each row, and what it was drawn with (its logarithm)."""
+        tokens = torch.empty(delta.shape[0], dtype=torch.int32, device=delta.device)
+        logprobs = torch.empty(delta.shape[0], dtype=torch.float32, device=delta.device)
+        pqe.sample_tokens(self.logits(delta, residual), u, tokens, self.status, logprobs=logprobs, **settings)
+        return tokens, logprobs
+
+
 def main(argv=None) -> dict:
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--sequences", type=int, default=8)
     ap.add_argument("--prompt", type=int, default=300)
     ap.add_argument("--steps", type=int, default=32)
+    ap.add_argument("--vocabulary", type=int, default=32000)
     a = ap.parse_args(argv)
-    tokens = a.sequences * (a.prompt + a.steps)
-    layer = DecoderLayer(n_pages=a.sequences * (-(-(a.prompt + a.steps) // 64)), max_tokens=max(a.sequences * a.prompt, 64))
-    seqs = Sequences(a.sequences, layer.cache.n_pages, 64, a.prompt + a.steps)
+    n = a.sequences
+    layer = DecoderLayer(n_pages=n * (-(-(a.prompt + a.steps) // 64)), max_tokens=max(n * a.prompt, 64), block_fp8=True)
+    last = Vocabulary(layer.H, a.vocabulary)
+    seqs = Sequences(n, layer.cache.n_pages, 64, a.prompt + a.steps)
     g = torch.Generator(device="cuda").manual_seed(1)
+    embed = torch.randn((a.vocabulary, layer.H), generator=g, device="cuda").bfloat16()
+    # the even sequences take the likeliest token, the odd ones draw theirs
+    odd = torch.arange(n, device="cuda") % 2
+    settings = {"temperature": odd * 0.8, "top_p": torch.full((n,), 0.95, device="cuda"), "top_k": torch.full((n,), 50, dtype=torch.int32, device="cuda")}
 
-    def step(new):
-        s = seqs.extend([new] * a.sequences)
-        delta = torch.randn((s["total"], layer.H), generator=g, device="cuda").bfloat16()
-        residual = torch.randn((s["total"], layer.H), generator=g, device="cuda").bfloat16()
-        return layer(delta, residual, s)
+    def step(tokens, new):
+        s = seqs.extend([new] * n)
+        residual = torch.zeros((s["total"], layer.H), dtype=torch.bfloat16, device="cuda")
+        delta = layer(embed[tokens], residual, s)
+        at = torch.arange(1, n + 1, device="cuda") * new - 1
+        return last(delta[at], residual[at], torch.rand(n, generator=g, device="cuda"), **settings)
 
-    step(a.prompt)
+    tokens, _ = step(torch.randint(0, a.vocabulary, (n * a.prompt,), generator=g, device="cuda"), a.prompt)
     torch.cuda.synchronize()
     t = time.perf_counter()
+    made = [tokens]
     for _ in range(a.steps):
-        out = step(1)
+        tokens, logprobs = step(tokens.long(), 1)
+        made.append(tokens)
     torch.cuda.synchronize()
     t = (time.perf_counter() - t) / max(a.steps, 1)
-    ok = layer.status.item() == 0 and bool(torch.isfinite(out).all())
-    print(f"{tokens} tokens through one layer; a step of {a.sequences} tokens takes {t * 1e6:.0f} us; "
-          f"{'ok' if ok else 'FAILED'} (status {layer.status.item()})")
+    made = torch.stack(made, 1)
+    status = layer.status.item() | last.status.item()
+    ok = status == 0 and bool((made >= 0).all()) and bool(torch.isfinite(logprobs).all())
+    print(f"{n * (a.prompt + a.steps)} tokens through one layer; a step of {n} tokens takes {t * 1e6:.0f} us; "
+          f"the first sequence's next tokens {made[0, :8].tolist()}; {'ok' if ok else 'FAILED'} (status {status})")
     layer.moe.close()
-    return {"ok": ok, "step_s": t}
+    return {"ok": ok, "step_s": t, "tokens": made}
 
 
 if __name__ == "__main__":
