@@ -15,44 +15,51 @@ constexpr int BLOCK = 128;
 struct RowArgs {
     const uint16_t *x;
     int64_t x_stride;
-    int T, H, blocks;
+    int T, H;
+    uint32_t blocks, part;  // blocks a row, and 2^24 / blocks rounded up
     uint8_t *q;
     float *scale;
 };
 
-// A CTA takes 64 blocks in a row (of one row of x after the other), four of each sixteen lanes, all loads first.
-constexpr int ROW_THREADS = 256, EACH = 4, TAKEN = ROW_THREADS / 16 * EACH;
+// A CTA takes 64 blocks in a row (of one row of x after the other), four of each sixteen lanes, all loads first. Sixty-four times
+// `blocks` of them are 64 rows, so CTA n starts n / blocks * 64 rows down, and what is left is
+// below 64 * blocks <= 2^14 blocks: the product with the reciprocal, high by less than 2^-10 then, gives the same whole part as
+// the division by up to 256.
+constexpr int ROW_THREADS = 256, EACH = 4, GROUPS = ROW_THREADS / 16, TAKEN = GROUPS * EACH;
 __global__ void __launch_bounds__(ROW_THREADS) quantize_rows_kernel(const RowArgs a) {
     const int lane = threadIdx.x & 15;
-    const int64_t units = (int64_t)a.T * a.blocks, u0 = (int64_t)blockIdx.x * TAKEN, row0 = u0 / a.blocks;
-    const uint32_t b0 = (uint32_t)(u0 - row0 * a.blocks) + (threadIdx.x >> 4);
-    pdl_acquire();
+    const uint32_t whole = blockIdx.x / a.blocks, b0 = (blockIdx.x - whole * a.blocks) * TAKEN + (threadIdx.x >> 4);
+    const int64_t row0 = (int64_t)whole * TAKEN;
     uint4 x[EACH];
     bool on[EACH];
+    int64_t to[EACH];
+    pdl_acquire();
 #pragma unroll
     for (int j = 0; j < EACH; ++j) {
-        const uint32_t b = b0 + j * (ROW_THREADS / 16), down = b / (uint32_t)a.blocks;
+        const uint32_t b = b0 + j * GROUPS, down = (uint32_t)(((uint64_t)b * a.part) >> 24);
         const int i = (int)(b - down * a.blocks) * BLOCK + lane * 8;
         on[j] = row0 + down < a.T && i < a.H;
+        to[j] = (row0 + down) * a.H + i;
         x[j] = make_uint4(0, 0, 0, 0);
         if (on[j]) x[j] = *reinterpret_cast<const uint4 *>(a.x + (row0 + down) * a.x_stride + i);
     }
+    uint32_t t[EACH];
 #pragma unroll
     for (int j = 0; j < EACH; ++j) {
-        const int64_t u = u0 + (threadIdx.x >> 4) + j * (ROW_THREADS / 16);
-        if (u0 + (threadIdx.x >> 5) * 2 + j * (ROW_THREADS / 16) >= units) break;  // the whole warp: the shuffles need all lanes
         float f[8];
         unpack8(x[j], f);
-        uint32_t t = 0;
+        t[j] = top8(f);
+    }
+    float s, inv;
+    block_scale(block_tops(t), s, inv);
+    const int64_t u = row0 * a.blocks + b0 + lane * GROUPS;
+    if (lane < EACH && u < (int64_t)a.T * a.blocks) a.scale[u] = s;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) t = max(t, abs_bits(f[e]));
-#pragma unroll
-        for (int o = 1; o < 16; o *= 2) t = max(t, __shfl_xor_sync(0xffffffffu, t, o));
-        if (!on[j]) continue;
-        float s;
-        const uint32_t b = b0 + j * (ROW_THREADS / 16), down = b / (uint32_t)a.blocks;
-        *reinterpret_cast<uint2 *>(a.q + (row0 + down) * a.H + (b - down * a.blocks) * BLOCK + lane * 8) = codes8_block(f, t, s);
-        if (lane == 0) a.scale[u] = s;
+    for (int j = 0; j < EACH; ++j) {
+        const float sj = __shfl_sync(0xffffffffu, s, j, 16), ij = __shfl_sync(0xffffffffu, inv, j, 16);
+        float f[8];
+        unpack8(x[j], f);
+        if (on[j]) *reinterpret_cast<uint2 *>(a.q + to[j]) = codes8_block(f, sj, ij);
     }
 }
 
@@ -87,7 +94,7 @@ int fp8_block_quantize(const void *x, int64_t x_stride, int T, int H, uint8_t *q
     PQE_CHECK_ARG(x && q && scale && x_stride >= H && x_stride % 8 == 0);
     PQE_CHECK_ARG(aligned(x, 16) && aligned(q, 16) && aligned(scale, 4));
     const int blocks = (H + fp8::BLOCK - 1) / fp8::BLOCK;
-    const fp8::RowArgs a{static_cast<const uint16_t *>(x), x_stride, T, H, blocks, q, scale};
+    const fp8::RowArgs a{static_cast<const uint16_t *>(x), x_stride, T, H, (uint32_t)blocks, ((1u << 24) + blocks - 1) / blocks, q, scale};
     const int64_t ctas = ((int64_t)T * blocks + fp8::TAKEN - 1) / fp8::TAKEN;
     PQE_CHECK_ARG(ctas <= INT32_MAX);
     return launch_pdl(fp8::quantize_rows_kernel, dim3((unsigned)ctas), dim3(fp8::ROW_THREADS), 0, as_stream(stream), a);

@@ -17,6 +17,7 @@
 namespace pqe {
 namespace norm {
 using namespace fp8;
+using namespace f32x2;
 
 struct Args {
     const uint16_t *x, *r, *w;
@@ -33,6 +34,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+__device__ __forceinline__ void set(float (&f)[8], int e, uint64_t v) {
+    const float2 p = unpair(v);
+    f[e] = p.x;
+    f[e + 1] = p.y;
 }
 
 // What a thread (of a warp or a CTA that shares a row) does with its V vectors of eight values, vector j at index
@@ -64,16 +71,17 @@ struct Part {
                 float f[8];
                 unpack8(r[j], f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) h[j][e] += f[e];
+                for (int e = 0; e < 8; e += 2) set(h[j], e, add2(pair(h[j][e], h[j][e + 1]), pair(f[e], f[e + 1])));
             }
             if (a.sum_out)
                 reinterpret_cast<uint4 *>(a.sum_out + (size_t)row * a.H)[i] =
                     make_uint4(pack_bf16(h[j][0], h[j][1]), pack_bf16(h[j][2], h[j][3]), pack_bf16(h[j][4], h[j][5]),
                                pack_bf16(h[j][6], h[j][7]));
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float u = h[j][e] * a.c;  // the sum overflows only where the mean does
-                ss = fmaf(u, u, ss);
+            for (int e = 0; e < 8; e += 2) {
+                const float2 u = unpair(mul2(pair(h[j][e], h[j][e + 1]), pair(a.c)));  // the sum overflows only where the mean does
+                ss = fmaf(u.x, u.x, ss);
+                ss = fmaf(u.y, u.y, ss);
             }
         }
         return ss;
@@ -92,10 +100,9 @@ struct Part {
                 float f[8];
                 unpack8(w[j], f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    h[j][e] = h[j][e] * inv * f[e];
-                    t = max(t, abs_bits(h[j][e]));
-                }
+                for (int e = 0; e < 8; e += 2)
+                    set(h[j], e, mul2(mul2(pair(h[j][e], h[j][e + 1]), pair(inv)), pair(f[e], f[e + 1])));
+                t = top8(h[j]);
                 if (a.y_out)
                     reinterpret_cast<uint4 *>(a.y_out + (size_t)row * a.H)[i] =
                         make_uint4(pack_bf16(h[j][0], h[j][1]), pack_bf16(h[j][2], h[j][3]), pack_bf16(h[j][4], h[j][5]),
@@ -127,21 +134,19 @@ struct Part {
     // the codes with a scale for each 128 values: sixteen neighbouring lanes (the last block may end early). As for
     // scale(), all 32 lanes are here.
     __device__ __forceinline__ void block_codes(const Args &a, int row, int first, int step) {
-        const int nv = a.H / 8;
+        const int nv = a.H / 8, lane = threadIdx.x & 15;
+        uint32_t t[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) t[j] = first + j * step < nv ? top8(h[j]) : 0u;
+        float s, inv;
+        block_scale(block_tops(t), s, inv);
+        const int own = first - lane + lane * step;  // the vector that starts block `lane` of these lanes
+        if (lane < V && own < nv) static_cast<float *>(a.q_scale)[(size_t)row * ((a.H + 127) / 128) + own / 16] = s;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int i = first + j * step;
-            uint32_t t = 0;
-            if (i < nv) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) t = max(t, abs_bits(h[j][e]));
-            }
-#pragma unroll
-            for (int o = 1; o < 16; o *= 2) t = max(t, __shfl_xor_sync(0xffffffffu, t, o));
-            if (i >= nv) continue;
-            float s;
-            reinterpret_cast<uint2 *>(a.q + (size_t)row * a.H)[i] = codes8_block(h[j], t, s);
-            if (i % 16 == 0) static_cast<float *>(a.q_scale)[(size_t)row * ((a.H + 127) / 128) + i / 16] = s;
+            const float sj = __shfl_sync(0xffffffffu, s, j, 16), ij = __shfl_sync(0xffffffffu, inv, j, 16);
+            if (i < nv) reinterpret_cast<uint2 *>(a.q + (size_t)row * a.H)[i] = codes8_block(h[j], sj, ij);
         }
     }
 
