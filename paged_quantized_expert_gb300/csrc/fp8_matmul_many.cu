@@ -218,17 +218,15 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
 #pragma unroll
             for (int c = 0; c < L::CW / 2; ++c) acc[c] = 0;
             constexpr int LD = 4;  // loads under way at a time
-            bool ready = false;  // this block's product, as seen a block earlier
             for (int kb = 0; kb < a.kb; ++kb, ++it) {
                 const int b = it % L::NBUF;
-                if (!ready && !__all_sync(0xffffffffu, mbar_wait(bar_tfull + 8 * b, (uint32_t)(it / L::NBUF) & 1u, a.wait_limit))) {
+                if (!__all_sync(0xffffffffu, mbar_wait(bar_tfull + 8 * b, (uint32_t)(it / L::NBUF) & 1u, a.wait_limit))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t t = t0 + b * BN;
                 const float *slot = scales + it % L::SLOTS * L::SLOT;
-                bool next = false;
                 uint64_t s2;
 #pragma unroll
                 for (int c = 0; c < L::CW; c += 16 * LD) {
@@ -238,9 +236,6 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
                     if (c == 0) {
                         const float s = slot[32 * q + lane] * slot[128 + part * L::CW / 128];
                         s2 = pair(s, s);
-                        // a barrier takes 100 clocks to ask: the next block's, beside this one's loads and sums
-                        const int n = it + 1;
-                        next = false; (void)n;
                     }
 #pragma unroll
                     for (int l = 0; l < LD; ++l) tmem_wait(d[l]);
