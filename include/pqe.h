@@ -764,7 +764,7 @@ PQE_API int fp8_block_quantize(const void *x, int64_t x_stride, int T, int H, ui
 /* pqe_quantize_fp8_blocks -- weights w fp32 [rows, cols] (device) to E4M3 codes
  * q [rows, cols] with one fp32 scale for each 128 x 128 tile, scale
  * [ceil(rows/128), ceil(cols/128)], by the same rule; it prepares weights and
- * is not on the per-step path. rows, cols >= 1. */
+ * is not on the per-step path. 1 <= rows <= 8388480, 1 <= cols <= 2^31 - 128. */
 PQE_API int pqe_quantize_fp8_blocks(const float *w, int rows, int cols, uint8_t *q, float *scale, void *stream);
 
 /* fp8_block_matmul -- out = x W^T:
@@ -806,7 +806,8 @@ PQE_API int fp8_block_matmul(const uint8_t *x, int64_t x_stride, const float *x_
  *   token = the first j, in index order, with sum_{i <= j, kept} w_i > u * sum_kept w
  *   logprob = ln(w_token / sum_kept w), what the token was drawn with
  * t == 0 takes the largest logit, the lower index among equal ones (logprob 0).
- * A logit of -infinity is never kept. Weights enter the sums with 2^-30 of
+ * A t above 0 and below 1e-36 counts as about that in w.
+ * A logit of -infinity is never kept. Weights enter the sums with 2^-29 of
  * their own size and 2^-43 of the largest, the sums are whole numbers: the same
  * in every run and for every row's place in the batch.
  * A row with a NaN or a +infinity among its logits, nothing above -infinity, or

@@ -3,7 +3,9 @@
 //
 // s = max|x| / 448, code = RNE_e4m3(x / s). A block of a row is sixteen lanes of
 // eight values: one load of 16 bytes, a maximum over the lanes, eight quotients.
-// Bound by memory: two bytes read and one written a value.
+// Bound by memory, two bytes read and one written a value, and by issue close behind: 16384 x 2560 24 us, 5.3 TB/s; 64 x 2560 1.9
+// us, a launch and a load. (Four blocks of sixteen lanes at a time: loads in flight, and fewer exchanges for four maxima
+// together than one by one; 28 us with a maximum and a scale for each by itself, 45 with a division for each value.)
 #include "fp8_codes.cuh"
 #include "pqe_common.cuh"
 
@@ -103,7 +105,7 @@ int fp8_block_quantize(const void *x, int64_t x_stride, int T, int H, uint8_t *q
 int pqe_quantize_fp8_blocks(const float *w, int rows, int cols, uint8_t *q, float *scale, void *stream) {
     PQE_CHECK_ARG(w && q && scale && rows >= 1 && cols >= 1 && aligned(w, 4) && aligned(scale, 4));
     const int64_t rb = ((int64_t)rows + fp8::BLOCK - 1) / fp8::BLOCK, cb = ((int64_t)cols + fp8::BLOCK - 1) / fp8::BLOCK;
-    PQE_CHECK_ARG(rb <= 65535);
+    PQE_CHECK_ARG(rb <= 65535 && cols <= INT32_MAX - (fp8::BLOCK - 1));  // the last tile's columns are ints too
     return launch_pdl(fp8::quantize_tiles_kernel, dim3((unsigned)cb, (unsigned)rb), dim3(256), 0, as_stream(stream), w, rows,
                       cols, q, scale);
 }

@@ -23,6 +23,11 @@ def test_quantize_tiles_arguments(i, v):
     _refused(pqe.load().pqe_quantize_fp8_blocks, [A, 4, 4, A, A, None], i, v)
 
 
+@pytest.mark.parametrize("i,v", [(1, 65535 * 128 + 1), (1, (1 << 31) - 1), (2, (1 << 31) - 127), (2, (1 << 31) - 1)])
+def test_quantize_tiles_beyond_the_grid_or_an_index(i, v):
+    _refused(pqe.load().pqe_quantize_fp8_blocks, [A, 4, 4, A, A, None], i, v)
+
+
 @pytest.mark.parametrize("i,v", [(0, None), (0, A + 8), (1, 112), (1, 136), (2, None), (2, A + 2), (3, None), (3, A + 8), (4, None), (4, A + 1), (5, -1),
                                  (5, (1 << 28) + 1), (6, 0), (6, -3), (6, (1 << 22) + 1), (7, 0), (7, 8), (7, 130), (7, 32784), (8, None), (8, A + 2), (9, 63), (11, None),
                                  (11, A + 2)])
