@@ -481,21 +481,22 @@ def _blocks(n: int) -> int:
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
-def _on_device(*tensors):
-    """Every tensor lies on the current CUDA device, whose streams the call uses."""
+def _on_device(stream, *tensors) -> Optional[int]:
+    """The stream's handle, after a check that every tensor lies on the current CUDA device, whose streams the call uses."""
     dev = tensors[0].get_device()  # -1 on the CPU
     for t in tensors:
         if t is not None and (t.get_device() != dev or dev < 0):
             raise ValueError(f"expected tensors on the current CUDA device, got one on {t.device}")
     if dev != _current_device():
         raise ValueError(f"expected tensors on the current CUDA device, got them on {tensors[0].device}")
+    return _raw_stream(dev) if stream is None else _stream(stream)
 
 
-def _matrix(t: torch.Tensor, name: str) -> tuple[int, int]:
-    """Pointer and row stride (elements) of a matrix whose rows, each contiguous, may lie apart."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+def _matrix(t: torch.Tensor, rows: int, cols: int, name: str) -> tuple[int, int]:
+    """Pointer and row stride (elements) of a matrix [rows, cols] whose rows, each contiguous, may lie apart."""
+    if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name}: expected a matrix of contiguous rows, got {tuple(t.shape)} with strides {t.stride()}")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.data_ptr(), t.stride(0) if rows > 1 else cols
 
 
 def _codes(t: torch.Tensor, name: str):
@@ -511,8 +512,7 @@ def fp8_block_quantize(x, q, scale, stream=None):
     _codes(q, "q")
     xp, xs = _rows(x, T, (H,))
     args = (xp, xs, T, H, _typed(q, q.dtype, "q", T * H), _typed(scale, torch.float32, "scale", T * _blocks(H)))
-    _on_device(x, q, scale)
-    _check("fp8_block_quantize", lib().fp8_block_quantize(*args, _stream(stream)))
+    _check("fp8_block_quantize", lib().fp8_block_quantize(*args, _on_device(stream, x, q, scale)))
 
 
 def pqe_quantize_fp8_blocks(w, q, scale, stream=None):
@@ -521,8 +521,7 @@ def pqe_quantize_fp8_blocks(w, q, scale, stream=None):
     _codes(q, "q")
     args = (_typed(w, torch.float32, "w", 0), rows, cols, _typed(q, q.dtype, "q", rows * cols),
             _typed(scale, torch.float32, "scale", _blocks(rows) * _blocks(cols)))
-    _on_device(w, q, scale)
-    _check("pqe_quantize_fp8_blocks", lib().pqe_quantize_fp8_blocks(*args, _stream(stream)))
+    _check("pqe_quantize_fp8_blocks", lib().pqe_quantize_fp8_blocks(*args, _on_device(stream, w, q, scale)))
 
 
 def pqe_test_set_matmul_kernel(tile: int, split: int):
@@ -535,23 +534,24 @@ def fp8_block_matmul(x, x_scale, w, w_scale, out, status, stream=None):
     """out [M, N] (bf16 or fp32; rows may lie apart) = x W^T of E4M3 codes x [M, K] (rows may lie apart) with fp32 scales
     [M, ceil(K/128)] and w [N, K] with [ceil(N/128), ceil(K/128)]."""
     M, K = x.shape
-    N = w.shape[0]
-    if w.dim() != 2 or w.shape[1] != K or out.shape != (M, N):
+    wide = w.shape
+    N = wide[0] if wide else 0
+    if wide != (N, K) or out.shape != (M, N):
         raise ValueError(f"shapes do not fit: x {tuple(x.shape)}, w {tuple(w.shape)}, out {tuple(out.shape)}")
-    if out.dtype is not torch.bfloat16 and out.dtype is not torch.float32:
+    f32 = torch.float32
+    wants_f32 = out.dtype is f32
+    if not wants_f32 and out.dtype is not torch.bfloat16:
         raise ValueError(f"out: expected bf16 or fp32, got {out.dtype}")
     if M == 0:
         return
     _codes(x, "x")
     _codes(w, "w")
-    xp, xs = _matrix(x, "x")
-    op, os_ = _matrix(out, "out")
-    f32 = torch.float32
-    args = (xp, xs, _typed(x_scale, f32, "x_scale", M * _blocks(K)), _typed(w, w.dtype, "w", N * K),
-            _typed(w_scale, f32, "w_scale", _blocks(N) * _blocks(K)), M, N, K, op, os_, int(out.dtype is f32),
-            _typed(status, torch.int32, "status", 1))
-    _on_device(x, x_scale, w, w_scale, out, status)
-    _check("fp8_block_matmul", lib().fp8_block_matmul(*args, _stream(stream)))
+    xp, xs = _matrix(x, M, K, "x")
+    op, os_ = _matrix(out, M, N, "out")
+    kb = _blocks(K)
+    args = (xp, xs, _typed(x_scale, f32, "x_scale", M * kb), _typed(w, w.dtype, "w", N * K),
+            _typed(w_scale, f32, "w_scale", _blocks(N) * kb), M, N, K, op, os_, wants_f32, _typed(status, torch.int32, "status", 1))
+    _check("fp8_block_matmul", lib().fp8_block_matmul(*args, _on_device(stream, x, x_scale, w, w_scale, out, status)))
 
 
 def sample_tokens(logits, u, tokens, status, temperature=None, top_k=None, top_p=None, min_p=None, logprobs=None, stream=None):
@@ -562,14 +562,13 @@ def sample_tokens(logits, u, tokens, status, temperature=None, top_k=None, top_p
         raise ValueError(f"logits: expected bf16 or fp32, got {logits.dtype}")
     if B == 0:
         return
-    lp, ls = _matrix(logits, "logits")
+    lp, ls = _matrix(logits, B, V, "logits")
     f32, i32 = torch.float32, torch.int32
-    opt = lambda t, dtype, name: None if t is None else _typed(t, dtype, name, B)  # noqa: E731
-    args = (lp, int(logits.dtype is f32), ls, B, V, opt(temperature, f32, "temperature"), opt(top_k, i32, "top_k"),
-            opt(top_p, f32, "top_p"), opt(min_p, f32, "min_p"), _typed(u, f32, "u", B), _typed(tokens, i32, "tokens", B),
-            opt(logprobs, f32, "logprobs"), _typed(status, i32, "status", 1))
-    _on_device(logits, u, tokens, status, temperature, top_k, top_p, min_p, logprobs)
-    _check("sample_tokens", lib().sample_tokens(*args, _stream(stream)))
+    args = (lp, logits.dtype is f32, ls, B, V, None if temperature is None else _typed(temperature, f32, "temperature", B),
+            None if top_k is None else _typed(top_k, i32, "top_k", B), None if top_p is None else _typed(top_p, f32, "top_p", B),
+            None if min_p is None else _typed(min_p, f32, "min_p", B), _typed(u, f32, "u", B), _typed(tokens, i32, "tokens", B),
+            None if logprobs is None else _typed(logprobs, f32, "logprobs", B), _typed(status, i32, "status", 1))
+    _check("sample_tokens", lib().sample_tokens(*args, _on_device(stream, logits, u, tokens, status, temperature, top_k, top_p, min_p, logprobs)))
 
 
 # ---- pager ---------------------------------------------------------------------
