@@ -154,6 +154,7 @@ _SIGS = {
     "fp8_block_quantize": (I32, [P, C.c_int64, I32, I32, P, P, P]),
     "pqe_quantize_fp8_blocks": (I32, [P, I32, I32, P, P, P]),
     "pqe_test_set_matmul_kernel": (I32, [I32, I32]),
+    "pqe_test_set_matmul_expiry": (I32, [I32, I32]),
     "fp8_block_matmul": (I32, [P, C.c_int64, P, P, P, I32, I32, I32, P, C.c_int64, I32, P, P]),
     "sample_tokens": (I32, [P, I32, C.c_int64, I32, I32, P, P, P, P, P, P, P, P, P]),
     "pqe_layer_scratch_bytes": (SZ, [P]),
@@ -528,6 +529,11 @@ def pqe_test_set_matmul_kernel(tile: int, split: int):
     """Test hook: the kernel of fp8_block_matmul by its tile (16, 32: few rows; 128, 256: many) and split; 0, 0 the default
     choice."""
     _check("pqe_test_set_matmul_kernel", lib().pqe_test_set_matmul_kernel(int(tile), int(split)))
+
+
+def pqe_test_set_matmul_expiry(who: int, block: int):
+    """Test hook: whose waits of fp8_block_matmul's kernels give up without a poll (0: nobody's), from a CTA's block `block` on."""
+    _check("pqe_test_set_matmul_expiry", lib().pqe_test_set_matmul_expiry(int(who), int(block)))
 
 
 def fp8_block_matmul(x, x_scale, w, w_scale, out, status, stream=None):

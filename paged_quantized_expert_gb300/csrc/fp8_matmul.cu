@@ -47,6 +47,7 @@ bool map_out(CUtensorMap *m, const Args &a) {
 }
 
 static std::atomic<int> g_tile{0}, g_split{0};  // pqe_test_set_matmul_kernel
+static std::atomic<int64_t> g_expiry{0};         // pqe_test_set_matmul_expiry: who << 32 | block
 
 // whether out can leave by TMA
 bool out_aligned(const Args &a) { return aligned(a.out, 16) && a.out_stride * (a.fp32 ? 4 : 2) % 16 == 0; }
@@ -119,6 +120,12 @@ int pqe_test_set_matmul_kernel(int tile, int split) {
     return PQE_OK;
 }
 
+int pqe_test_set_matmul_expiry(int who, int block) {
+    PQE_CHECK_ARG(who >= fp8mm::EXPIRE_NONE && who <= fp8mm::EXPIRE_SUMS && block >= 0);
+    fp8mm::g_expiry.store((int64_t)who << 32 | block, std::memory_order_relaxed);
+    return PQE_OK;
+}
+
 int fp8_block_matmul(const uint8_t *x, int64_t x_stride, const float *x_scale, const uint8_t *w, const float *w_scale,
                      int M, int N, int K, void *out, int64_t out_stride, int out_fp32, int32_t *status, void *stream) {
     PQE_CHECK_ARG(M >= 0 && M <= 1 << 28 && N >= 1 && N <= 1 << 22 && K >= 16 && K <= 32768 && K % 16 == 0);
@@ -129,7 +136,9 @@ int fp8_block_matmul(const uint8_t *x, int64_t x_stride, const float *x_scale, c
     int dev = 0, sms = 0;
     const int rc = device_info(dev, sms);
     if (rc != PQE_OK) return rc;
-    const fp8mm::Call c{x, w, x_stride, K, {x_scale, w_scale, out, out_stride, M, N, (K + 127) / 128, out_fp32, status, wait_limit()}};
+    const int64_t expiry = fp8mm::g_expiry.load(std::memory_order_relaxed);
+    const fp8mm::Call c{x, w, x_stride, K, {x_scale, w_scale, out, out_stride, M, N, (K + 127) / 128, out_fp32, status, wait_limit(),
+                                            (int)(expiry >> 32), (int)(expiry & INT32_MAX)}};
     return fp8mm::run(c, sms, as_stream(stream));
 }
 

@@ -17,6 +17,9 @@ constexpr int BK = 128;  // values (bytes) of K in a scale block, and in a stage
 // limit other waits have, a CTA does not leave its shared memory and TMEM to them.
 constexpr uint32_t DRAIN = 1u << 16;
 
+// whose waits give up by pqe_test_set_matmul_expiry
+enum Expiry { EXPIRE_NONE, EXPIRE_LOADS, EXPIRE_SECOND_LOADS, EXPIRE_MMA, EXPIRE_SCALES, EXPIRE_SUMS };
+
 struct Args {
     const float *xs, *ws;  // scales [M, kb], [ceil(N / 128), kb]
     void *out;
@@ -24,6 +27,9 @@ struct Args {
     int M, N, kb, fp32;
     int32_t *status;
     uint32_t wait_limit;
+    int expire, expire_from;  // whose waits give up (none), and from which block of a CTA's on
+    // polls of a wait of `who` for its CTA's block `it`
+    __device__ __forceinline__ uint32_t polls(int who, int it) const { return expire == who && it >= expire_from ? 0 : wait_limit; }
 };
 
 struct Call {
@@ -67,6 +73,14 @@ int launch_clusters(void (*kern)(KArgs...), unsigned grid, unsigned block, size_
 }
 
 // ---- device ----
+
+// takes bytes off what the barrier's phase still waits for
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 
 // instruction descriptor, kind::f8f6f4: D fp32, A and B E4M3, both K-major
 __host__ __device__ constexpr uint32_t idesc(int m, int n) {

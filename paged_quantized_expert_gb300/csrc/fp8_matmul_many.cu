@@ -19,7 +19,8 @@
 // issue in turn (137 against 135), scales read from global memory by each epilogue warp (32 lines a load: 135, 126 with the
 // scale warps), the next barrier asked ahead (126 against 123), six stages (130 against 126), one SM a tile of 128 x 256 (136), tiles of a last round in halves where half
 // of the pairs or more would be idle in it (127 against 118 to 122: the loops over K lose more by being there twice).
-// Every wait is bounded; after one expires the roles stop waiting, drain what they issued and the pair ends.
+// Every wait is bounded. After one expires the roles stop, and before the CTAs end the first of them waits for every load that
+// either has issued (each counts its own), and warp 1 for the MMAs.
 #include <atomic>
 
 #include "fp8_matmul.cuh"
@@ -46,7 +47,7 @@ struct Many {
     static constexpr int SCALE_OFF = OUT_OFF + EPI_WARPS * NOUT * BUF;
     static constexpr int BAR_OFF = SCALE_OFF + SLOTS * SLOT * 4;
     static constexpr int TMEM_OFF = BAR_OFF + 8 * (2 * STAGES + 2 * NBUF + 1);
-    static constexpr int SMEM = TMEM_OFF + 16;
+    static constexpr int SMEM = TMEM_OFF + 16;                   // TMEM's address, whether a role stopped, loads issued by each CTA
     static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
 };
 
@@ -83,6 +84,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     const uint32_t bar_tfull = bar_empty + 8 * L::STAGES, bar_tempty = bar_tfull + 8 * L::NBUF, bar_done = bar_tempty + 8 * L::NBUF;
     float *scales = reinterpret_cast<float *>(smem + L::SCALE_OFF);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::TMEM_OFF);
+    volatile uint32_t *stopped = tmem_slot + 1, *issued = tmem_slot + 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
     const int first = (int)blockIdx.x / CTAS, step = (int)gridDim.x / CTAS;
@@ -93,6 +95,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
             mbar_init(bar_empty + 8 * s, 1);  // each CTA's: the commit of the MMAs that read the stage
         }
         mbar_init(bar_done, 1);  // each CTA's: the last commit
+        *stopped = 0;
         for (int b = 0; b < L::NBUF; ++b) {
             mbar_init(bar_tfull + 8 * b, 3);               // each CTA's: the commit, and its two scale warps
             mbar_init(bar_tempty + 8 * b, CTAS * EPI_WARPS);  // the first CTA's: the epilogue warps of both
@@ -119,31 +122,30 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     const uint32_t tmem = *tmem_slot;
     pdl_acquire();
 
+    // (one lane, where loads may be left that no MMA has waited for) every CTA learns it
+    auto stop = [&] {
+        atomicOr(a.status, PQE_STATUS_TIMEOUT);
+        for (int r = 0; r < CTAS; ++r) st_cluster(map_rank(smem_u32(tmem_slot + 1), r), 1);
+    };
     if (warp < EPI_WARP0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
         if (warp == 0 && lane == 0) {
+            const int who = rank == 0 ? EXPIRE_LOADS : EXPIRE_SECOND_LOADS;
             int it = 0;
             bool ok = true;
             for (int i = first; i < items && ok; i += step) {
                 const int m0 = i / n_tiles * (128 * CTAS) + 128 * (int)rank, n0 = i % n_tiles * BN + L::B_ROWS * (int)rank;
                 for (int kb = 0; kb < a.kb; ++kb, ++it) {
                     const int s = it % L::STAGES;
-                    if (!(ok = mbar_wait(bar_empty + 8 * s, ((uint32_t)(it / L::STAGES) & 1u) ^ 1u, a.wait_limit))) break;
+                    if (!(ok = mbar_wait(bar_empty + 8 * s, ((uint32_t)(it / L::STAGES) & 1u) ^ 1u, a.polls(who, it)))) break;
                     const uint32_t at = sbase + s * L::STAGE, bar = CTAS == 2 ? map_rank(bar_full + 8 * s, 0) : bar_full + 8 * s;
                     if (rank == 0) mbar_expect_tx(bar_full + 8 * s, CTAS * L::STAGE);
                     tma_load<CTAS>(at, &tmX, kb * BK, m0, bar);
                     tma_load<CTAS>(at + L::A_BYTES, &tmW, kb * BK, n0, bar);
                 }
             }
-            if (!ok) {
-                // no MMA may have waited for what was issued last: it lands (the pair's on the first CTA's barriers, some of it
-                // perhaps on none that is armed: hence the pause)
-                atomicOr(a.status, PQE_STATUS_TIMEOUT);
-                if (rank == 0)
-                    for (int j = it > L::STAGES ? it - L::STAGES : 0; j < it; ++j)
-                        mbar_wait(bar_full + 8 * (j % L::STAGES), (uint32_t)(j / L::STAGES) & 1u, DRAIN);
-                for (int j = 0; j < 200; ++j) __nanosleep(1000);
-            }
+            st_cluster(map_rank(smem_u32(tmem_slot + 2 + rank), 0), it);
+            if (!ok) stop();
         }
         if (warp >= SCALE_WARP0) {
             // x's scales of 64 rows and one of W's, fetched a group of blocks ahead
@@ -173,7 +175,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
                     for (int j = 0; j < G; ++j) {
                         if (kb + j >= a.kb || !ok) break;
                         const int b = it % L::NBUF;
-                        ok = __all_sync(0xffffffffu, mbar_wait(bar_tfull + 8 * b, ((uint32_t)(it / L::NBUF) & 1u) ^ 1u, a.wait_limit));
+                        ok = __all_sync(0xffffffffu, mbar_wait(bar_tfull + 8 * b, ((uint32_t)(it / L::NBUF) & 1u) ^ 1u, a.polls(EXPIRE_SCALES, it)));
                         if (!ok) break;
                         float *slot = scales + it % L::SLOTS * L::SLOT;
                         slot[64 * w + lane] = vx[j][0];
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
             for (int i = first; i < items && ok; i += step)
                 for (int kb = 0; kb < a.kb; ++kb, ++it) {
                     const int s = it % L::STAGES, b = it % L::NBUF;
-                    ok = mbar_wait(bar_full + 8 * s, (uint32_t)(it / L::STAGES) & 1u, a.wait_limit) &&
+                    ok = mbar_wait(bar_full + 8 * s, (uint32_t)(it / L::STAGES) & 1u, a.polls(EXPIRE_MMA, it)) &&
                          mbar_wait(bar_tempty + 8 * b, ((uint32_t)(it / L::NBUF) & 1u) ^ 1u, a.wait_limit);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     tc_fence_after();
@@ -202,9 +204,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
                     commit<CTAS>(one, bar_empty + 8 * s);
                     commit<CTAS>(one, bar_tfull + 8 * b);
                 }
-            if (!ok && lane == 0) atomicOr(a.status, PQE_STATUS_TIMEOUT);
-            if (!ok)  // what it did not wait for lands before the CTAs end
-                for (int j = 0; j < 200; ++j) __nanosleep(1000);
+            if (!ok && lane == 0) stop();
             commit<CTAS>(one, bar_done);
         }
     } else {
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
             constexpr int LD = 4;  // loads under way at a time
             for (int kb = 0; kb < a.kb; ++kb, ++it) {
                 const int b = it % L::NBUF;
-                if (!__all_sync(0xffffffffu, mbar_wait(bar_tfull + 8 * b, (uint32_t)(it / L::NBUF) & 1u, a.wait_limit))) {
+                if (!__all_sync(0xffffffffu, mbar_wait(bar_tfull + 8 * b, (uint32_t)(it / L::NBUF) & 1u, a.polls(EXPIRE_SUMS, it)))) {
                     ok = false;
                     break;
                 }
@@ -316,8 +316,26 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
     }
     __syncwarp();
     tc_fence_before();
-    if (CTAS == 1) __syncthreads();
-    else cluster_sync();  // neither CTA goes while the other's loads or arrivals may still reach it
+    auto all = [] {
+        if (CTAS == 1) __syncthreads();
+        else cluster_sync();
+    };
+    all();  // neither CTA goes while the other's loads or arrivals may still reach it
+    if (*stopped) {
+        if (rank == 0 && threadIdx.x == 0) {
+            // Loads of the last STAGES blocks may be under way: the MMAs waited for those before. A pair's count together, on the
+            // first CTA's barrier of the stage, which that CTA armed for both with its own load.
+            const int n0 = issued[0], n1 = issued[CTAS - 1], most = max(n0, n1);
+            for (int j = max(0, most - L::STAGES); j < most; ++j) {
+                const uint32_t bar = bar_full + 8 * (j % L::STAGES);
+                if (j >= n0) mbar_expect_tx(bar, L::STAGE);
+                else if (j >= n1) mbar_complete_tx(bar, L::STAGE);
+                mbar_wait(bar, (uint32_t)(j / L::STAGES) & 1u, DRAIN);
+            }
+        }
+        __syncwarp();
+        all();
+    }
     if (warp == 1) mbar_wait(bar_done, 0, DRAIN);  // nor before the MMAs are done, and have said so to both
     __syncwarp();
     if (warp == 1) {

@@ -1,0 +1,84 @@
+"""Waits of the block-scaled products that expire, with no GPU fault: a hook makes one role of a kernel give up its waits from one of
+its blocks on, while the others run into a short limit. The call comes back and says so, the loads under way have landed before
+its CTAs end, and the next call is right."""
+import time
+
+import pytest
+import torch
+
+from test_gpu_fp8_block import check, inputs
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+LOADS, SECOND_LOADS, MMA, SCALES, SUMS = 1, 2, 3, 4, 5
+
+
+@pytest.fixture
+def hooks(cuda_lib):
+    cuda_lib.pqe_set_wait_limit(2000)
+    yield cuda_lib
+    cuda_lib.pqe_test_set_matmul_kernel(0, 0)
+    cuda_lib.pqe_test_set_matmul_expiry(0, 0)
+    cuda_lib.pqe_set_wait_limit(0)
+
+
+def expires(pqe, kernel, who, block, sizes):
+    """Three calls whose waits expire, each followed by one that is right."""
+    a = inputs(*sizes, 3)
+    out = torch.empty(sizes[:2], device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pqe.pqe_test_set_matmul_kernel(*kernel)
+    for _ in range(3):
+        pqe.pqe_test_set_matmul_expiry(who, block)
+        torch.cuda.synchronize()
+        t = time.perf_counter()
+        pqe.fp8_block_matmul(*a, out, status)
+        torch.cuda.synchronize()
+        assert time.perf_counter() - t < 10
+        assert status.item() == pqe.PQE_STATUS_TIMEOUT
+        pqe.pqe_test_set_matmul_expiry(0, 0)
+        status.zero_()
+        out.fill_(float("nan"))
+        pqe.pqe_set_wait_limit(0)
+        pqe.fp8_block_matmul(*a, out, status)
+        check(out, *a)
+        assert status.item() == 0
+        pqe.pqe_set_wait_limit(2000)
+
+
+@pytest.mark.parametrize("who", [LOADS, SECOND_LOADS, MMA, SCALES, SUMS])
+@pytest.mark.parametrize("kernel", [(128, 128), (256, 128), (256, 256)], ids=lambda k: f"{k[0]}-{k[1]}")
+def test_many_rows(hooks, kernel, who):
+    """From the first block on, inside the ring's first round, later, and at the last block of a tile."""
+    if who == SECOND_LOADS and kernel[0] == 128:
+        pytest.skip("one CTA a tile")
+    for block in (0, 2, 7, 15):
+        expires(hooks, kernel, who, block, (300, 700, 2048))
+
+
+@pytest.mark.parametrize("who", [LOADS, SECOND_LOADS, MMA, SCALES, SUMS])
+def test_many_rows_in_a_later_tile(hooks, who):
+    """1413 tiles of four blocks on 76 pairs."""
+    expires(hooks, (256, 128), who, 30, (2050, 20000, 512))
+
+
+def test_nobody_gives_up(hooks):
+    """The hook at a block that no CTA reaches, or for a role that the kernel does not have, changes nothing."""
+    a = inputs(300, 700, 2048, 4)
+    out = torch.empty((300, 700), device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    hooks.pqe_set_wait_limit(0)
+    for kernel, who, block in (((256, 256), LOADS, 16), ((256, 128), MMA, 16), ((128, 128), SECOND_LOADS, 0)):
+        hooks.pqe_test_set_matmul_kernel(*kernel)
+        hooks.pqe_test_set_matmul_expiry(who, block)
+        out.fill_(float("nan"))
+        hooks.fp8_block_matmul(*a, out, status)
+        check(out, *a)
+    assert status.item() == 0
+
+
+def test_hook_refuses(cuda_lib):
+    for bad in ((-1, 0), (6, 0), (1, -1)):
+        with pytest.raises(cuda_lib.PqeError):
+            cuda_lib.pqe_test_set_matmul_expiry(*bad)
