@@ -792,11 +792,12 @@ PQE_API int pqe_quantize_fp8_blocks(const float *w, int rows, int cols, uint8_t 
  * call.) */
 PQE_API int pqe_test_set_matmul_kernel(int tile, int split);
 /* (pqe_test_set_matmul_expiry: a test hook for the expiry of waits, with no GPU
- * fault: of the kernels for many rows, who gives up its waits without a poll,
- * from its CTA's block number `block` (of 128 along K, all of the CTA's tiles)
- * on: 1 the loads, 2 those of a pair's second CTA, 3 the MMAs, 4 the scales, 5
- * the sums; the others by pqe_set_wait_limit. 0: nobody. Process-wide, read at
- * each call.) */
+ * fault: who gives up its waits without a poll, from its CTA's block number
+ * `block` (of 128 along K, all of the CTA's tiles) on: 1 the loads, 2 those of a
+ * pair's second CTA, 3 the MMAs, 4 the scales of the kernel for many rows, 5 the
+ * sums, 6 what the CTAs that share a tile's K send one another (in those of the
+ * cluster from number `block` on); the others by pqe_set_wait_limit. 0: nobody.
+ * Process-wide, read at each call.) */
 PQE_API int pqe_test_set_matmul_expiry(int who, int block);
 PQE_API int fp8_block_matmul(const uint8_t *x, int64_t x_stride, const float *x_scale, const uint8_t *w,
                              const float *w_scale, int M, int N, int K, void *out, int64_t out_stride, int out_fp32,

@@ -121,7 +121,7 @@ int pqe_test_set_matmul_kernel(int tile, int split) {
 }
 
 int pqe_test_set_matmul_expiry(int who, int block) {
-    PQE_CHECK_ARG(who >= fp8mm::EXPIRE_NONE && who <= fp8mm::EXPIRE_SUMS && block >= 0);
+    PQE_CHECK_ARG(who >= fp8mm::EXPIRE_NONE && who <= fp8mm::EXPIRE_PARTS && block >= 0);
     fp8mm::g_expiry.store((int64_t)who << 32 | block, std::memory_order_relaxed);
     return PQE_OK;
 }

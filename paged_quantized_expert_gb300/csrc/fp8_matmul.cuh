@@ -18,7 +18,7 @@ constexpr int BK = 128;  // values (bytes) of K in a scale block, and in a stage
 constexpr uint32_t DRAIN = 1u << 16;
 
 // whose waits give up by pqe_test_set_matmul_expiry
-enum Expiry { EXPIRE_NONE, EXPIRE_LOADS, EXPIRE_SECOND_LOADS, EXPIRE_MMA, EXPIRE_SCALES, EXPIRE_SUMS };
+enum Expiry { EXPIRE_NONE, EXPIRE_LOADS, EXPIRE_SECOND_LOADS, EXPIRE_MMA, EXPIRE_SCALES, EXPIRE_SUMS, EXPIRE_PARTS };
 
 struct Args {
     const float *xs, *ws;  // scales [M, kb], [ceil(N / 128), kb]

@@ -13,7 +13,8 @@
 // SM: one's tile end, or the next call's set-up, beside the other's stream.
 // 16 x 131072 x 2048: 44 us, 6.2 TB/s, the weights' bytes. 1 x 3584 x 2048: 3.6 us, 64 x 2048 x 2560: 5.1, of which set-up (TMEM,
 // barriers), the first TMA and MMA, and the parts' way through the cluster are some 3: latency.
-// Every wait is bounded; after one expires the roles stop waiting, drain what they issued and the CTA ends.
+// Every wait is bounded. After one expires the roles stop waiting, and before the CTA ends its loads, its MMAs and the parts sent to
+// it have come.
 #include <atomic>
 
 #include "fp8_matmul.cuh"
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
                 const int nt = i / m_tiles, mt = i % m_tiles;
                 for (int kb = k0; kb < k1; ++kb, ++it) {
                     const int s = it % L::STAGES;
-                    if (!(ok = mbar_wait(bar_empty + 8 * s, ((uint32_t)(it / L::STAGES) & 1u) ^ 1u, a.wait_limit))) break;
+                    if (!(ok = mbar_wait(bar_empty + 8 * s, ((uint32_t)(it / L::STAGES) & 1u) ^ 1u, a.polls(EXPIRE_LOADS, it)))) break;
                     const uint32_t at = sbase + s * L::STAGE;
                     mbar_expect_tx(bar_full + 8 * s, L::STAGE);
                     tma_load_2d(at, &tmW, kb * BK, nt * 128, bar_full + 8 * s);
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
         for (int i = first; i < items && ok; i += step)
             for (int kb = k0; kb < k1; ++kb, ++it) {
                 const int s = it % L::STAGES, b = it & 1;
-                ok = mbar_wait(bar_tempty + 8 * b, ((uint32_t)(it >> 1) & 1u) ^ 1u, a.wait_limit) &&
+                ok = mbar_wait(bar_tempty + 8 * b, ((uint32_t)(it >> 1) & 1u) ^ 1u, a.polls(EXPIRE_MMA, it)) &&
                      mbar_wait(bar_full + 8 * s, (uint32_t)(it / L::STAGES) & 1u, a.wait_limit);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 tc_fence_after();
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
                 fetch(at + L::GROUP);
                 for (int j = 0; j < L::GROUP && at + j < nk; ++j, ++it) {
                     const int b = it & 1;
-                    if (!mbar_wait(bar_tfull + 8 * b, (uint32_t)(it >> 1) & 1u, limit)) {
+                    if (!mbar_wait(bar_tfull + 8 * b, (uint32_t)(it >> 1) & 1u, min(limit, a.polls(EXPIRE_SUMS, it)))) {
                         limit = 1;  // the others keep to their barriers: go on without waiting
                         atomicOr(a.status, PQE_STATUS_TIMEOUT);
                     }
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
                              : "memory");
             }
             // (every CTA sends its parts, also one whose waits expired: none leaves before all have come)
-            if (!mbar_wait_cluster(bar_parts, 0, max(a.wait_limit, DRAIN))) {
+            if (!mbar_wait_cluster(bar_parts, 0, a.polls(EXPIRE_PARTS, rank) ? max(a.wait_limit, DRAIN) : 0)) {
                 late = true;
                 atomicOr(a.status, PQE_STATUS_TIMEOUT);
             }
@@ -238,7 +239,11 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
     if (parts_log && warp < 2) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     tc_fence_before();
     const bool any_late = __syncthreads_or(late);
-    if (parts_log && any_late) cluster_sync();  // what the others send may still come: until they are through, or gone
+    if (parts_log && any_late) {  // what the others send may still come
+        cluster_sync();           // all of it has been sent (a CTA that is through is gone and does not count)
+        if (threadIdx.x == 0) mbar_wait_cluster(bar_parts, 0, DRAIN);
+        __syncthreads();
+    }
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::TMEM_COLS) : "memory");

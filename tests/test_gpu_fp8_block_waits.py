@@ -11,7 +11,7 @@ from test_gpu_fp8_block import check, inputs
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
 
-LOADS, SECOND_LOADS, MMA, SCALES, SUMS = 1, 2, 3, 4, 5
+LOADS, SECOND_LOADS, MMA, SCALES, SUMS, PARTS = 1, 2, 3, 4, 5, 6
 
 
 @pytest.fixture
@@ -63,6 +63,27 @@ def test_many_rows_in_a_later_tile(hooks, who):
     expires(hooks, (256, 128), who, 30, (2050, 20000, 512))
 
 
+@pytest.mark.parametrize("who", [LOADS, MMA, SUMS])
+@pytest.mark.parametrize("kernel", [(16, 0), (16, 1), (16, 2), (32, 0), (32, 1), (32, 2), (32, 3)], ids=lambda k: f"{k[0]}-{k[1]}")
+def test_few_rows(hooks, kernel, who):
+    """From a CTA's first block on, inside the ring's first round, and (33 blocks of K, shared by up to eight) at its last or one near it."""
+    for block in (0, 2, max(3, (33 >> kernel[1]) - 1)):
+        expires(hooks, kernel, who, block, (60, 700, 4224))
+
+
+@pytest.mark.parametrize("who,block", [(LOADS, 40), (MMA, 41), (SUMS, 42)])
+def test_few_rows_in_a_later_tile(hooks, who, block):
+    """3282 tiles of four blocks on 304 CTAs: ten or eleven each."""
+    expires(hooks, (32, 0), who, block, (33 * 5, 70000, 512))
+
+
+@pytest.mark.parametrize("kernel", [(16, 1), (16, 2), (32, 1), (32, 2), (32, 3)], ids=lambda k: f"{k[0]}-{k[1]}")
+def test_parts_of_a_cluster(hooks, kernel):
+    """The wait for the parts gives up in all CTAs of a cluster, in all but the first, and in the last alone."""
+    for first in {0, 1, (1 << kernel[1]) - 1}:
+        expires(hooks, kernel, PARTS, first, (60, 700, 4224))
+
+
 def test_nobody_gives_up(hooks):
     """The hook at a block that no CTA reaches, or for a role that the kernel does not have, changes nothing."""
     a = inputs(300, 700, 2048, 4)
@@ -79,6 +100,6 @@ def test_nobody_gives_up(hooks):
 
 
 def test_hook_refuses(cuda_lib):
-    for bad in ((-1, 0), (6, 0), (1, -1)):
+    for bad in ((-1, 0), (7, 0), (1, -1)):
         with pytest.raises(cuda_lib.PqeError):
             cuda_lib.pqe_test_set_matmul_expiry(*bad)
