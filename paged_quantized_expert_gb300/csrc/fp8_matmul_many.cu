@@ -41,8 +41,10 @@ struct Many {
     static constexpr int CW = BN / 2;                            // columns of an epilogue warp
     static constexpr int BUF = 32 * 64, NOUT = 4;                // store buffers of a warp: 32 rows of 64 bytes
     static constexpr int OUT_OFF = STAGES * STAGE;
-    // scales of a block: x's of the CTA's 128 rows, W's of the tile's two 128-row blocks. A slot is written anew when the MMAs
-    // NBUF blocks before are done; those waited for the epilogue of the block NBUF before them.
+    // scales of a block: x's of the CTA's 128 rows, W's of the tile's two 128-row blocks. A slot is written anew when the block
+    // NBUF before is full, and for that the epilogue warps have arrived too, once they had read the block NBUF before it. (Not a
+    // barrier of the slots' own: a second poll a block in the scale warps took 13.0 us for 1024 x 3584 x 2048 in tiles of 256 x
+    // 128, 11.6 without.)
     static constexpr int SLOTS = 2 * NBUF, SLOT = 128 + 4;
     static constexpr int SCALE_OFF = OUT_OFF + EPI_WARPS * NOUT * BUF;
     static constexpr int BAR_OFF = SCALE_OFF + SLOTS * SLOT * 4;
@@ -65,7 +67,7 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
 
 // an arrival on a barrier of either CTA. It orders no memory of this thread's: what it says is that TMEM has been read, which
 // the tcgen05 fences around it order (with release.cluster each arrival waited for the thread's earlier loads and stores: 57 us
-// against 29 for 2048 x 4096 x 2560).
+// against 29 for 2048 x 4096 x 2560). That the block's scales have been read is said apart, inside the warp's CTA.
 template <int CTAS>
 __device__ __forceinline__ void arrive(uint32_t bar) {
     if constexpr (CTAS == 1) mbar_arrive_plain(bar);
@@ -97,7 +99,8 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         mbar_init(bar_done, 1);  // each CTA's: the last commit
         *stopped = 0;
         for (int b = 0; b < L::NBUF; ++b) {
-            mbar_init(bar_tfull + 8 * b, 3);               // each CTA's: the commit, and its two scale warps
+            // each CTA's: the commit, its two scale warps, its epilogue warps when they are through with the buffer's last block
+            mbar_init(bar_tfull + 8 * b, 3 + EPI_WARPS);
             mbar_init(bar_tempty + 8 * b, CTAS * EPI_WARPS);  // the first CTA's: the epilogue warps of both
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -213,6 +216,8 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
         uint8_t *buf = smem + L::OUT_OFF + (warp - EPI_WARP0) * L::NOUT * L::BUF;
         const uint32_t t0 = tmem + part * L::CW + ((uint32_t)(32 * q) << 16);
         const uint32_t tempty0 = CTAS == 2 ? map_rank(bar_tempty, 0) : bar_tempty;
+        if (lane == 0)
+            for (int b = 0; b < L::NBUF; ++b) mbar_arrive_plain(bar_tfull + 8 * b);
         int it = 0;
         bool ok = true;
         for (int i = first; i < items && ok; i += step) {
@@ -249,7 +254,7 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive<CTAS>(tempty0 + 8 * b);
+                if (lane == 0) arrive<CTAS>(tempty0 + 8 * b), mbar_arrive_plain(bar_tfull + 8 * b);
             }
             if (!ok) {
                 if (lane == 0) atomicOr(a.status, PQE_STATUS_TIMEOUT);

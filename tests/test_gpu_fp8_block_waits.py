@@ -84,6 +84,21 @@ def test_parts_of_a_cluster(hooks, kernel):
         expires(hooks, kernel, PARTS, first, (60, 700, 4224))
 
 
+@pytest.mark.parametrize("kernel", [(128, 128), (256, 128), (256, 256)], ids=lambda k: f"{k[0]}-{k[1]}")
+def test_scales_of_many_blocks(hooks, kernel):
+    """Several tiles a CTA, 64 blocks each, whose scales differ by up to 2^24: every slot of scales is used anew many times. A scale
+    of another block would show in the bound, one that came late from run to run."""
+    a = inputs(2300, 5000, 8192, 6)
+    outs = [torch.full((2300, 5000), float("nan"), device=DEV) for _ in range(4)]
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    hooks.pqe_set_wait_limit(0)
+    hooks.pqe_test_set_matmul_kernel(*kernel)
+    for o in outs:
+        hooks.fp8_block_matmul(*a, o, status)
+    check(outs[0], *a)
+    assert all(torch.equal(o, outs[0]) for o in outs) and status.item() == 0
+
+
 def test_nobody_gives_up(hooks):
     """The hook at a block that no CTA reaches, or for a role that the kernel does not have, changes nothing."""
     a = inputs(300, 700, 2048, 4)
