@@ -46,8 +46,8 @@ bool map_out(CUtensorMap *m, const Args &a) {
                   (uint64_t)a.out_stride * size, 32, 64 / size, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
-static std::atomic<int> g_tile{0}, g_split{0};  // pqe_test_set_matmul_kernel
-static std::atomic<int64_t> g_expiry{0};         // pqe_test_set_matmul_expiry: who << 32 | block
+static std::atomic<int> g_kernel{0};      // pqe_test_set_matmul_kernel: tile << 16 | split, one word, so that no call sees parts of two
+static std::atomic<int64_t> g_expiry{0};  // pqe_test_set_matmul_expiry: who << 32 | block
 
 // whether out can leave by TMA
 bool out_aligned(const Args &a) { return aligned(a.out, 16) && a.out_stride * (a.fp32 ? 4 : 2) % 16 == 0; }
@@ -95,7 +95,7 @@ static Choice least(const Call &c, int sms) {
 }
 
 static int run(const Call &c, int sms, cudaStream_t s) {
-    const int tile = g_tile.load(std::memory_order_relaxed), split = g_split.load(std::memory_order_relaxed);
+    const int kernel = g_kernel.load(std::memory_order_relaxed), tile = kernel >> 16, split = kernel & 0xFFFF;
     Choice use = least(c, sms);
     if (tile) {
         use = {tile, split, 0};
@@ -115,8 +115,7 @@ extern "C" {
 int pqe_test_set_matmul_kernel(int tile, int split) {
     PQE_CHECK_ARG((tile == 0 && split == 0) || (tile == 16 && split >= 0 && split <= 2) || (tile == 32 && split >= 0 && split <= 3) ||
                   (tile == 128 && split == 128) || (tile == 256 && (split == 128 || split == 256)));
-    fp8mm::g_tile.store(tile, std::memory_order_relaxed);
-    fp8mm::g_split.store(split, std::memory_order_relaxed);
+    fp8mm::g_kernel.store(tile << 16 | split, std::memory_order_relaxed);
     return PQE_OK;
 }
 

@@ -1,6 +1,7 @@
-"""Waits of the block-scaled products that expire, with no GPU fault: a hook makes one role of a kernel give up its waits from one of
-its blocks on, while the others run into a short limit. The call comes back and says so, the loads under way have landed before
-its CTAs end, and the next call is right."""
+"""Test hooks of the block-scaled products: the choice of kernel, and waits that expire with no GPU fault. A hook makes one role of a
+kernel give up its waits from one of its blocks on, while the others run into a short limit. The call comes back and says so,
+the loads under way have landed before its CTAs end, and the next call is right."""
+import threading
 import time
 
 import pytest
@@ -111,6 +112,33 @@ def test_nobody_gives_up(hooks):
         out.fill_(float("nan"))
         hooks.fp8_block_matmul(*a, out, status)
         check(out, *a)
+    assert status.item() == 0
+
+
+def test_kernel_hook_set_while_calls_are_made(cuda_lib):
+    """A call sees one choice or another, never the tile of one with the split of the other, which no kernel takes."""
+    a = inputs(40, 300, 1024, 5)
+    out = torch.empty((40, 300), device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    done = threading.Event()
+
+    def turn():
+        while not done.is_set():
+            for kernel in ((32, 3), (256, 256), (16, 0), (128, 128), (32, 0), (256, 128)):
+                cuda_lib.pqe_test_set_matmul_kernel(*kernel)
+
+    t = threading.Thread(target=turn)
+    t.start()
+    try:
+        for _ in range(200):
+            out.fill_(float("nan"))
+            for _ in range(20):
+                cuda_lib.fp8_block_matmul(*a, out, status)
+            check(out, *a)
+    finally:
+        done.set()
+        t.join()
+        cuda_lib.pqe_test_set_matmul_kernel(0, 0)
     assert status.item() == 0
 
 
