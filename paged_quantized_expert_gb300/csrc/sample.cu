@@ -52,7 +52,7 @@ struct Args {
 constexpr int THREADS = 512, WARPS = THREADS / 32;
 constexpr int OCTAVE = 32;                   // bins for a factor of two
 constexpr int FAR = 44 * OCTAVE + 1;         // what falls into this bin weighs less than 2^-44: nothing
-constexpr int BINS = 1536;                   // FAR and a little, in slices of whole warps
+constexpr int BINS = 1440;                   // FAR and a little, in slices for up to MAX_PARTS CTAs
 constexpr int LIST = 2 * THREADS;            // elements of a bin that one CTA sorts, two a thread
 constexpr int GROUPS = 128, FEW_K = 100;     // groups of lanes whose largest logits are compared; up to this top_k by them alone
 constexpr int RANKED = 256;                  // candidates of a row that it ranks by comparing each with each
@@ -111,6 +111,15 @@ struct Shared {
         u64 spare[RANKED];            // at the end
     };
 };
+
+static_assert(BINS > FAR && BINS % MAX_PARTS == 0, "");
+constexpr size_t HEAD = (sizeof(Shared) + 127) / 128 * 128 + 64;  // + room to align the pieces
+static_assert(HEAD + CHUNK_MAX * sizeof(float) <= 227 * 1024, "shared memory of one CTA");
+// the most logits of a CTA with which two fit on an SM: of its 228 KB the system takes 1 KB a CTA (64 rows of 152064, 19008 a CTA:
+// all kept 39 us, 52 with one CTA an SM; top_p 93, 140)
+constexpr int CHUNK_TWO = (int)((114 * 1024 - 1024 - HEAD) / sizeof(float));
+static_assert(2 * (HEAD + CHUNK_TWO * sizeof(float) + 1024) <= 228 * 1024, "");
+static_assert(MAX_PARTS * CHUNK_TWO >= 152064, "a usual vocabulary keeps two CTAs an SM");
 
 // What a row's weights go by.
 constexpr float MAGIC = 12582912.f;  // 1.5 * 2^23: a number added to it is rounded to a whole one
@@ -892,15 +901,12 @@ static int launch(const Args &a, int B, cudaStream_t s) {
     int dev = 0, sms = 0;
     const int rc = device_info(dev, sms);
     if (rc != PQE_OK) return rc;
-    constexpr size_t HEAD = (sizeof(Shared) + 127) / 128 * 128 + 64;  // + room to align the pieces
-    static_assert(HEAD + CHUNK_MAX * sizeof(float) <= 227 * 1024, "shared memory of one CTA");
     if (!attr_set[dev].load(std::memory_order_relaxed)) {
         PQE_CUDA_TRY(cudaFuncSetAttribute(sample_kernel<FP32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           (int)(HEAD + CHUNK_MAX * sizeof(float))));
         attr_set[dev].store(1, std::memory_order_relaxed);
     }
     // as few CTAs a row as leave room for two on an SM; more where SMs would stay idle
-    constexpr int CHUNK_TWO = 19968;
     int log = 0;
     while (log < 3 && (a.V + (1 << log) - 1) >> log > CHUNK_TWO) ++log;
     while (log < 3 && ((int64_t)B << (log + 1)) <= sms && a.V >> (log + 1) >= 2048) ++log;
