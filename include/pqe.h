@@ -815,9 +815,10 @@ PQE_API int fp8_block_matmul(const uint8_t *x, int64_t x_stride, const float *x_
  *   logprob = ln(w_token / sum_kept w), what the token was drawn with
  * t == 0 takes the largest logit, the lower index among equal ones (logprob 0).
  * A t above 0 and below 1e-36 counts as about that in w.
- * A logit of -infinity is never kept. Weights enter the sums with 2^-29 of
- * their own size and 2^-43 of the largest, the sums are whole numbers: the same
- * in every run and for every row's place in the batch.
+ * A logit of -infinity is never kept. Weights enter the sums with 2^-28 of
+ * their own size (the sum that top_p is a part of: 2^-27) and 2^-43 of the
+ * largest, the sums are whole numbers: the same in every run and for every row's
+ * place in the batch.
  * A row with a NaN or a +infinity among its logits, nothing above -infinity, or
  * a setting out of range (t negative or not finite, top_p or min_p NaN, u
  * outside [0, 1)) gives token -1, logprob NaN and PQE_STATUS_NO_TOKEN; the other

@@ -54,14 +54,15 @@ bool out_aligned(const Args &a) { return aligned(a.out, 16) && a.out_stride * (a
 
 // Which kernel takes a call: the least of estimates in us, from measurements on one GB300 (K = 2048, bf16 out unless said).
 //   few, 16 or 32 tokens a tile: 2.2 (2.3) to begin and end, 0.23 (0.29) a block of K and round of tiles; where SMs are left 2 to
-//   8 CTAs share the blocks, for 0.8 (1 x 3584: 3.3 by four, 5.9 alone; 64 x 2048 x 2560: 4.9; 333 x 1003 x 1040 fp32: 5.3;
-//   64 x 512 x 16384: 7.5 by eight, 39 alone)
-//   many, 128 x 128 an SM: 2.7, 0.24 a block in a first round of tiles, 0.29 in several (128 x 3584: 6.7)
-//   many, 256 x 128 a pair: 3.2, 0.235, 0.27 (512 x 3584: 7.3; 4962 x 232 x 8112: 21; 27 and 29 with the other two)
-//   many, 256 x 256 a pair: 4.1, 0.31, 0.44 (1024 x 3584: 9.8; the other two 11.6, 11.3. 4099 x 3584: 29.8; 33.9, 32.0.
-//   16384 x 4096 x 2560: 122; 155, 142)
-// and of no kernel less than the bytes at 6.2 TB/s (64 x 131072 fp32: 52 by 128 x 128 tiles, 54 by 32 tokens, 63, 65 by pairs;
-// 16 x 131072: 44 by 16 tokens; 256 x 131072: 76 by pairs, 111 by 128 x 128). The kernels for many rows store element by element
+//   8 CTAs share the blocks, for 0.8 (1 x 3584: 3.5 by four, 6.0 alone; 64 x 2048 x 2560: 5.0; 333 x 1003 x 1040 fp32: 5.4;
+//   64 x 512 x 16384: 7.6 by eight, 41 alone)
+//   many, 128 x 128 an SM: 2.7, 0.24 a block in a first round of tiles, 0.29 in several (128 x 3584: 7.0; 512 x 3584: 7.5)
+//   many, 256 x 128 a pair: 3.2, 0.235, 0.27 (512 x 3584: 7.6; 4962 x 232 x 8112: 21; 29 with 256 x 256 and 26 to 30 with 128 x 128,
+//   which takes it, the estimates being 0.2 apart)
+//   many, 256 x 256 a pair: 4.1, 0.31, 0.44 (1024 x 3584: 10.0; the other two 12.1, 11.6. 4099 x 3584: 30; 35, 33.
+//   16384 x 4096 x 2560: 120; 158, 146)
+// and of no kernel less than the bytes at 6.2 TB/s (64 x 131072 fp32: 52 by 128 x 128 tiles, 55 by 32 tokens, 63, 66 by pairs;
+// 16 x 131072: 44 by 16 tokens; 256 x 131072: 65, 70 by pairs, 100 by 128 x 128). The kernels for many rows store element by element
 // where out's rows are not aligned to 16 bytes, 2 a round.
 struct Choice {
     int rows, cols;  // few: tokens a tile, log2 of the CTAs that share one; many: 128 or 256 rows, columns

@@ -11,7 +11,7 @@
 //
 // Warp 0 issues TMA (a ring of W and x stages), warp 1 the MMAs, warps 2-5 (one a TMEM lane quarter) scale and add. Two CTAs an
 // SM: one's tile end, or the next call's set-up, beside the other's stream.
-// 16 x 131072 x 2048: 44 us, 6.2 TB/s, the weights' bytes. 1 x 3584 x 2048: 3.6 us, 64 x 2048 x 2560: 5.1, of which set-up (TMEM,
+// 16 x 131072 x 2048: 44 us, 6.2 TB/s, the weights' bytes. 1 x 3584 x 2048: 3.5 us, 64 x 2048 x 2560: 5.0, of which set-up (TMEM,
 // barriers), the first TMA and MMA, and the parts' way through the cluster are some 3: latency.
 // Every wait is bounded. After one expires the roles stop waiting, and before the CTA ends its loads, its MMAs and the parts sent to
 // it have come.

@@ -10,15 +10,17 @@
 // shared memory, warps 4-11 scale and add. Finished rows go through shared memory and leave as TMA stores (which cut what lies
 // outside), or, where out is not aligned to 16 bytes, element by element.
 //
-// 16384 x 4096 x 2560: 118 to 122 us, 2.8 to 2.9 PFLOP/s; 4099 x 3584 x 2048 30; 64 x 131072 x 2048 to fp32 52 (128 x 128 tiles,
-// 5.8 TB/s of weights and results). What bounds the first: a block's product cannot be added to the next one's in the tensor
-// core, so all of TMEM is read once a block. Without those reads (a copy of the kernel) the same loads and MMAs take 115 us, with
-// accumulators enough never to wait 111; the two accumulators' round trip (MMA latency, commit, reading 128 columns, the arrival
-// at the pair's first CTA) is what the rest is. A product with one scale for all of K, by the library, takes 96.
+// In a replayed graph: 16384 x 4096 x 2560 120 us, 2.9 PFLOP/s (as calls in a row, where power lowers the clock, 135); 4099 x
+// 3584 x 2048 30; 64 x 131072 x 2048 to fp32 52 (128 x 128 tiles, 5.8 TB/s of weights and results). What bounds the first: a
+// block's product cannot be added to the next one's in the tensor core, so all of TMEM is read once a block. Without those reads
+// (a copy of the kernel) the same loads and MMAs take 115 us, with accumulators enough never to wait 111; the two accumulators'
+// round trip (MMA latency, commit, reading 128 columns, the arrival at the pair's first CTA) is what the rest is. A product with
+// one scale for all of K, by the library, takes 96.
 // Tried: 16 epilogue warps of 64 columns (154 us then against 135: TMEM reads at 221 bytes a clock, 294 with 8), two warps that
 // issue in turn (137 against 135), scales read from global memory by each epilogue warp (32 lines a load: 135, 126 with the
-// scale warps), the next barrier asked ahead (126 against 123), six stages (130 against 126), one SM a tile of 128 x 256 (136), tiles of a last round in halves where half
-// of the pairs or more would be idle in it (127 against 118 to 122: the loops over K lose more by being there twice).
+// scale warps), the next barrier asked ahead (126 against 123), six stages (130 against 126), one SM a tile of 128 x 256 (136),
+// tiles of a last round in halves where half of the pairs or more would be idle in it (127 against 118 to 122: the loops over K
+// lose more by being there twice).
 // Every wait is bounded. After one expires the roles stop, and before the CTAs end the first of them waits for every load that
 // either has issued (each counts its own), and warp 1 for the MMAs.
 #include <atomic>

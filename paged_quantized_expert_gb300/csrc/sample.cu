@@ -4,24 +4,30 @@
 // the kept weights, in index order, passes u times their total. A row lies in the shared memory of a cluster of 1 to 8 CTAs, so
 // logits are read once; sums are whole numbers (weights times 2^43), the same in any order.
 //
-//   all kept (no top_k, no top_p)  a sum for each thread's stretch of the row, a scan, and the thread whose stretch u falls
-//                                  into walks it.
-//   a border to be found           a histogram of the logits, 32 bins for each factor of two of the weights: counts, and for
+//   all kept (no top_k, no top_p)  a sum for each thread's part of a warp's stretch of the row, a scan, and the warp whose stretch u
+//                                  falls into walks it.
+//   a top_k of FEW_K at most       the largest logits of GROUPS groups of lanes: what is not below the top_k-th of them holds the
+//                                  first top_k and is hardly more. Up to RANKED candidates go to a list, where the first CTA
+//                                  compares each with each and finishes.
+//   another border                 a histogram of the logits, 32 bins for each factor of two of the weights: counts, and for
 //                                  top_p sums. The bins are merged in slices, a CTA each; the CTA whose slice the border falls
-//                                  into finds the bin. Where what lies above the border's bin and in it fits a list (2048),
-//                                  the first CTA sorts and finishes it. Otherwise the bin alone goes to a list (1024), which
-//                                  gives the border's value and how many of its equals are kept, and the row is walked as above.
+//                                  into finds the bin. Where what lies above the border's bin and in it is RANKED at most, it
+//                                  is listed and finished in the same way. Otherwise the bin alone goes to a list (LIST at most)
+//                                  that the first CTA sorts, which gives the border's value and how many of its equals are kept,
+//                                  and the row is walked as above.
 //   more than that in one bin      (thousands of equal logits, or nearly) bisection on the values' bits.
 //
 // Weights: with P = 32 log2(e) (max - l) / t, n a whole number near it and below, f the rest, w = 2^(-n / 32) 2^(-f / 32): the
-// first factor from a table of all n, the second from five terms of its series. P is held in two floats: w is within 2^-29 of
-// itself (and 2^-44 of the largest), sums of thousands of them within far less. u of 24 bits falls so near a border of two tokens
-// that it matters about once in a million rows of 10^5 nearly equal tokens.
+// first factor from a table of all n, the second from five terms of its series. P is held in two floats: w is within 2^-28 of
+// itself (the roundings of f ln(2) / 32, of its series and their product, by an emulation 2^-28.07 at worst) and 2^-44 of the
+// largest, sums of thousands of them within far less. u of 24 bits falls so near a border of two tokens that it matters about
+// once in a million rows of 10^5 nearly equal tokens.
 //
-// Rows of 131072 fp32: one 9 us (all kept), 7.2 (top_k), 22 (top_p); 64 of them 31, 41, 63, and 50 with settings of each kind. 512
-// rows of 32000, all kept: 54 us; reading them takes 10. What bounds it is a CTA's chain (begin, loads, maximum through the cluster,
-// weights, sums through the cluster, the walk) with two CTAs an SM to overlap: without the weights those rows take 39 us, and a
-// barrier of the cluster is 1000 to 1400 clocks. Then issue slots: 58 instructions for 32 logits a pass (41% of them used).
+// Rows of 131072 fp32: one 8.7 us (all kept), 7.6 (top_k), 20.5 (top_p); 64 of them 31.7, 41, 65, 51 with settings of each kind,
+// 14 greedy. 512 rows of 32000, all kept: 54 us; reading them takes 10. What bounds it is a CTA's chain (begin, loads, maximum
+// through the cluster, weights, sums through the cluster, the walk) with two CTAs an SM to overlap: without the weights those
+// rows take 39 us, and a barrier of the cluster is 1000 to 1400 clocks. Then issue slots: 58 instructions for 32 logits a pass
+// (41% of them used).
 // Tried: weights from a table made for the row, fewer fp32 operations but as many instructions (53 us; top_p 65), a cluster that
 // is through takes over a waiting one (clusterlaunchcontrol: 63 against 54; the loop around a row costs registers).
 #include <math.h>
