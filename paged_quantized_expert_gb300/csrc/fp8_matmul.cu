@@ -40,17 +40,24 @@ bool map_codes(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, u
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
-bool map_out(CUtensorMap *m, const Args &a) {
+bool map_out(CUtensorMap *m, const Args &a, int cols) {
     const int size = a.fp32 ? 4 : 2;
-    return encode(m, a.fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, (uint64_t)a.M, (uint64_t)a.N,
+    return encode(m, a.fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, (uint64_t)a.M, (uint64_t)cols,
                   (uint64_t)a.out_stride * size, 32, 64 / size, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
 static std::atomic<int> g_kernel{0};      // pqe_test_set_matmul_kernel: tile << 16 | split, one word, so that no call sees parts of two
 static std::atomic<int64_t> g_expiry{0};  // pqe_test_set_matmul_expiry: who << 32 | block
 
-// whether out can leave by TMA
-bool out_aligned(const Args &a) { return aligned(a.out, 16) && a.out_stride * (a.fp32 ? 4 : 2) % 16 == 0; }
+// whether out's rows lie as TMA needs them
+static bool out_aligned(const Args &a) { return aligned(a.out, 16) && a.out_stride * (a.fp32 ? 4 : 2) % 16 == 0; }
+
+// A store of a box that ends inside 16 bytes writes all of them, over what lies behind the row: where rows end so, only the boxes
+// that lie wholly in them leave by TMA.
+int tma_columns(const Args &a) {
+    const int size = a.fp32 ? 4 : 2;
+    return !out_aligned(a) ? 0 : (int64_t)a.N * size % 16 == 0 ? a.N : a.N / (64 / size) * (64 / size);
+}
 
 // Which kernel takes a call: the least of estimates in us, from measurements on one GB300 (K = 2048, bf16 out unless said).
 //   few, 16 or 32 tokens a tile: 2.2 (2.3) to begin and end, 0.23 (0.29) a block of K and round of tiles; where SMs are left 2 to

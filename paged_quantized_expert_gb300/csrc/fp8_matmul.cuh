@@ -46,9 +46,10 @@ int matmul_many(const Call &c, int cols, int ctas, int sms, cudaStream_t s);
 
 // tensor map over bytes [rows, cols], rows `stride` apart, box [box_rows, 128], 128-byte swizzle; zeros outside
 bool map_codes(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint64_t stride, uint32_t box_rows);
-bool out_aligned(const Args &a);
-// tensor map over the result, box of 32 rows of 64 bytes, 64-byte swizzle
-bool map_out(CUtensorMap *m, const Args &a);
+// columns of the result, from the first on, that leave by TMA
+int tma_columns(const Args &a);
+// tensor map over the first `cols` columns of the result, box of 32 rows of 64 bytes, 64-byte swizzle
+bool map_out(CUtensorMap *m, const Args &a, int cols);
 
 // launch_pdl in clusters of `cluster` CTAs
 template <typename... KArgs>

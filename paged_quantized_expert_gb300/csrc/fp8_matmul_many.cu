@@ -8,7 +8,7 @@
 //
 // Persistent: a pair (or SM) takes every pairs-th tile. Warp 0 issues TMA, warp 1 the MMAs, warps 2 and 3 bring the scales to
 // shared memory, warps 4-11 scale and add. Finished rows go through shared memory and leave as TMA stores (which cut what lies
-// outside), or, where out is not aligned to 16 bytes, element by element.
+// outside), or, where out is not aligned to 16 bytes or a row ends inside 16, element by element (the latter's last 64 bytes).
 //
 // In a replayed graph: 16384 x 4096 x 2560 120 us, 2.9 PFLOP/s (as calls in a row, where power lowers the clock, 135); 4099 x
 // 3584 x 2048 30; 64 x 131072 x 2048 to fp32 52 (128 x 128 tiles, 5.8 TB/s of weights and results). What bounds the first: a
@@ -79,7 +79,7 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
 template <int BN, int CTAS, bool FP32>
 __global__ void __launch_bounds__(MANY_THREADS, 1)
     matmul_many_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-                       const __grid_constant__ CUtensorMap tmOut, const Args a, int n_tiles, int items, int tma_out) {
+                       const __grid_constant__ CUtensorMap tmOut, const Args a, int n_tiles, int items, int tma_cols) {
     using L = Many<BN, CTAS>;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint32_t sbase;  // in a register: as a constant it is put together anew for every descriptor (126 us against 122)
@@ -289,24 +289,25 @@ __global__ void __launch_bounds__(MANY_THREADS, 1)
                         *reinterpret_cast<uint4 *>(mine + 16 * (v ^ ((lane >> 1) & 3))) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
-                if (tma_out) {
+                if (tma_cols) {
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0 && row0 < a.M) {
 #pragma unroll
                         for (int j = 0; j < N; ++j)
-                            if (col0 + (p0 + j) * PER < a.N)
+                            if (col0 + (p0 + j) * PER < tma_cols)
                                 asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
                                                  reinterpret_cast<uint64_t>(&tmOut)),
                                              "r"(col0 + (p0 + j) * PER), "r"(row0), "r"(smem_u32(buf + j * L::BUF))
                                              : "memory");
                         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     }
-                } else {
+                }
+                if (tma_cols < a.N) {
                     __syncwarp();
                     constexpr int SIZE = FP32 ? 4 : 2;
                     const int c = lane % PER;
-                    for (int j = 0; j < N; ++j)
+                    for (int j = max(0, (tma_cols - col0) / PER - p0); j < N; ++j)
                         for (int r = lane / PER; r < 32; r += 32 / PER) {
                             const int col = col0 + (p0 + j) * PER + c, row = row0 + r;
                             if (row >= a.M || col >= a.N) continue;
@@ -364,16 +365,16 @@ static int launch(const Call &c, int sms, cudaStream_t s) {
         PQE_CUDA_TRY(cudaFuncSetAttribute(matmul_many_kernel<BN, CTAS, FP32>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM));
         attr_set[dev].store(1, std::memory_order_relaxed);
     }
-    const int tma_out = out_aligned(c.a);
+    const int tma_cols = tma_columns(c.a);
     CUtensorMap mx, mw, mo = {};
     if (!map_codes(&mx, c.x, (uint64_t)c.a.M, (uint64_t)c.K, (uint64_t)c.x_stride, 128) ||
-        !map_codes(&mw, c.w, (uint64_t)c.a.N, (uint64_t)c.K, (uint64_t)c.K, L::B_ROWS) || (tma_out && !map_out(&mo, c.a)))
+        !map_codes(&mw, c.w, (uint64_t)c.a.N, (uint64_t)c.K, (uint64_t)c.K, L::B_ROWS) || (tma_cols && !map_out(&mo, c.a, tma_cols)))
         return PQE_ERR_UNSUPPORTED;
     const int n_tiles = (c.a.N + BN - 1) / BN;
     const int64_t items = (int64_t)n_tiles * (((int64_t)c.a.M + 128 * CTAS - 1) / (128 * CTAS)), most = sms / CTAS;
     if (items > INT32_MAX / 8) return PQE_ERR_INVALID_ARG;
     return launch_clusters(matmul_many_kernel<BN, CTAS, FP32>, CTAS * (unsigned)(items < most ? items : most), MANY_THREADS, L::SMEM, CTAS, s, mx, mw, mo,
-                           c.a, n_tiles, (int)items, tma_out);
+                           c.a, n_tiles, (int)items, tma_cols);
 }
 
 int matmul_many(const Call &c, int cols, int ctas, int sms, cudaStream_t s) {
